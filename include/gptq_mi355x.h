@@ -301,6 +301,146 @@ gptq_status gptq_pack(const uint8_t* codes, const float* scales, const int32_t* 
                       int32_t bits, int32_t group_size, int32_t checkpoint_format, int32_t scales_dtype,
                       int32_t* qweight, int32_t* qzeros, void* scales_out, void* stream);
 
+/* ---- Serving operators next to the quantized projections -----------------------------------------
+ * One decoder layer of a served model around the projections above: low-rank adapters of many
+ * requests beside a shared projection, appending rotated keys and values to a paged cache held in
+ * 8 bits, and attention over that cache.  Conventions as for the calls above: device pointers,
+ * caller-owned buffers and workspaces, checks before any device work, work queued on `stream` only
+ * (no allocation, no synchronisation: every call below can be captured in a HIP graph).
+ *
+ * What lives in device memory (page tables, lengths, adapter ids) cannot be checked by the host
+ * without a synchronisation, so the kernels check it where they use it: an entry outside its range
+ * is treated as absent, as stated at each call, and never addresses memory. */
+
+/* A paged cache of one layer.  A page holds page_size consecutive tokens of one sequence; for each
+ * page and head its codes are int8 in [-127, 127] with one float32 scale: value = code * scale. */
+typedef struct {
+  int8_t* k_codes;     /* [num_pages, kv_heads, page_size, head_dim], 16-byte aligned          */
+  int8_t* v_codes;     /* the same shape                                                       */
+  float* k_scale;      /* [num_pages, kv_heads], 4-byte aligned                                */
+  float* v_scale;      /* the same shape                                                       */
+  int64_t num_pages;   /* 1 .. 2^31 - 1                                                        */
+  int32_t kv_heads;    /* 1 .. 1024                                                            */
+  int32_t page_size;   /* 16, 32, 64, 128 or 256 tokens                                        */
+  int32_t head_dim;    /* 64 or 128                                                            */
+  int32_t reserved;    /* must be 0                                                            */
+} gptq_kv_cache;
+
+/* A batch of sequences of different lengths, their tokens packed one sequence after the other.
+ * Token i of sequence b is row cu[b] + i of the packed tensors.  Rows outside [0, rows), pages
+ * outside the table's width and page ids outside [0, num_pages) are absent: nothing is read or
+ * written for them. */
+typedef struct {
+  const int32_t* page_table; /* [batch, table_width]: page of tokens [j * page_size, ...)      */
+  const int32_t* at;         /* [batch]: see each call                                         */
+  const int32_t* cu;         /* [batch + 1], ascending from 0                                  */
+  int64_t rows;              /* cu[batch]: rows of the packed tensors, 0 .. 2^24               */
+  int32_t batch;             /* 0 .. 2^20 sequences                                            */
+  int32_t table_width;       /* 1 .. 2^22 pages                                                */
+  int32_t max_rows;          /* at least the rows of every sequence: 0 .. rows.  Rows beyond it
+                                are absent                                                     */
+  int32_t reserved;          /* must be 0                                                      */
+} gptq_kv_batch;
+
+/* Rotation of the pairs (a, b) of a head's first `dim` values by the angle of its position:
+ * (a cos - b sin, b cos + a sin), in float32.  Pairs are (i, i + dim / 2), or (2 i, 2 i + 1) when
+ * interleaved.  Positions past the tables' last row use that row (the caller sizes the tables). */
+typedef struct {
+  const float* cos;      /* [rows, dim / 2] contiguous, 16-byte aligned                        */
+  const float* sin;      /* the same shape                                                     */
+  int32_t rows;          /* 1 .. 2^24                                                          */
+  int32_t dim;           /* a multiple of 16, up to head_dim                                   */
+  int32_t interleaved;   /* 0 or 1                                                             */
+  int32_t reserved;      /* must be 0                                                          */
+} gptq_rope;
+
+/* Appends the batch's new keys and values to the cache; batch->at[b] is the number of tokens that
+ * sequence b has in the cache before the call, so its row i becomes token at[b] + i.
+ *   k, v   [rows, kv_heads, head_dim] of `dtype` (F16 or BF16), rows k_stride / v_stride elements
+ *          apart (multiples of 8), 16-byte aligned; k is rotated at its position when rope is given.
+ *   q      [rows, q_heads, head_dim], rows q_stride apart, or NULL: rotated the same way into q_out
+ *          (rows q_out_stride apart), rounded once to `dtype`.  q_out may be q with the same
+ *          stride, and must not overlap anything else.  NULL q needs no rope.
+ *   rope   NULL: nothing is rotated.
+ * For each page and head that gets tokens, over the page's rotated new values x in float32:
+ *   had  = the page's scale when it holds older tokens of the sequence, else 0
+ *   unit = max(had, max |x| / 127), the page's new scale
+ *   older codes become rint(code * (had / unit)) when unit > had; new codes are
+ *   rint(x / unit) within [-127, 127] (0 when unit is 0).
+ * A page filled in one call is therefore rounded once; one filled token by token is rounded again
+ * only when a token exceeds everything before it.  Codes past the newest token are left alone.
+ * Infinities take no part in the maximum and become +-127; NaN becomes 0.
+ * Two sequences must not append to the same page in one call.
+ * Errors: GPTQ_E_INVALID_ARG (NULL, alignment, strides, dtype, reserved, overlap), GPTQ_E_SHAPE
+ * (sizes out of range), GPTQ_E_UNSUPPORTED (page_size, head_dim, rope dim), GPTQ_E_DEVICE (the
+ * current device is not gfx950), GPTQ_E_HIP.  rows == 0 or batch == 0: GPTQ_OK, nothing launched. */
+gptq_status gptq_kv_append(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const void* q, int64_t q_stride, int32_t q_heads,
+                           void* q_out, int64_t q_out_stride, int32_t dtype, const gptq_rope* rope, void* stream);
+
+/* Reads cached tokens back as values: row i of sequence b of k_out and v_out (either may be NULL)
+ * [rows, kv_heads, head_dim], contiguous, `dtype` F16, BF16 or F32, 16-byte aligned, is token
+ * batch->at[b] + i: the float32 product code * scale, rounded to `dtype`.  Absent tokens read as 0.
+ * Errors as for gptq_kv_append. */
+gptq_status gptq_kv_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch, void* k_out, void* v_out, int32_t dtype,
+                         void* stream);
+
+/* Shape of an attention call over the cache. */
+typedef struct {
+  int32_t q_heads;   /* a multiple of kv_heads, up to 64 a kv head: query head h reads kv head
+                        h / (q_heads / kv_heads)                                               */
+  int32_t dtype;     /* F16 or BF16, of q and out                                              */
+  float scale;       /* of the scores, finite                                                  */
+  int32_t causal;    /* 1: a query sees tokens up to its own; 0: all of its sequence's         */
+  int32_t window;    /* > 0: only tokens less than `window` before its own; 0: no window       */
+  int32_t max_kv;    /* at least every at[b] (clipped by the table's width): sizes the split   */
+  int64_t q_stride;  /* elements between rows of q, a multiple of 8                            */
+  int64_t out_stride;
+} gptq_attention;
+
+/* out = softmax(scale * q k^T) v of every query over its sequence's cached tokens, with
+ * k, v = code * scale of the page and head.  batch->at[b] is the number of tokens of sequence b in
+ * the cache, the queries' own included: its row i stands at position at[b] - n + i of n rows.
+ *   q, out  [rows, q_heads, head_dim] of the call's dtype, 16-byte aligned; out must not overlap q
+ *           or the workspace.
+ * A query that sees no token (a negative position, absent pages) gives zeros.  Scores, the running
+ * maximum and sum and the output are held in float32; matrix operands are float16 (codes exactly,
+ * q scaled by a power of two of its row, probabilities scaled so that they keep their bits), and
+ * out is rounded once.  A call with the same arguments gives the same bits.
+ * workspace: gptq_kv_attention_workspace_size() bytes (0 when the keys are not split), 256-byte
+ * aligned.  Errors: as for gptq_kv_append, and GPTQ_E_WORKSPACE. */
+gptq_status gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const gptq_kv_batch* batch,
+                                             const gptq_attention* call, size_t* bytes);
+gptq_status gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const gptq_attention* call,
+                              const void* q, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Low-rank adapters of one projection: adapter i adds scale[i] * B_i (A_i x) to its rows. */
+typedef struct {
+  const void* a;        /* [adapters, rank, in_features] of dtype, contiguous, 16-byte aligned   */
+  const void* b;        /* [adapters, out_features, rank] of dtype, contiguous, 16-byte aligned  */
+  const float* scale;   /* [adapters]                                                            */
+  int32_t adapters;     /* 1 .. 65536                                                            */
+  int32_t rank;         /* a multiple of 8 up to 128; adapters of a smaller rank are zero-padded */
+  int32_t in_features;  /* K, a multiple of 32 up to 2^20                                        */
+  int32_t out_features; /* N, a multiple of 32 up to 2^20                                        */
+  int32_t dtype;        /* F16 or BF16, also of x, y and out                                     */
+  int32_t reserved;     /* must be 0                                                             */
+} gptq_lora_bank;
+
+/* out[m] = y[m] + scale[i] * B_i (A_i x[m]) with i = ids[m]: y is the shared projection's output
+ * (gptq_gemm), x its input.  Rows whose id is outside [0, adapters) keep y (-1: no adapter).  The
+ * rows' adapters may come in any order; rows of one adapter next to each other share its reads.
+ *   x [M, K], y and out [M, N], row-major, 16-byte aligned; out may be y, and must not otherwise
+ *   overlap anything.  ids int32 [M].
+ * Both products accumulate in float32; A_i x[m] is kept to 16 bits or more for the second, and out
+ * is rounded once.  A call with the same arguments gives the same bits.
+ * workspace: gptq_lora_workspace_size() bytes, 256-byte aligned.  M == 0: GPTQ_OK, nothing launched.
+ * Errors: GPTQ_E_INVALID_ARG, GPTQ_E_SHAPE (K or N, adapters, M > 2^24), GPTQ_E_UNSUPPORTED (rank),
+ * GPTQ_E_WORKSPACE, GPTQ_E_DEVICE, GPTQ_E_HIP. */
+gptq_status gptq_lora_workspace_size(const gptq_lora_bank* bank, int64_t M, size_t* bytes);
+gptq_status gptq_lora_add(const gptq_lora_bank* bank, const void* x, const void* y, const int32_t* ids, int64_t M,
+                          void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

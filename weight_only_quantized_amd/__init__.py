@@ -7,6 +7,10 @@ There is no CPU or PyTorch fallback.
 
     h = repack(qweight, qzeros, scales, g_idx, bits=4, group_size=128)
     y = h.gemm(x)          # x [M, K] fp16/bf16 on the GPU -> y [M, N], same dtype
+
+Next to the projections of a served decoder layer (serving.py): LoraBank (low-rank adapters of many
+requests beside a projection) and KVCache (a paged cache in 8 bits: append with rotation, attention,
+read back).
 """
 from __future__ import annotations
 
@@ -14,7 +18,7 @@ import ctypes
 import os
 
 __all__ = ["LIB_PATH", "GPTQError", "Desc", "Handle", "load_library", "repack", "validate", "symbols",
-           "STATUS", "PATH_AUTO", "PATH_SKINNY", "PATH_TILED"]
+           "STATUS", "PATH_AUTO", "PATH_SKINNY", "PATH_TILED", "KVCache", "LoraBank"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq_mi355x.so")
 
@@ -29,7 +33,9 @@ PATH_AUTO, PATH_SKINNY, PATH_TILED = 0, 1, 2
 symbols = ["gptq_validate", "gptq_repack", "gptq_workspace_size", "gptq_gemm", "gptq_gemm_bias", "gptq_gemm_noalloc",
            "gptq_destroy",
            "gptq_info", "gptq_decode_runtime", "gptq_status_str", "gptq_last_hip_error", "gptq_hessian",
-           "gptq_quantize_workspace_size", "gptq_quantize", "gptq_pack", "gptq_read_floor"]
+           "gptq_quantize_workspace_size", "gptq_quantize", "gptq_pack", "gptq_read_floor",
+           "gptq_kv_append", "gptq_kv_read", "gptq_kv_attention_workspace_size", "gptq_kv_attention",
+           "gptq_lora_workspace_size", "gptq_lora_add"]
 
 
 class GPTQError(RuntimeError):
@@ -97,10 +103,18 @@ def load_library(path: str = LIB_PATH):
     lib.gptq_quantize.argtypes = [P, P, I32, I32, ctypes.POINTER(QuantParams), P, P, P, P, P, SZ, P]
     lib.gptq_pack.argtypes = [P, P, P, I32, I32, I32, I32, I32, I32, P, P, P, P]
     lib.gptq_read_floor.argtypes = [P, SZ, P, P]
+    lib.gptq_kv_append.argtypes = [P, P, P, I64, P, I64, P, I64, I32, P, I64, I32, P, P]
+    lib.gptq_kv_read.argtypes = [P, P, P, P, I32, P]
+    lib.gptq_kv_attention_workspace_size.argtypes = [P, P, P, ctypes.POINTER(SZ)]
+    lib.gptq_kv_attention.argtypes = [P, P, P, P, P, P, SZ, P]
+    lib.gptq_lora_workspace_size.argtypes = [P, I64, ctypes.POINTER(SZ)]
+    lib.gptq_lora_add.argtypes = [P, P, P, P, I64, P, P, SZ, P]
     for f in ("gptq_validate", "gptq_repack", "gptq_workspace_size", "gptq_gemm", "gptq_gemm_bias", "gptq_gemm_noalloc",
               "gptq_destroy",
               "gptq_info", "gptq_decode_runtime", "gptq_last_hip_error", "gptq_hessian",
-              "gptq_quantize_workspace_size", "gptq_quantize", "gptq_pack", "gptq_read_floor"):
+              "gptq_quantize_workspace_size", "gptq_quantize", "gptq_pack", "gptq_read_floor",
+              "gptq_kv_append", "gptq_kv_read", "gptq_kv_attention_workspace_size", "gptq_kv_attention",
+              "gptq_lora_workspace_size", "gptq_lora_add"):
         getattr(lib, f).restype = I32
     _lib = lib
     return lib
@@ -377,3 +391,11 @@ def pack(codes, scales, zeros, *, bits, group_size, checkpoint_format="gptq_v2",
     if st:
         raise GPTQError(st, "gptq_pack", lib)
     return qweight, qzeros, s_out
+
+
+def __getattr__(name):
+    # the serving classes need torch at import time; the package itself does not
+    if name in ("KVCache", "LoraBank"):
+        from . import serving
+        return getattr(serving, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

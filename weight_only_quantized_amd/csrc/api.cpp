@@ -19,6 +19,7 @@
 
 #include "bank_spread.h"
 #include "internal.h"
+#include "serving.h"
 
 namespace gq {
 
@@ -38,7 +39,7 @@ static int seg_steps_of(int gs_eff, int gs) {
   return (gs_eff / 32) % 4 == 0 ? 4 : 1;
 }
 
-static bool is_gfx950_device(int dev) {
+bool is_gfx950_device(int dev) {
   static std::mutex mu;
   static int cache[64];
   static bool init = false;
