@@ -393,7 +393,8 @@ typedef struct {
   float scale;       /* of the scores, finite                                                  */
   int32_t causal;    /* 1: a query sees tokens up to its own; 0: all of its sequence's         */
   int32_t window;    /* > 0: only tokens less than `window` before its own; 0: no window       */
-  int32_t max_kv;    /* at least every at[b] (clipped by the table's width): sizes the split   */
+  int32_t max_kv;    /* at least every at[b]: sizes the split of the keys.  Tokens past it
+                        are absent                                                             */
   int64_t q_stride;  /* elements between rows of q, a multiple of 8                            */
   int64_t out_stride;
 } gptq_attention;

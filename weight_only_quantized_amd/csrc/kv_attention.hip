@@ -92,9 +92,16 @@ __global__ void __launch_bounds__(kThreads) kv_attention_row_kernel(KvAttentionC
 
 }  // namespace
 
-size_t kv_attention_ws_bytes(const gptq_kv_cache&, const gptq_kv_batch&, const gptq_attention&) { return 0; }
+static bool few_rows(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  return (int64_t)b.max_rows * (a.q_heads / c.kv_heads) <= 64;
+}
+
+size_t kv_attention_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  return few_rows(c, b, a) ? kv_decode_ws_bytes(c, b, a) : 0;
+}
 
 hipError_t launch_kv_attention(const KvAttentionCall& a, hipStream_t s) {
+  if (few_rows(a.c, a.b, a.a)) return launch_kv_decode(a, s);
   const int page_shift = __builtin_ctz(a.c.page_size);
   const int64_t blocks = a.b.rows * a.a.q_heads;
   if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;

@@ -1,0 +1,147 @@
+// Device helpers of attention over the paged 8-bit cache.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "serving.h"
+#include "serving_dev.h"
+
+namespace gq {
+
+// A column's weights are powers of two relative to a top that moves only when one would pass
+// 2^kGrow; it then moves to kAbove below the largest.  Both keep weights inside float16's normal
+// range (2^-14 .. 2^16) down to 2^-20 of the largest.
+constexpr float kGrow = 14.0f, kAbove = 6.0f;
+constexpr float kNoTop = -1e30f;          // finite, so that hidden tokens (-inf) never meet -inf
+constexpr float kLog2e = 1.44269504088896f;
+
+// Rows of a sequence in a batch; a sequence whose rows leave the packed tensors has none.
+struct SeqRows {
+  int64_t row0;
+  int rows;          // handled: at most max_rows
+  int64_t length;    // tokens in the cache
+  int64_t before;    // position of row 0
+};
+__device__ __forceinline__ SeqRows sequence_rows(const gptq_kv_batch& b, int seq) {
+  const int64_t r0 = b.cu[seq], r1 = b.cu[seq + 1], n = r1 - r0, length = b.at[seq];
+  const bool good = n > 0 && r0 >= 0 && r1 <= b.rows;
+  return SeqRows{r0, good ? (int)(n < b.max_rows ? n : b.max_rows) : 0, length, length - n};
+}
+
+// Tokens past the table's width or the stated largest length are absent.
+__device__ __forceinline__ int64_t key_room(const gptq_kv_batch& b, const gptq_attention& a, int page_shift) {
+  const int64_t room = (int64_t)b.table_width << page_shift;
+  return a.max_kv < room ? a.max_kv : room;
+}
+
+// Tokens [begin, end) that row `row` sees; begin <= end.
+struct KeyRange {
+  int64_t begin, end;
+};
+__device__ __forceinline__ KeyRange key_range(const SeqRows& s, int row, const gptq_attention& a, int64_t room) {
+  const int64_t at = s.before + row;
+  int64_t end = s.length < room ? s.length : room;
+  if (a.causal && at + 1 < end) end = at + 1;
+  if (end < 0) end = 0;
+  int64_t begin = a.window > 0 ? at - a.window + 1 : 0;
+  if (begin < 0) begin = 0;
+  if (begin > end) begin = end;
+  return KeyRange{begin, end};
+}
+
+// A tile of 16 tokens of one kv head, one a lane: where its codes start, the key scale, and the value
+// scale as log2 and inverse.  An absent tile reads page 0 with a key scale of 0 and a log of -inf:
+// its weights are 0.  Value scales below 2^-64 count as 2^-64 (an all-zero page has scale 0).
+struct PageTile {
+  uint64_t base;
+  float k_scale, v_log, v_inv;
+};
+__device__ __forceinline__ PageTile page_tile(const gptq_kv_cache& c, const gptq_kv_batch& b, int seq, int kv_head,
+                                              int64_t pos, bool wanted, int page_shift) {
+  PageTile t{0, 0.0f, -__builtin_inff(), 0.0f};
+  const int64_t j = pos >> page_shift;
+  if (!wanted || pos < 0 || j >= b.table_width) return t;
+  const int page = b.page_table[(int64_t)seq * b.table_width + j];
+  if (page < 0 || page >= c.num_pages) return t;
+  const int64_t unit = (int64_t)page * c.kv_heads + kv_head;
+  t.base = (uint64_t)((unit << page_shift) + (pos & ((1 << page_shift) - 1))) * c.head_dim;
+  const float vs = __builtin_fmaxf(c.v_scale[unit], 0x1p-64f);
+  t.k_scale = c.k_scale[unit];
+  t.v_log = __builtin_amdgcn_logf(vs);
+  t.v_inv = __builtin_amdgcn_exp2f(-t.v_log);     // of the log, so that both cancel
+  return t;
+}
+
+__device__ __forceinline__ float lane_f32(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// Codes to float16, exactly: byte b becomes 0x64'(b ^ 0x80) = 1024 + (code + 128), minus 1152.
+__device__ __forceinline__ uint32_t less_1152(uint32_t w) {
+  const f16x2 v = __builtin_bit_cast(f16x2, w) + f16x2{(_Float16)-1152.0f, (_Float16)-1152.0f};
+  return __builtin_bit_cast(uint32_t, v);
+}
+// eight codes next to each other
+__device__ __forceinline__ u32x4 codes_f16(uint32_t a, uint32_t b) {
+  a ^= 0x80808080u;
+  b ^= 0x80808080u;
+  return u32x4{less_1152(__builtin_amdgcn_perm(0x64646464u, a, 0x04010400u)),
+               less_1152(__builtin_amdgcn_perm(0x64646464u, a, 0x04030402u)),
+               less_1152(__builtin_amdgcn_perm(0x64646464u, b, 0x04010400u)),
+               less_1152(__builtin_amdgcn_perm(0x64646464u, b, 0x04030402u))};
+}
+// byte `byte` (0 .. 3) of two words: the codes of two tokens
+__device__ __forceinline__ uint32_t pair_f16(uint32_t first, uint32_t second, int byte) {
+  const uint32_t sel = 0x0c000c00u | (uint32_t)(4 + byte) << 16 | (uint32_t)byte;
+  return less_1152(__builtin_amdgcn_perm(second, first, sel) ^ 0x64806480u);
+}
+
+// A query row's float16 operands, N of eight values at at[offset(i)], from lanes that together hold
+// the row (xor `mask0`, `mask1` reach the others); returns the power of two that was taken out.
+// float16 rows are exact as they are; bfloat16 rows are scaled so that the largest magnitude is in
+// [2^14, 2^15), where float16 holds their 8 bits exactly down to 2^-29 of it.
+template <int BF16, int N, typename Offset>
+__device__ __forceinline__ float load_query(const uint16_t* at, Offset offset, f16x8* q, int mask0, int mask1) {
+  u32x4 w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = *(const u32x4*)(at + offset(i));
+  if constexpr (!BF16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = __builtin_bit_cast(f16x8, w[i]);
+    return 1.0f;
+  } else {
+    uint32_t most = 0;                        // magnitudes compare as integers
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = w[i][e] << 16 & 0x7fff0000u, hi = w[i][e] & 0x7fff0000u;
+        most = most > lo ? most : lo;
+        most = most > hi ? most : hi;
+      }
+    uint32_t other = __shfl_xor((int)most, mask0);
+    most = most > other ? most : other;
+    if (mask1) {
+      other = __shfl_xor((int)most, mask1);
+      most = most > other ? most : other;
+    }
+    int e = (int)(most >> 23) - 127;          // -127: zero or subnormal, 128: not finite
+    e = e < -112 ? -112 : e;
+    const float down = __builtin_ldexpf(1.0f, 14 - e);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        q[i][2 * k] = (_Float16)(__builtin_bit_cast(float, w[i][k] << 16) * down);
+        q[i][2 * k + 1] = (_Float16)(__builtin_bit_cast(float, w[i][k] & 0xffff0000u) * down);
+      }
+    return __builtin_ldexpf(1.0f, e - 14);
+  }
+}
+
+}  // namespace gq

@@ -35,6 +35,9 @@ struct KvAttentionCall {
 };
 size_t kv_attention_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
 hipError_t launch_kv_attention(const KvAttentionCall& a, hipStream_t s);
+// Few rows a sequence (kv_decode.hip): split over the keys, joined by a second launch.
+size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
+hipError_t launch_kv_decode(const KvAttentionCall& a, hipStream_t s);
 
 struct LoraCall {
   gptq_lora_bank bank;
