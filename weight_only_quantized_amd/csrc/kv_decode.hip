@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
   constexpr int kPitch = DIM + 4;   // of a column's sums in LDS and memory
   __shared__ __align__(16) float sums[kWaves][16][kPitch];
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col16 = lane & 15, quad = lane >> 4;
   int id = blockIdx.x;
   const int kv_head = id % a.c.kv_heads;
@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
   // the wave's tiles, one a lane
   const int steps = run1 > run0 ? (int)((run1 - run0 + kStride - 1) / kStride) : 0;
   const int64_t my_pos = run0 + ((lane >> 1) * kWaves + wave) * kStep + (lane & 1) * 16;
-  const PageTile mine = page_tile(a.c, a.b, seq, kv_head, my_pos, my_pos < run1, page_shift);
+  const TilePage mine = tile_page(a.c, a.b, seq, kv_head, my_pos, my_pos < run1, page_shift);
+  const float my_log = scale_log(mine.v_scale), my_inv = scale_inv(my_log);
 
   // this lane's columns: visible tokens and the query (columns past the last repeat it)
   int begin[CT], end[CT];
@@ -128,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
   auto load = [&](Step& d, int i) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint64_t base = lane_u64(mine.base, 2 * i + t);
+      const uint64_t base = tile_base(a.c, __builtin_amdgcn_readlane(mine.page, 2 * i + t), kv_head,
+                                      (int)run0 + (i * kWaves + wave) * kStep + t * 16, page_shift);
       const int8_t *kb = a.c.k_codes + base, *vb = a.c.v_codes + base;
 #pragma unroll
       for (int j = 0; j < KL; ++j) d.k[t][j] = *(const u32x4*)(kb + k_off + j * 64);
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
         }
       }
       ks[t] = lane_f32(mine.k_scale, 2 * i + t);
-      lv[t] = lane_f32(mine.v_log, 2 * i + t);
+      lv[t] = lane_f32(my_log, 2 * i + t);
     }
     const bool edge = pos < inner_lo || pos + kStep > inner_hi;     // some column does not see the whole step
     float x[2][4];
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const float rv = lane_f32(mine.v_inv, 2 * i + t);
+        const float rv = lane_f32(my_inv, 2 * i + t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float p = __builtin_amdgcn_exp2f(x[t][e]);

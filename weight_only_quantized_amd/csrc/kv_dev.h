@@ -49,38 +49,41 @@ __device__ __forceinline__ KeyRange key_range(const SeqRows& s, int row, const g
   return KeyRange{begin, end};
 }
 
-// A tile of 16 tokens of one kv head, one a lane: where its codes start, the key scale, and the value
-// scale as log2 and inverse.  An absent tile reads page 0 with a key scale of 0 and a log of -inf:
-// its weights are 0.  Value scales below 2^-64 count as 2^-64 (an all-zero page has scale 0).
-struct PageTile {
-  uint64_t base;
-  float k_scale, v_log, v_inv;
+// The page of a tile of 16 tokens, one a lane, and its scales for one kv head.  An absent tile has
+// page -1 and scales 0: its weights are 0.  Value scales below 2^-64 count as 2^-64 (an all-zero page
+// has scale 0).
+struct TilePage {
+  int page;
+  float k_scale, v_scale;
 };
-__device__ __forceinline__ PageTile page_tile(const gptq_kv_cache& c, const gptq_kv_batch& b, int seq, int kv_head,
+__device__ __forceinline__ TilePage tile_page(const gptq_kv_cache& c, const gptq_kv_batch& b, int seq, int kv_head,
                                               int64_t pos, bool wanted, int page_shift) {
-  PageTile t{0, 0.0f, -__builtin_inff(), 0.0f};
+  TilePage t{-1, 0.0f, 0.0f};
   const int64_t j = pos >> page_shift;
   if (!wanted || pos < 0 || j >= b.table_width) return t;
   const int page = b.page_table[(int64_t)seq * b.table_width + j];
   if (page < 0 || page >= c.num_pages) return t;
   const int64_t unit = (int64_t)page * c.kv_heads + kv_head;
-  t.base = (uint64_t)((unit << page_shift) + (pos & ((1 << page_shift) - 1))) * c.head_dim;
-  const float vs = __builtin_fmaxf(c.v_scale[unit], 0x1p-64f);
+  t.page = page;
   t.k_scale = c.k_scale[unit];
-  t.v_log = __builtin_amdgcn_logf(vs);
-  t.v_inv = __builtin_amdgcn_exp2f(-t.v_log);     // of the log, so that both cancel
+  t.v_scale = __builtin_fmaxf(c.v_scale[unit], 0x1p-64f);
   return t;
+}
+// Bytes before a tile's codes (page 0's for an absent tile, which is safe to read).
+__device__ __forceinline__ uint64_t tile_base(const gptq_kv_cache& c, int page, int kv_head, int pos, int page_shift) {
+  const uint64_t unit = (uint64_t)(page < 0 ? 0 : page) * (uint32_t)c.kv_heads + (uint32_t)kv_head;
+  return ((unit << page_shift) + (uint32_t)(pos & ((1 << page_shift) - 1))) * (uint32_t)c.head_dim;
+}
+// log2 of a value scale and the inverse of that power of two (so that both cancel); -inf and 0 when
+// the tile is absent.
+__device__ __forceinline__ float scale_log(float v_scale) { return __builtin_amdgcn_logf(v_scale); }
+__device__ __forceinline__ float scale_inv(float v_log) {
+  return v_log > -1e30f ? __builtin_amdgcn_exp2f(-v_log) : 0.0f;
 }
 
 __device__ __forceinline__ float lane_f32(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
-__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
-  return (uint64_t)hi << 32 | lo;
-}
-
 // Codes to float16, exactly: byte b becomes 0x64'(b ^ 0x80) = 1024 + (code + 128), minus 1152.
 __device__ __forceinline__ uint32_t less_1152(uint32_t w) {
   const f16x2 v = __builtin_bit_cast(f16x2, w) + f16x2{(_Float16)-1152.0f, (_Float16)-1152.0f};

@@ -97,6 +97,15 @@ gptq_status check_attention(const gptq_kv_cache* c, const gptq_kv_batch* b, cons
   return GPTQ_OK;
 }
 
+// Few rows a sequence: at most 64 (row, head) columns for each kv head.
+bool few_rows(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  return (int64_t)b.max_rows * (a.q_heads / c.kv_heads) <= 64;
+}
+
+size_t kv_attention_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  return few_rows(c, b, a) ? kv_decode_ws_bytes(c, b, a) : 0;
+}
+
 gptq_status check_bank(const gptq_lora_bank* k, int64_t M) {
   if (!k || k->reserved != 0 || !is_16bit(k->dtype)) return GPTQ_E_INVALID_ARG;
   if (k->rank < 8 || k->rank > 128 || k->rank % 8 != 0) return GPTQ_E_UNSUPPORTED;
@@ -207,7 +216,8 @@ gptq_status gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* b
   }
   if ((st = check_device()) != GPTQ_OK) return st;
   const KvAttentionCall a{*cache, *batch, *call, (const uint16_t*)q, (uint16_t*)out, workspace};
-  const hipError_t e = launch_kv_attention(a, (hipStream_t)stream);
+  const hipError_t e = few_rows(*cache, *batch, *call) ? launch_kv_decode(a, (hipStream_t)stream)
+                                                       : launch_kv_prefill(a, (hipStream_t)stream);
   return e == hipSuccess ? GPTQ_OK : hip_fail(e);
 }
 

@@ -33,11 +33,11 @@ struct KvAttentionCall {
   uint16_t* out;
   void* ws;
 };
-size_t kv_attention_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
-hipError_t launch_kv_attention(const KvAttentionCall& a, hipStream_t s);
 // Few rows a sequence (kv_decode.hip): split over the keys, joined by a second launch.
 size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
 hipError_t launch_kv_decode(const KvAttentionCall& a, hipStream_t s);
+// Many rows a sequence (kv_prefill.hip).
+hipError_t launch_kv_prefill(const KvAttentionCall& a, hipStream_t s);
 
 struct LoraCall {
   gptq_lora_bank bank;
