@@ -8,22 +8,51 @@ import oracle.serving_oracle as so
 import weight_only_quantized_amd as wq
 
 A = 1 << 20          # a well-aligned address: the checks only compare addresses, nothing is read
+P, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
 
-def S():
-    from weight_only_quantized_amd import serving
-    return serving
+class Cache(ctypes.Structure):
+    _fields_ = [("k_codes", P), ("v_codes", P), ("k_scale", P), ("v_scale", P), ("num_pages", I64), ("kv_heads", I32),
+                ("page_size", I32), ("head_dim", I32), ("reserved", I32)]
+
+
+class Batch(ctypes.Structure):
+    _fields_ = [("page_table", P), ("at", P), ("cu", P), ("rows", I64), ("batch", I32), ("table_width", I32),
+                ("max_rows", I32), ("reserved", I32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("cos", P), ("sin", P), ("rows", I32), ("dim", I32), ("interleaved", I32), ("reserved", I32)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("q_heads", I32), ("dtype", I32), ("scale", ctypes.c_float), ("causal", I32), ("window", I32),
+                ("max_kv", I32), ("q_stride", I64), ("out_stride", I64)]
+
+
+class Bank(ctypes.Structure):
+    _fields_ = [("a", P), ("b", P), ("scale", P), ("adapters", I32), ("rank", I32), ("in_features", I32),
+                ("out_features", I32), ("dtype", I32), ("reserved", I32)]
+
+
+def test_the_binding_packs_the_header_structures():
+    from weight_only_quantized_amd import serving as s
+    pairs = ((s._CACHE, Cache, range(1, 10)), (s._BATCH, Batch, range(1, 9)), (s._ROPE, Rope, range(1, 7)),
+             (s._ATTENTION, Attention, (1, 2, 0.5, 4, 5, 6, 7, 8)), (s._BANK, Bank, range(1, 10)))
+    for packed, structure, values in pairs:
+        assert packed.size == ctypes.sizeof(structure)
+        assert packed.pack(*values) == bytes(structure(*values)), structure
 
 
 def cache(**kw):
-    c = S()._Cache(A, A + (64 << 20), A + (128 << 20), A + (129 << 20), 8, 2, 16, 64, 0)
+    c = Cache(A, A + (64 << 20), A + (128 << 20), A + (129 << 20), 8, 2, 16, 64, 0)
     for k, v in kw.items():
         setattr(c, k, v)
     return c
 
 
 def batch(**kw):
-    b = S()._Batch(A, A, A, 4, 2, 3, 4, 0)
+    b = Batch(A, A, A, 4, 2, 3, 4, 0)
     for k, v in kw.items():
         setattr(b, k, v)
     return b
@@ -41,7 +70,7 @@ def append(c=None, b=None, k=FREE, ks=128, v=FREE + (1 << 20), vs=128, q=None, q
 
 
 def rope(**kw):
-    r = S()._Rope(A, A, 100, 64, 0, 0)
+    r = Rope(A, A, 100, 64, 0, 0)
     for k, v in kw.items():
         setattr(r, k, v)
     return r
@@ -82,7 +111,7 @@ def test_append_refusals():
 
 def attention(c=None, b=None, q=FREE, out=FREE + (1 << 20), ws=None, ws_bytes=0, **kw):
     lib = wq.load_library()
-    a = S()._Attention(4, 0, 0.125, 1, 0, 48, 256, 256)
+    a = Attention(4, 0, 0.125, 1, 0, 48, 256, 256)
     for k, v in kw.items():
         setattr(a, k, v)
     c, b = (cache() if c is None else c), (batch() if b is None else b)
@@ -100,7 +129,7 @@ def test_attention_refusals():
                      (dict(c=cache(head_dim=32)), "E_UNSUPPORTED")):
         assert attention(**kw) == want, kw
     lib, n = wq.load_library(), ctypes.c_size_t()
-    a = S()._Attention(4, 0, 0.125, 1, 0, 48, 256, 256)
+    a = Attention(4, 0, 0.125, 1, 0, 48, 256, 256)
     assert lib.gptq_kv_attention_workspace_size(ctypes.byref(cache()), ctypes.byref(batch()), ctypes.byref(a), None) == 1
     assert lib.gptq_kv_attention_workspace_size(None, ctypes.byref(batch()), ctypes.byref(a), ctypes.byref(n)) == 1
 
@@ -111,7 +140,7 @@ def test_attention_workspace_is_checked():
     lib, n = wq.load_library(), ctypes.c_size_t()
     c, b = cache(num_pages=4096), batch(rows=1, max_rows=1, batch=1, table_width=4096)
     c.v_codes, c.k_scale, c.v_scale = A + (64 << 20), A + (128 << 20), A + (129 << 20)
-    a = S()._Attention(4, 0, 0.125, 1, 0, 65536, 256, 256)
+    a = Attention(4, 0, 0.125, 1, 0, 65536, 256, 256)
     assert lib.gptq_kv_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), ctypes.byref(a), ctypes.byref(n)) == 0
     if n.value:
         ws = FREE + (64 << 20)
@@ -138,7 +167,7 @@ def test_lora_refusals():
     n = ctypes.c_size_t()
 
     def bank(**kw):
-        k = S()._Bank(A, A + (1 << 20), A + (2 << 20), 3, 16, 64, 96, 0, 0)
+        k = Bank(A, A + (1 << 20), A + (2 << 20), 3, 16, 64, 96, 0, 0)
         for f, v in kw.items():
             setattr(k, f, v)
         return k
