@@ -5,17 +5,18 @@
 //
 // What bounds it: bytes.  Single tokens of many requests read A_i and B_i of every adapter in use
 // once; prompts read x and y and write out.  Both products run on v_mfma_f32_16x16x32 with columns =
-// rows of x, straight from memory to registers: rows of A_i (or B_i) are the other operand, and the
-// inner index is permuted alike on both sides so that a lane reads 32 bytes and four lanes a whole
-// 128-byte line.
+// rows of x, straight from memory to registers: rows of A_i (or B_i) are the other operand.
 //
-// Rows in any order: a workgroup takes 16 to 64 neighbouring rows and goes through the adapters that
-// occur among them, keeping each product for its own adapter's rows (so no row meets another's
-// values, not even times zero).  With few rows the adapters of a tile go to several workgroups.
+// Rows in any order: a wave or workgroup takes 16 to 64 neighbouring rows and goes through the
+// adapters that occur among them, keeping each product for its own adapter's rows (so no row meets
+// another's values, not even times zero).  With few rows the adapters of a tile go to several
+// workgroups.
 //
-// Sums over K are split over the waves and, with few rows, over workgroups; the parts are added in
-// order by the second launch, which then takes low as two 16-bit numbers (value and remainder,
-// float16 after a power-of-two scaling of the row): 16 bits or more for one more product.
+// Sums over K are split: with few rows over the waves of a workgroup and over workgroups, whose
+// parts the second launch adds in order; with many rows over workgroups only, whose waves take
+// different rows and meet in the first-level cache over A_i, and a small launch in between adds the
+// parts once.  low goes into the second product as two 16-bit numbers (value and remainder, float16
+// after a power-of-two scaling of the row): 16 bits or more for one more product.
 #include <hip/hip_runtime.h>
 
 #include "bufmem.h"
@@ -27,12 +28,16 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = 4;
 
+constexpr int kManyRows = 32;  // rows of a wave of the first launch when there are many
+
 struct LoraPlan {
-  int low_tiles, low_rows;     // row tiles of the first launch, of 16 or 32 rows
+  bool few;                    // few rows: adapters of a tile over workgroups, low added by its readers
+  int low_tiles;               // row tiles of the first launch: of 16 (few) or 4 * kManyRows rows
   int up_tiles, up_rows;       // of the second, of 16, 32 or 64 rows
   int turns;                   // workgroups that share a tile's adapters
-  int slices, wave_k;          // parts of K, each four waves of wave_k
+  int slices, slice_k;         // parts of K
   int blocks_n, per_n;         // workgroups over N, each per_n times 256 outputs
+  size_t part_bytes;           // of the parts; then low's two numbers and the rows' powers of two
 };
 
 // Adapter of each row of a tile, one a lane (-1: none, or past the last row).
@@ -57,66 +62,72 @@ __device__ __forceinline__ void each_adapter(int id, int turn, int turns, F f) {
   }
 }
 
-// low: part[slice][row][rank] = the slice's share of A_i x.
-template <int BF16, int RT, int CT>   // rank tiles and row tiles of 16
+// acc = A_i x over inputs [k0, k1) for CT tiles of 16 rows: ranks 16 r + 4 quad + e of row 16 t + col.
+// Rows and ranks past the last, and inputs past k1, read as 0.
+template <int BF16, int RT, int CT>
+__device__ __forceinline__ void low_product(rsrc_t x_rsrc, rsrc_t a_rsrc, int K, int k0, int k1, int lane,
+                                            f32x4 (&acc)[RT][CT]) {
+  const uint32_t voff = (uint32_t)((lane & 15) * K + (lane >> 4) * 8) * 2;
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < CT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+  constexpr int kDeep = RT + CT <= 3 ? 8 : RT + CT <= 6 ? 4 : 2;   // 32-value steps whose loads are in flight
+  for (int k = k0; k < k1; k += 32 * kDeep) {
+    u32x4 xs[kDeep][CT], ws[kDeep][RT];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int k_at = k + d * 32;
+      const uint32_t at = k_at < k1 ? voff + (uint32_t)k_at * 2 : kOob;
+#pragma unroll
+      for (int t = 0; t < CT; ++t) xs[d][t] = load_b128(x_rsrc, at + (uint32_t)(t * 16 * K) * 2, 0);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) ws[d][t] = load_b128(a_rsrc, at + (uint32_t)(t * 16 * K) * 2, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < CT; ++t) acc[r][t] = mfma16<BF16>(ws[d][r], xs[d][t], acc[r][t]);
+  }
+}
+
+__device__ __forceinline__ rsrc_t adapter_a(const LoraCall& c, int a) {
+  const int64_t n = (int64_t)c.bank.rank * c.bank.in_features;
+  return make_rsrc((const uint16_t*)c.bank.a + a * n, (uint32_t)n * 2);
+}
+
+// Few rows: part[slice][row][rank] = the slice's share of A_i x, the slice's K over the four waves.
+template <int BF16, int RT>   // rank tiles of 16
 __global__ void __launch_bounds__(kThreads, 2) lora_low_kernel(LoraCall c, LoraPlan p) {
-  constexpr int kRows = 16 * CT, kPitch = RT * 16 + 4;
-  __shared__ __align__(16) float sums[kWaves][kRows][kPitch];
+  constexpr int kPitch = RT * 16 + 4;
+  __shared__ __align__(16) float sums[kWaves][16][kPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, quad = lane >> 4;
   int id = blockIdx.x;
   const int slice = id % p.slices;
   id /= p.slices;
   const int turn = id % p.turns;
-  const int64_t row0 = (int64_t)(id / p.turns) * kRows;
+  const int64_t row0 = (int64_t)(id / p.turns) * 16;
   const int K = c.bank.in_features, rank = c.bank.rank;
-  const int my_id = lane_id(c, row0, kRows, lane);
-  const int k0 = (slice * kWaves + wave) * p.wave_k;
-  const int k1 = k0 + p.wave_k < K ? k0 + p.wave_k : K;
-  // rows and ranks past the last, and inputs past the slice, lie past the resources: they read as 0
-  const int rows = c.M - row0 < kRows ? (int)(c.M - row0) : kRows;
+  const int my_id = lane_id(c, row0, 16, lane);
+  const int k0 = slice * p.slice_k + wave * (p.slice_k / kWaves);
+  const int k1 = k0 + p.slice_k / kWaves < K ? k0 + p.slice_k / kWaves : K;
+  const int rows = c.M - row0 < 16 ? (int)(c.M - row0) : 16;
   const rsrc_t x_rsrc = make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2);
-  const uint32_t voff = (uint32_t)(col * K + quad * 16) * 2;
   float* part = (float*)c.ws + (int64_t)slice * c.M * rank;
 
+  bool first = true;
   each_adapter(my_id, turn, p.turns, [&](int a) {
-    const rsrc_t a_rsrc = make_rsrc((const uint16_t*)c.bank.a + (int64_t)a * rank * K, (uint32_t)rank * K * 2);
-    f32x4 acc[RT][CT];
+    f32x4 acc[RT][1];
+    low_product<BF16>(x_rsrc, adapter_a(c, a), K, k0, k1, lane, acc);
+    if (!first) __syncthreads();                       // the last adapter's sums are read
+    first = false;
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < CT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
-    constexpr int kDeep = RT * CT <= 2 ? 4 : RT <= 4 ? 2 : 1;      // 64-value steps whose loads are in flight
-    for (int k = k0; k < k1; k += 64 * kDeep) {
-      u32x4 xs[kDeep][CT][2], ws[kDeep][RT][2];
-#pragma unroll
-      for (int d = 0; d < kDeep; ++d) {
-        const uint32_t at = k + d * 64 + quad * 16 < k1 ? voff + (uint32_t)(k + d * 64) * 2 : kOob;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int t = 0; t < CT; ++t) xs[d][t][h] = load_b128(x_rsrc, at + 16 * h + (uint32_t)(t * 16 * K) * 2, 0);
-#pragma unroll
-          for (int t = 0; t < RT; ++t) ws[d][t][h] = load_b128(a_rsrc, at + 16 * h + (uint32_t)(t * 16 * K) * 2, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int d = 0; d < kDeep; ++d)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int t = 0; t < CT; ++t) acc[r][t] = mfma16<BF16>(ws[d][r][h], xs[d][t][h], acc[r][t]);
-    }
-    __syncthreads();                                   // the last adapter's sums are read
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < CT; ++t) *(f32x4*)&sums[wave][t * 16 + col][r * 16 + quad * 4] = acc[r][t];
+    for (int r = 0; r < RT; ++r) *(f32x4*)&sums[wave][lane & 15][r * 16 + (lane >> 4) * 4] = acc[r][0];
     __syncthreads();
-    for (int i = threadIdx.x; i < kRows * RT * 16; i += kThreads) {
+    for (int i = threadIdx.x; i < 16 * RT * 16; i += kThreads) {
       const int row = i / (RT * 16), r = i % (RT * 16);
       if (__shfl(my_id, row) != a || r >= rank) continue;
       float s = 0.0f;
@@ -127,10 +138,107 @@ __global__ void __launch_bounds__(kThreads, 2) lora_low_kernel(LoraCall c, LoraP
   });
 }
 
-// out = y + B_i low.
-template <int BF16, int KS, int CT>   // 32-value steps of the rank, row tiles of 16
-__global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(LoraCall c, LoraPlan p) {
-  constexpr int kRows = 16 * CT;
+// Many rows: the same, each wave its own kManyRows rows over all of the slice.
+template <int BF16, int RT>
+__global__ void __launch_bounds__(kThreads, 2) lora_low_rows_kernel(LoraCall c, LoraPlan p) {
+  constexpr int CT = kManyRows / 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slice = blockIdx.x % p.slices;
+  const int64_t row0 = ((int64_t)(blockIdx.x / p.slices) * kWaves + wave) * kManyRows;
+  if (row0 >= c.M) return;
+  const int K = c.bank.in_features, rank = c.bank.rank;
+  const int my_id = lane_id(c, row0, kManyRows, lane);
+  const int k0 = slice * p.slice_k, k1 = k0 + p.slice_k < K ? k0 + p.slice_k : K;
+  const int rows = c.M - row0 < kManyRows ? (int)(c.M - row0) : kManyRows;
+  const rsrc_t x_rsrc = make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2);
+  float* part = (float*)c.ws + ((int64_t)slice * c.M + row0) * rank;
+  each_adapter(my_id, 0, 1, [&](int a) {
+    f32x4 acc[RT][CT];
+    low_product<BF16>(x_rsrc, adapter_a(c, a), K, k0, k1, lane, acc);
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+      const int row = t * 16 + (lane & 15);
+      const bool mine = __shfl(my_id, row) == a;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int at = r * 16 + (lane >> 4) * 4;
+        if (mine && at < rank) *(f32x4*)(part + row * rank + at) = acc[r][t];
+      }
+    }
+  });
+}
+
+// low of eight ranks: the slices' parts in order, times the adapter's scale.
+__device__ __forceinline__ void add_parts(const float* from, int slices, int64_t apart, float scale, float* low) {
+  f32x4 s0{0, 0, 0, 0}, s1{0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < slices; ++s) {
+    s0 += *(const f32x4*)(from + s * apart);
+    s1 += *(const f32x4*)(from + s * apart + 4);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    low[e] = s0[e] * scale;
+    low[4 + e] = s1[e] * scale;
+  }
+}
+__device__ __forceinline__ float largest8(const float* v) {
+  float most = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) most = __builtin_fmaxf(most, __builtin_fabsf(v[e]));
+  return most;
+}
+// The power of two that takes a float16 row's largest magnitude into [2^13, 2^14).
+__device__ __forceinline__ int row_exponent(float most) {
+  const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127 - 13;
+  return e < -120 ? -120 : e > 114 ? 114 : e;
+}
+// low * down as value and remainder
+template <int BF16>
+__device__ __forceinline__ void split8(const float* low, float down, u32x4* high, u32x4* rest) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float v0 = low[2 * e] * down, v1 = low[2 * e + 1] * down;
+    const uint16_t h0 = from_f32<BF16>(v0), h1 = from_f32<BF16>(v1);
+    (*high)[e] = (uint32_t)h0 | (uint32_t)h1 << 16;
+    (*rest)[e] = (uint32_t)from_f32<BF16>(v0 - to_f32<BF16>(h0)) | (uint32_t)from_f32<BF16>(v1 - to_f32<BF16>(h1)) << 16;
+  }
+}
+
+// Many rows, between the products: low's two numbers of each row with an adapter, sixteen lanes a
+// row, eight ranks a lane.
+template <int BF16>
+__global__ void __launch_bounds__(kThreads) lora_join_kernel(LoraCall c, LoraPlan p) {
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
+  const int r = (threadIdx.x & 15) * 8, rank = c.bank.rank;
+  const int id = row < c.M ? c.ids[row] : -1;
+  const bool used = id >= 0 && id < c.bank.adapters;
+  float low[8] = {};
+  if (used && r < rank) add_parts((const float*)c.ws + row * rank + r, p.slices, c.M * rank, c.bank.scale[id], low);
+  float down = 1.0f;
+  uint16_t* lows = (uint16_t*)((uint8_t*)c.ws + p.part_bytes);
+  if constexpr (!BF16) {
+    float most = largest8(low);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) most = __builtin_fmaxf(most, __shfl_xor(most, d));
+    const int e = row_exponent(most);
+    down = __builtin_ldexpf(1.0f, -e);
+    if (used && r == 0) ((float*)(lows + 2 * c.M * rank))[row] = __builtin_ldexpf(1.0f, e);
+  }
+  if (!used || r >= rank) return;
+  u32x4 high, rest;
+  split8<BF16>(low, down, &high, &rest);
+  *(u32x4*)(lows + row * rank + r) = high;
+  *(u32x4*)(lows + (c.M + row) * rank + r) = rest;
+}
+
+// out = y + B_i low.  The waves of a workgroup share low (two 16-bit numbers, in LDS) and take 64
+// outputs each of a run of 256.
+template <int BF16, int KS, int CT, bool JOINED>   // 32-value steps of the rank, row tiles of 16; low joined
+__global__ void __launch_bounds__(kThreads, KS == 4 ? 2 : 3) lora_up_kernel(LoraCall c, LoraPlan p) {
+  constexpr int kRows = 16 * CT, kPitch = KS * 4 + 1;      // 16-byte chunks of a row: no two of eight rows on a bank
+  __shared__ __align__(16) u32x4 lows[2][kRows * kPitch];  // value, remainder
+  __shared__ float scaled[kRows];                          // the power of two that a row was scaled by
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   int id = blockIdx.x;
@@ -141,102 +249,118 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(LoraCall c, LoraPl
   const int N = c.bank.out_features, rank = c.bank.rank;
   const int my_id = lane_id(c, row0, kRows, lane);
   const int n_first = block_n * p.per_n * 256 + wave * 64;
+  const int rows = c.M - row0 < kRows ? (int)(c.M - row0) : kRows;
+  const rsrc_t y_rsrc = make_rsrc(c.y + row0 * N, (uint32_t)rows * N * 2);
+  const rsrc_t out_rsrc = make_rsrc(c.out + row0 * N, (uint32_t)rows * N * 2);
   int ids[CT];
 #pragma unroll
   for (int t = 0; t < CT; ++t) ids[t] = __shfl(my_id, t * 16 + col);
 
+  bool first = true;
   each_adapter(my_id, turn, p.turns, [&](int a) {
-    // low of the adapter's rows (zeros elsewhere), added over the slices in order
-    u32x4 high[CT][KS], rest[CT][KS];
-    float back[CT];
-    const float scale = c.bank.scale[a];
-#pragma unroll
-    for (int t = 0; t < CT; ++t) {
-      float low[KS][8];
-      float most = 0.0f;
-      const float* from = (const float*)c.ws + (row0 + t * 16 + col) * rank + quad * 8;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        f32x4 s0{0, 0, 0, 0}, s1{0, 0, 0, 0};
-        if (ids[t] == a && k * 32 + quad * 8 < rank) {
-#pragma unroll 4
-          for (int s = 0; s < p.slices; ++s) {
-            const float* at = from + (int64_t)s * c.M * rank + k * 32;
-            s0 += *(const f32x4*)at;
-            s1 += *(const f32x4*)(at + 4);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          low[k][e] = s0[e] * scale;
-          low[k][4 + e] = s1[e] * scale;
-          most = __builtin_fmaxf(most, __builtin_fmaxf(__builtin_fabsf(low[k][e]), __builtin_fabsf(low[k][4 + e])));
-        }
-      }
-      back[t] = 1.0f;
-      float down = 1.0f;
-      if constexpr (!BF16) {                           // the row's largest magnitude into [2^13, 2^14)
-        most = __builtin_fmaxf(most, __shfl_xor(most, 16));
-        most = __builtin_fmaxf(most, __shfl_xor(most, 32));
-        int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127 - 13;
-        e = e < -120 ? -120 : e > 114 ? 114 : e;
-        down = __builtin_ldexpf(1.0f, -e);
-        back[t] = __builtin_ldexpf(1.0f, e);
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v0 = low[k][2 * e] * down, v1 = low[k][2 * e + 1] * down;
-          const uint16_t h0 = from_f32<BF16>(v0), h1 = from_f32<BF16>(v1);
-          high[t][k][e] = (uint32_t)h0 | (uint32_t)h1 << 16;
-          rest[t][k][e] = (uint32_t)from_f32<BF16>(v0 - to_f32<BF16>(h0)) |
-                          (uint32_t)from_f32<BF16>(v1 - to_f32<BF16>(h1)) << 16;
-        }
-    }
     const rsrc_t b_rsrc = make_rsrc((const uint16_t*)c.bank.b + (int64_t)a * N * rank, (uint32_t)N * rank * 2);
-    for (int i = 0; i < p.per_n; ++i) {
-      const int n0 = n_first + i * 256;
-      if (n0 >= N) break;
-      // a lane's outputs are n0 + 16 quad .. + 15: row 4 q + e of tile t is output n0 + 16 q + 4 t + e
-      const int n = n0 + quad * 16;
-      f32x4 acc[4][CT];
+    // a lane's outputs are n0 + 32 h + 8 quad .. + 7: row 4 q + e of tile t is output n0 + 32 (t / 2) + 8 q +
+    // 4 (t % 2) + e, so that four lanes read and write 64 bytes of a row at once (past N, and in rows of
+    // other adapters: past the resource, read as 0 and not written)
+    u32x4 w[4][KS], in[CT][2];
+    uint32_t at[CT][2];
+    auto load = [&](int n0) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint32_t at = (uint32_t)((col >> 2) * 16 + t * 4 + (col & 3)) * rank * 2;   // past N: past the resource
-        u32x4 w[KS];
+        const uint32_t of = (uint32_t)((t >> 1) * 32 + (col >> 2) * 8 + (t & 1) * 4 + (col & 3)) * rank * 2;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const int r = k * 32 + quad * 8;
-          w[k] = load_b128(b_rsrc, r < rank ? at + r * 2 : kOob, (uint32_t)n0 * rank * 2);
-        }
-#pragma unroll
-        for (int m = 0; m < CT; ++m) {
-          acc[t][m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int k = 0; k < KS; ++k) acc[t][m] = mfma16<BF16>(w[k], high[m][k], acc[t][m]);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) acc[t][m] = mfma16<BF16>(w[k], rest[m][k], acc[t][m]);
+          w[t][k] = load_b128(b_rsrc, r < rank ? of + r * 2 : kOob, (uint32_t)n0 * rank * 2);
         }
       }
-      if (n >= N) continue;
 #pragma unroll
       for (int m = 0; m < CT; ++m) {
-        if (ids[m] != a) continue;
-        const int64_t at = (row0 + m * 16 + col) * N + n;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32x4 in = *(const u32x4*)(c.y + at + 8 * h);
+          at[m][h] = ids[m] == a && n0 + h * 32 < N ? (uint32_t)((m * 16 + col) * N + n0 + h * 32 + quad * 8) * 2 : kOob;
+          in[m][h] = load_b128(y_rsrc, at[m][h], 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (n_first < N) load(n_first);                    // on its way while low is added up
+
+    if (!first) __syncthreads();
+    first = false;
+    if constexpr (JOINED) {
+      // rows of other adapters hold zeros
+      const uint16_t* from = (const uint16_t*)((const uint8_t*)c.ws + p.part_bytes);
+      for (int i = threadIdx.x; i < kRows * KS * 4; i += kThreads) {
+        const int row = i / (KS * 4), r = i % (KS * 4) * 8;
+        const bool mine = __shfl(my_id, row) == a && r < rank;
+        const int64_t of = (row0 + row) * rank + r;
+        lows[0][row * kPitch + r / 8] = mine ? *(const u32x4*)(from + of) : u32x4{0, 0, 0, 0};
+        lows[1][row * kPitch + r / 8] = mine ? *(const u32x4*)(from + of + c.M * rank) : u32x4{0, 0, 0, 0};
+        if (!BF16 && r == 0) scaled[row] = mine ? ((const float*)(from + 2 * c.M * rank))[row0 + row] : 1.0f;
+      }
+    } else {
+      // wave w takes row tiles w, w + 4
+      for (int t = wave; t < CT; t += kWaves) {
+        float low[KS][8], most = 0.0f;
+        const bool mine = __shfl(my_id, t * 16 + col) == a;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) low[k][e] = 0.0f;
+          if (mine && k * 32 + quad * 8 < rank)
+            add_parts((const float*)c.ws + (row0 + t * 16 + col) * rank + k * 32 + quad * 8, p.slices, c.M * rank,
+                      c.bank.scale[a], low[k]);
+          most = __builtin_fmaxf(most, largest8(low[k]));
+        }
+        float down = 1.0f;
+        if constexpr (!BF16) {
+          most = __builtin_fmaxf(most, __shfl_xor(most, 16));
+          most = __builtin_fmaxf(most, __shfl_xor(most, 32));
+          const int e = row_exponent(most);
+          down = __builtin_ldexpf(1.0f, -e);
+          if (quad == 0) scaled[t * 16 + col] = __builtin_ldexpf(1.0f, e);
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int at = (t * 16 + col) * kPitch + k * 4 + quad;
+          split8<BF16>(low[k], down, &lows[0][at], &lows[1][at]);
+        }
+      }
+    }
+    __syncthreads();
+    float back[CT];
+#pragma unroll
+    for (int m = 0; m < CT; ++m) back[m] = BF16 ? 1.0f : scaled[m * 16 + col];
+
+    for (int i = 0; i < p.per_n && n_first + i * 256 < N; ++i) {
+#pragma unroll
+      for (int m = 0; m < CT; ++m) {
+        f32x4 acc[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const u32x4 low = lows[part][(m * 16 + col) * kPitch + k * 4 + quad];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t] = mfma16<BF16>(w[t][k], low, acc[t]);
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           u32x4 o;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const f32x4& v = acc[2 * h + (e >> 1)][m];
-            o[e] = (uint32_t)from_f32<BF16>(__builtin_fmaf(v[2 * (e & 1)], back[m], to_f32<BF16>((uint16_t)in[e]))) |
-                   (uint32_t)from_f32<BF16>(__builtin_fmaf(v[2 * (e & 1) + 1], back[m], to_f32<BF16>((uint16_t)(in[e] >> 16)))) << 16;
+            const f32x4& v = acc[2 * h + (e >> 1)];
+            const uint32_t y2 = in[m][h][e];
+            o[e] = (uint32_t)from_f32<BF16>(__builtin_fmaf(v[2 * (e & 1)], back[m], to_f32<BF16>((uint16_t)y2))) |
+                   (uint32_t)from_f32<BF16>(__builtin_fmaf(v[2 * (e & 1) + 1], back[m], to_f32<BF16>((uint16_t)(y2 >> 16)))) << 16;
           }
-          *(u32x4*)(c.out + at + 8 * h) = o;
+          __builtin_amdgcn_raw_buffer_store_b128(o, out_rsrc, at[m][h], 0, 0);
         }
       }
+      if (i + 1 < p.per_n && n_first + (i + 1) * 256 < N) load(n_first + (i + 1) * 256);
     }
   });
   // rows without an adapter
@@ -258,42 +382,44 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 LoraPlan plan_of(const gptq_lora_bank& bank, int64_t M) {
   LoraPlan p;
-  const bool few = M <= 128;
-  p.low_rows = few ? 16 : 32;
-  p.up_rows = few ? 16 : bank.rank > 64 ? 32 : 64;
-  p.low_tiles = (int)div_up(M, p.low_rows);
+  p.few = M <= 128;
+  p.up_rows = p.few ? 16 : bank.rank > 64 ? 32 : 64;
+  p.low_tiles = (int)div_up(M, p.few ? 16 : kWaves * kManyRows);
   p.up_tiles = (int)div_up(M, p.up_rows);
-  int64_t turns = few ? (M < 16 ? M : 16) : 1;
+  int64_t turns = p.few ? (M < 16 ? M : 16) : 1;
   if (turns > bank.adapters) turns = bank.adapters;
   p.turns = (int)turns;
-  // K: enough workgroups to fill the card, slices of at least one 64-value step a wave
-  const int64_t units = p.low_tiles * turns, steps = div_up(bank.in_features, 64 * kWaves);
+  // K: enough workgroups to fill the card, slices of at least 64 values a wave
+  const int64_t units = p.low_tiles * turns, step = p.few ? 64 * kWaves : 64, steps = div_up(bank.in_features, step);
   int64_t slices = div_up(512, units);
   if (slices > 16) slices = 16;
   if (slices > steps) slices = steps;
-  p.wave_k = (int)(div_up(steps, slices) * 64);
-  p.slices = (int)div_up(bank.in_features, (int64_t)p.wave_k * kWaves);
+  p.slice_k = (int)(div_up(steps, slices) * step);
+  p.slices = (int)div_up(bank.in_features, p.slice_k);
   const int64_t blocks = div_up(bank.out_features, 256);
-  int64_t per = p.up_tiles * turns * blocks / 1024;
+  int64_t per = p.up_tiles * turns * blocks / 1536;
   p.per_n = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
-  if (few) p.per_n = 1;
   p.blocks_n = (int)div_up(blocks, p.per_n);
+  p.part_bytes = (size_t)div_up((int64_t)p.slices * M * bank.rank * 4, 256) * 256;
   return p;
 }
 
 template <int BF16, int RT>
 void launch_low(const LoraCall& c, const LoraPlan& p, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.low_tiles * p.turns * p.slices)), block(kThreads);
-  if (p.low_rows == 16) lora_low_kernel<BF16, RT, 1><<<grid, block, 0, s>>>(c, p);
-  else lora_low_kernel<BF16, RT, 2><<<grid, block, 0, s>>>(c, p);
+  if (p.few) lora_low_kernel<BF16, RT><<<grid, block, 0, s>>>(c, p);
+  else lora_low_rows_kernel<BF16, RT><<<grid, block, 0, s>>>(c, p);
 }
 
 template <int BF16, int KS>
 void launch_up(const LoraCall& c, const LoraPlan& p, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.up_tiles * p.turns * p.blocks_n)), block(kThreads);
-  if (p.up_rows == 16) lora_up_kernel<BF16, KS, 1><<<grid, block, 0, s>>>(c, p);
-  else if (KS == 4) lora_up_kernel<BF16, KS, 2><<<grid, block, 0, s>>>(c, p);
-  else lora_up_kernel<BF16, KS, KS == 4 ? 2 : 4><<<grid, block, 0, s>>>(c, p);
+  if (p.few) {
+    lora_up_kernel<BF16, KS, 1, false><<<grid, block, 0, s>>>(c, p);
+  } else {
+    lora_join_kernel<BF16><<<dim3((uint32_t)div_up(c.M, kThreads / 16)), block, 0, s>>>(c, p);
+    lora_up_kernel<BF16, KS, KS == 4 ? 2 : 4, true><<<grid, block, 0, s>>>(c, p);
+  }
 }
 
 template <int BF16>
@@ -315,7 +441,8 @@ hipError_t launch_type(const LoraCall& c, hipStream_t s) {
 }  // namespace
 
 size_t lora_ws_bytes(const gptq_lora_bank& bank, int64_t M) {
-  return ((size_t)plan_of(bank, M).slices * M * bank.rank * 4 + 255) / 256 * 256;
+  const LoraPlan p = plan_of(bank, M);
+  return p.few ? p.part_bytes : (p.part_bytes + (size_t)M * bank.rank * 4 + (size_t)M * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_lora(const LoraCall& c, hipStream_t s) {
