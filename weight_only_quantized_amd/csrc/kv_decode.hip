@@ -13,13 +13,16 @@
 // after a power-of-two scaling of its row, and a weight keeps 11 bits down to 2^-20 of the largest
 // one: the one rounding below 32 bits, of the size of the output's own.
 //
-// Split.  One workgroup takes up to 32 (row, head) columns of one sequence and kv head over a run of
-// tokens; its four waves take 32 tokens each in turn and join at the end through LDS.  Long runs
-// are split over workgroups whose unnormalised sums a second launch joins in order.  Products are
-// computed as rows = tokens, columns = queries (v_mfma_f32_16x16x32_f16), which leaves each lane
-// with the weights of just those tokens whose values it holds as the second product's operand:
-// codes go from memory to the matrix cores without LDS.
+// Split.  The work is cut into steps of 32 tokens of a unit: up to 32 (row, head) columns of one
+// sequence and kv head.  All units' steps in order are dealt to as many waves as the card holds at
+// once, the same number to each: sequences of any lengths fill it evenly, and no wave waits for
+// another.  Units that cross waves leave unnormalised sums that a second launch joins in order.
+// Products are computed as rows = tokens, columns = queries (v_mfma_f32_16x16x32_f16), which leaves
+// each lane with the weights of just those tokens whose values it holds as the second product's
+// operand: codes go from memory to the matrix cores without LDS.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "kv_dev.h"
 
@@ -27,73 +30,132 @@ namespace gq {
 namespace {
 
 constexpr int kThreads = 256, kWaves = 4;
-constexpr int kStep = 32;                          // tokens of a wave's step: two tiles of 16
-constexpr int kStride = kStep * kWaves;            // tokens of a workgroup's step
-constexpr int kMaxRun = 64 / 2 * kStride;          // a wave holds its tiles' pages one a lane
+constexpr int kStep = 32;                          // tokens of a step: two tiles of 16
+constexpr int kMaxRun = 64 * 16;                   // a wave holds the pages of its tiles one a lane
 
 struct DecodePlan {
-  int col_tiles;    // 16-column tiles of a workgroup: 1 or 2
-  int col_groups;   // workgroups for a sequence and kv head's columns
-  int splits;       // runs of `run` tokens
-  int run;
+  int col_tiles;    // 16-column tiles of a unit: 1 or 2
+  int col_groups;   // units of a sequence and kv head, at most
+  int waves;
+  int units;        // batch * kv_heads * col_groups
+  int width;        // columns of a part: those that a unit can have
+  int split;        // units may cross waves: they leave parts
+  int many_parts;   // few or very long units, of some 32 parts or more: a workgroup joins them, else a wave
 };
 
-// Tokens [lo, hi) that some column of a column group sees; lo at a tile.
-struct GroupRange {
-  int columns;             // of the sequence and kv head
-  int64_t lo, hi;
-  KeyRange first, last;    // of the group's first and last row
+// A unit's parts, in the workspace: `count` of them from slot `first` on, one a wave.  Wave w
+// leaves its part of unit u in slot w + u, which no other pair shares since both only ascend.
+struct UnitParts {
+  int first, count;
 };
-__device__ __forceinline__ GroupRange group_range(const SeqRows& s, const KvAttentionCall& a, const DecodePlan& plan,
-                                                  int first_col, int page_shift) {
-  const int group = a.a.q_heads / a.c.kv_heads;
-  GroupRange r;
-  r.columns = s.rows * group;
-  const int width = 16 * plan.col_tiles;
-  const int last_col = first_col + width < r.columns ? first_col + width - 1 : r.columns - 1;
-  const int64_t room = key_room(a.b, a.a, page_shift);
-  r.first = key_range(s, first_col / group, a.a, room);
-  r.last = key_range(s, last_col / group, a.a, room);
-  r.lo = r.first.begin & ~(int64_t)15;
-  r.hi = r.last.end;
-  const int64_t most = r.lo + (int64_t)plan.run * plan.splits;      // never past what was planned
-  r.hi = r.hi < most ? r.hi : most;
-  return r;
+__host__ __device__ inline size_t parts_offset(const DecodePlan& p) { return ((size_t)p.units * sizeof(UnitParts) + 255) / 256 * 256; }
+
+// Tokens [lo, hi) that some row of a sequence sees, lo at 16, in `steps`; `groups` units of them for
+// each kv head.  A sequence with rows has a step even if they see nothing (it writes zeros).
+struct SeqWork {
+  SeqRows s;
+  int lo, hi, steps, groups;
+};
+template <int CT>
+__device__ __forceinline__ SeqWork sequence_work(const KvAttentionCall& a, const SeqRows& s, int room) {
+  SeqWork w;
+  w.s = s;
+  w.lo = w.hi = w.steps = w.groups = 0;
+  if (w.s.rows == 0) return w;
+  w.lo = key_range(w.s, 0, a.a, room).begin & ~15;
+  w.hi = key_range(w.s, w.s.rows - 1, a.a, room).end;
+  w.steps = w.hi > w.lo ? (w.hi - w.lo + kStep - 1) / kStep : 1;
+  w.groups = (w.s.rows * (a.a.q_heads / a.c.kv_heads) + 16 * CT - 1) / (16 * CT);
+  return w;
+}
+
+// The kernel's first argument, read again: keeping all of it in scalar registers over the loop on
+// units takes more than there are.
+__device__ __forceinline__ KvAttentionCall call_again() {
+  auto p = (const __attribute__((address_space(4))) KvAttentionCall*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const KvAttentionCall*)p;
 }
 
 template <int BF16, int DIM, int CT>
-__global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
-    kv_decode_kernel(KvAttentionCall a, DecodePlan plan, int page_shift) {
+__global__ void __launch_bounds__(kThreads, 2)
+    kv_decode_kernel(KvAttentionCall call, DecodePlan plan, int page_shift) {
   constexpr int KL = DIM / 64;      // 16-byte loads of a lane for a tile's keys
   constexpr int VB = DIM / 16;      // bytes of a value row that a lane holds, one for each output tile
   constexpr int VW = VB / 4;
-  constexpr int kPitch = DIM + 4;   // of a column's sums in LDS and memory
-  __shared__ __align__(16) float sums[kWaves][16][kPitch];
+  constexpr int kPitch = DIM + 4;   // of a column's sums in memory
+  // a wave's keys of a step: memory is read a row by neighbouring lanes (lanes that each read their
+  // own row cost the address unit a cycle a lane), the product wants a row a lane.  16-byte pieces
+  // of row r are stored at piece ^ kTurn(r): eight rows' pieces cover all banks.
+  __shared__ __align__(16) u32x4 key_rows[kWaves][2][16 * (DIM / 16)];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col16 = lane & 15, quad = lane >> 4;
-  int id = blockIdx.x;
-  const int kv_head = id % a.c.kv_heads;
-  id /= a.c.kv_heads;
-  const int first_col = id % plan.col_groups * (16 * CT);
-  id /= plan.col_groups;
-  const int seq = id % a.b.batch, split = id / a.b.batch;
+  const int room = key_room(call.b, call.a, page_shift);
+  const int group = call.a.q_heads / call.c.kv_heads;
 
-  const SeqRows s = sequence_rows(a.b, seq);
-  const int group = a.a.q_heads / a.c.kv_heads;
-  if (first_col >= s.rows * group) return;
-  const GroupRange g = group_range(s, a, plan, first_col, page_shift);
-  const int64_t run0 = g.lo + (int64_t)split * plan.run;
-  if (split > 0 && run0 >= g.hi) return;
-  const int64_t run1 = g.hi < run0 + plan.run ? g.hi : run0 + plan.run;
-  const bool alone = g.lo + plan.run >= g.hi;      // no other run of these columns has tokens
-  const int64_t room = key_room(a.b, a.a, page_shift);
+  // this wave's steps [share w, share (w + 1)) of all, and the sequence where they start: a scan over
+  // 64 sequences at a time, one a lane
+  const int wave_id = blockIdx.x * kWaves + wave;
+  SeqRows held;                                   // of sequence q + lane
+  auto steps_of = [&](int q) {
+    held = q < call.b.batch ? sequence_rows(call.b, q) : SeqRows{0, 0, 0, 0};
+    const SeqWork w = sequence_work<CT>(call, held, room);
+    return w.steps * w.groups * call.c.kv_heads;
+  };
+  const bool one_scan = call.b.batch <= 64;       // then `held` stays
+  int all = 0, mine = 0, upto = 0;
+  if (one_scan) {
+    mine = steps_of(lane);
+    upto = wave_scan(mine);
+    all = __builtin_amdgcn_readlane(upto, 63);
+  } else {
+    for (int q = 0; q < call.b.batch; q += 64) all += wave_sum(steps_of(q + lane));
+  }
+  const int full = (all + plan.waves - 1) / plan.waves;
+  if ((int64_t)full * wave_id >= all) return;
+  const int pos0 = full * wave_id, dealt = all - pos0 < full ? all - pos0 : full;
+  int seq = 0, skipped = 0;                       // the sequence, and its steps that come before
+  for (int q = 0, before = 0; q < call.b.batch; q += 64) {
+    if (!one_scan) {
+      mine = steps_of(q + lane);
+      upto = before + wave_scan(mine);            // steps up to and with this lane's sequence
+    }
+    const uint64_t past = __ballot(upto <= pos0);
+    if (past != ~0ull) {
+      const int at = __builtin_popcountll(past);
+      seq = q + at;
+      skipped = pos0 - __builtin_amdgcn_readlane(upto - mine, at);
+      break;
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+  auto rows_of = [&](int q) {
+    if (!one_scan) return sequence_rows(call.b, q);
+    return SeqRows{__builtin_amdgcn_readlane(held.row0, q), __builtin_amdgcn_readlane(held.rows, q),
+                   __builtin_amdgcn_readlane(held.length, q), __builtin_amdgcn_readlane(held.before, q)};
+  };
+  int left = dealt;
 
-  // the wave's tiles, one a lane
-  const int steps = run1 > run0 ? (int)((run1 - run0 + kStride - 1) / kStride) : 0;
-  const int64_t my_pos = run0 + ((lane >> 1) * kWaves + wave) * kStep + (lane & 1) * 16;
-  const TilePage mine = tile_page(a.c, a.b, seq, kv_head, my_pos, my_pos < run1, page_shift);
-  const float my_log = scale_log(mine.v_scale), my_inv = scale_inv(my_log);
+  while (left > 0 && seq < call.b.batch) {
+  const KvAttentionCall a = call_again();
+  const SeqWork work = sequence_work<CT>(a, rows_of(seq), room);
+  const SeqRows s = work.s;
+  if (skipped >= work.steps * work.groups * a.c.kv_heads) {   // the next sequence (without rows: no steps)
+    skipped = 0;
+    ++seq;
+    continue;
+  }
+  const int unit = skipped / work.steps, step0 = skipped % work.steps;
+  const int kv_head = unit / work.groups, first_col = unit % work.groups * (16 * CT), columns = s.rows * group;
+  const int steps = work.steps - step0 < left ? work.steps - step0 : left;
+  const bool alone = steps == work.steps;        // the unit is all here
+  const int unit_id = (seq * a.c.kv_heads + kv_head) * plan.col_groups + unit % work.groups;
+  if (plan.split && step0 == 0 && lane == 0)
+    ((UnitParts*)a.ws)[unit_id] = UnitParts{wave_id + unit_id, (dealt - left + work.steps - 1) / full + 1};
+  const int run0 = work.lo + step0 * kStep;
+  const int run1 = work.hi < run0 + steps * kStep ? work.hi : run0 + steps * kStep;
+  const int last_col = first_col + 16 * CT < columns ? first_col + 16 * CT - 1 : columns - 1;
 
   // this lane's columns: visible tokens and the query (columns past the last repeat it)
   int begin[CT], end[CT];
@@ -102,18 +164,20 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     int c = first_col + ct * 16 + col16;
-    c = c < g.columns ? c : g.columns - 1;
+    c = c < columns ? c : columns - 1;
     const int row = c / group, head = kv_head * group + c % group;
     const KeyRange r = key_range(s, row, a.a, room);
-    begin[ct] = (int)r.begin;
-    end[ct] = (int)r.end;
-    const uint16_t* at = a.q + (s.row0 + row) * a.a.q_stride + head * DIM + quad * 16;
+    begin[ct] = r.begin;
+    end[ct] = r.end;
+    const uint16_t* at = a.q + (int64_t)(s.row0 + row) * a.a.q_stride + head * DIM + quad * 16;
     q_scale[ct] = load_query<BF16, 2 * KL>(at, [](int i) { return (i >> 1) * 64 + (i & 1) * 8; }, q[ct], 16, 32) *
                   (a.a.scale * kLog2e);
     top[ct] = kNoTop;
     total[ct] = 0.0f;
   }
-  const int inner_lo = (int)g.last.begin, inner_hi = (int)g.first.end;   // all columns see these tokens
+  // all columns see these tokens
+  const int inner_lo = key_range(s, last_col / group, a.a, room).begin;
+  const int inner_hi = key_range(s, first_col / group, a.a, room).end;
 
   f32x4 acc[CT][VB];
 #pragma unroll
@@ -125,80 +189,116 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
     u32x4 k[2][KL];
     uint32_t v[2][4][VW];
   };
-  const uint32_t k_off = col16 * DIM + quad * 16, v_off = quad * 4 * DIM + col16 * VB;
-  auto load = [&](Step& d, int i) {
+  // up to 32 steps at a time, from token `base` on: their pages, 16 tokens a lane
+  int base = run0;
+  TilePage pages;
+  float my_log, my_inv;
+  const uint32_t k_off = lane * 16, v_off = quad * 4 * DIM + col16 * VB;
+  // Keys and values of a step are loaded again, for two steps ahead, as soon as they are used: up to two
+  // steps of a wave are on their way (steps past the last are absent tiles: they read page 0).
+  auto step_base = [&](int i, int t) {
+    return tile_base(a.c, __builtin_amdgcn_readlane(pages.page, (2 * i + t) & 63), kv_head,
+                     base + i * kStep + t * 16, page_shift);
+  };
+  auto load_keys = [&](Step& d, int i) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint64_t base = tile_base(a.c, __builtin_amdgcn_readlane(mine.page, 2 * i + t), kv_head,
-                                      (int)run0 + (i * kWaves + wave) * kStep + t * 16, page_shift);
-      const int8_t *kb = a.c.k_codes + base, *vb = a.c.v_codes + base;
+      const int8_t* kb = a.c.k_codes + step_base(i, t);
 #pragma unroll
-      for (int j = 0; j < KL; ++j) d.k[t][j] = *(const u32x4*)(kb + k_off + j * 64);
+      for (int j = 0; j < KL; ++j) d.k[t][j] = *(const u32x4*)(kb + k_off + j * 1024);
+    }
+  };
+  constexpr int kPieces = DIM / 16;               // of a key row
+  auto turn = [](int row) { return DIM == 128 ? row & 7 : row >> 1 & 3; };
+  const int put_row = lane / kPieces, put_at = put_row * kPieces + (lane % kPieces ^ turn(put_row));
+  const int get_at = col16 * kPieces + (quad ^ turn(col16));      // piece quad; piece 4 + quad is at ^ 4
+  auto load_values = [&](Step& d, int i) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int8_t* vb = a.c.v_codes + step_base(i, t);
 #pragma unroll
       for (int e = 0; e < 4; ++e) __builtin_memcpy(d.v[t][e], __builtin_assume_aligned(vb + v_off + e * DIM, VB), VB);
     }
   };
-  auto compute = [&](const Step& d, int i) {
-    const int pos = (int)run0 + (i * kWaves + wave) * kStep;
+  auto compute = [&](Step& d, int i, auto more) {
+    const int pos = base + i * kStep;
     f32x4 dot[2][CT];
     float ks[2], lv[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < KL; ++j) key_rows[wave][t][put_at + j * 64] = d.k[t][j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");        // the wave's LDS accesses stay in order
+    if constexpr (decltype(more)::value) load_keys(d, i + 2);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) dot[t][ct] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < KL; ++j) {
-        const f16x8 k0 = __builtin_bit_cast(f16x8, codes_f16(d.k[t][j][0], d.k[t][j][1]));
-        const f16x8 k1 = __builtin_bit_cast(f16x8, codes_f16(d.k[t][j][2], d.k[t][j][3]));
+        const u32x4 k = key_rows[wave][t][get_at ^ (j * 4)];
+        const f16x8 k0 = __builtin_bit_cast(f16x8, codes_f16(k[0], k[1]));
+        const f16x8 k1 = __builtin_bit_cast(f16x8, codes_f16(k[2], k[3]));
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           dot[t][ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[ct][2 * j], dot[t][ct], 0, 0, 0);
           dot[t][ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[ct][2 * j + 1], dot[t][ct], 0, 0, 0);
         }
       }
-      ks[t] = lane_f32(mine.k_scale, 2 * i + t);
+      ks[t] = lane_f32(pages.k_scale, 2 * i + t);
       lv[t] = lane_f32(my_log, 2 * i + t);
     }
-    const bool edge = pos < inner_lo || pos + kStep > inner_hi;     // some column does not see the whole step
-    float x[2][4];
-    // x = the exponents of column tile ct's weights relative to `from`; returns the largest
-    auto exponents = [&](int ct, float from) {
-      float most = -__builtin_inff();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // x = the exponents of the weights relative to the columns' tops
+    float x[CT][2][4], most = -__builtin_inff();
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float by = q_scale[ct] * ks[t], plus = lv[t] - top[ct];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[t][e] = __builtin_fmaf(dot[t][ct][e], q_scale[ct] * ks[t], lv[t] - from);
-          if (edge) {
-            const int p = pos + t * 16 + quad * 4 + e;
-            if (p < begin[ct] || p >= end[ct]) x[t][e] = -__builtin_inff();
-          }
-          most = __builtin_fmaxf(most, x[t][e]);
+          x[ct][t][e] = __builtin_fmaf(dot[t][ct][e], by, plus);
+          most = __builtin_fmaxf(most, x[ct][t][e]);
         }
-      return most;
-    };
+      }
+    // seldom: some column does not see the whole step, or a top has to move
+    if (__builtin_expect(pos < inner_lo || pos + kStep > inner_hi || __any(most > kGrow), 0)) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int p = pos + t * 16 + quad * 4 + e;
+            const float v = __builtin_fmaf(dot[t][ct][e], q_scale[ct] * ks[t], lv[t]);
+            x[ct][t][e] = p < begin[ct] || p >= end[ct] ? -__builtin_inff() : v;
+            m = __builtin_fmaxf(m, x[ct][t][e]);
+          }
+        m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+        m = __builtin_fmaxf(m, __shfl_xor(m, 32));                  // the four lanes of a column agree
+        const bool moves = m - top[ct] > kGrow;
+        const float to = moves ? m - kAbove : top[ct], keep = moves ? __builtin_amdgcn_exp2f(top[ct] - to) : 1.0f;
+        top[ct] = to;
+        total[ct] *= keep;
+#pragma unroll
+        for (int t = 0; t < VB; ++t) acc[ct][t] *= keep;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[ct][t][e] -= to;
+      }
+    }
     f16x8 w[CT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      if (__any(exponents(ct, top[ct]) > kGrow)) {
-        float most = exponents(ct, 0.0f);
-        most = __builtin_fmaxf(most, __shfl_xor(most, 16));
-        most = __builtin_fmaxf(most, __shfl_xor(most, 32));         // the four lanes of a column agree
-        if (most - top[ct] > kGrow) {
-          const float moved = most - kAbove, keep = __builtin_amdgcn_exp2f(top[ct] - moved);
-          top[ct] = moved;
-          total[ct] *= keep;
-#pragma unroll
-          for (int t = 0; t < VB; ++t) acc[ct][t] *= keep;
-        }
-        (void)exponents(ct, top[ct]);
-      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const float rv = lane_f32(my_inv, 2 * i + t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(x[t][e]);
+          const float p = __builtin_amdgcn_exp2f(x[ct][t][e]);
           total[ct] = __builtin_fmaf(p, rv, total[ct]);
           w[ct][t * 4 + e] = (_Float16)p;
         }
@@ -212,134 +312,156 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 3 : 2)
       for (int ct = 0; ct < CT; ++ct)
         acc[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), w[ct], acc[ct][t], 0, 0, 0);
     }
+    if constexpr (decltype(more)::value) load_values(d, i + 2);
   };
 
-  Step even, odd;
-  if (steps > 0) load(even, 0);
-  for (int i = 0; i < steps; i += 2) {
-    if (i + 1 < steps) load(odd, i + 1);
-    compute(even, i);
-    if (i + 1 < steps) {
-      if (i + 2 < steps) load(even, i + 2);
-      compute(odd, i + 1);
+  for (; base < run1; base += kMaxRun) {
+    const int my_pos = base + lane * 16;
+    pages = tile_page(a.c, a.b, seq, kv_head, my_pos, my_pos < run1, page_shift);
+    my_log = scale_log(pages.v_scale);
+    my_inv = scale_inv(my_log);
+    const int n = run1 - base < kMaxRun ? (run1 - base + kStep - 1) / kStep : kMaxRun / kStep;
+    Step even, odd;
+    // in the order of the steps: a wait for one load waits for all before it
+    load_keys(even, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_values(even, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_keys(odd, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    load_values(odd, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (CT == 1) {               // pairs, so that every wait in the loop is for what it needs
+      int i = 0;
+      for (; i + 1 < n; i += 2) {
+        compute(even, i, std::true_type{});
+        compute(odd, i + 1, std::true_type{});
+      }
+      if (i < n) compute(even, i, std::false_type{});
+    } else {                               // (two column tiles have no registers for the last step's copy)
+      for (int i = 0; i < n; i += 2) {
+        compute(even, i, std::true_type{});
+        if (i + 1 < n) compute(odd, i + 1, std::true_type{});
+      }
     }
   }
 
-  // join the four waves, one column tile at a time: output tile t of lane (col16, quad) holds values
-  // VB * (4 quad + e) + t
+  // output tile t of lane (col16, quad) holds values VB (4 quad + e) + t
+  const KvAttentionCall e_call = call_again();
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
-    if (ct) __syncthreads();
     float sum = total[ct];
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    float* mine_sums = sums[wave][col16];
+    const int c = first_col + ct * 16 + col16;
+    if (c >= columns) continue;
+    if (alone) {
+      const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+      uint16_t* to = e_call.out + (int64_t)(s.row0 + c / group) * e_call.a.out_stride + (kv_head * group + c % group) * DIM;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4; ++e) {
+        uint32_t o[VB / 2];
 #pragma unroll
-      for (int t = 0; t < VB; t += 4)
-        *(f32x4*)(mine_sums + VB * (4 * quad + e) + t) =
-            f32x4{acc[ct][t][e], acc[ct][t + 1][e], acc[ct][t + 2][e], acc[ct][t + 3][e]};
-    if (quad == 0) {
-      mine_sums[DIM] = top[ct];
-      mine_sums[DIM + 1] = sum;
-    }
-    __syncthreads();
-    constexpr int kPer = DIM / 16;                 // values of a thread: 16 threads a column
-    const int c = first_col + ct * 16 + (int)(threadIdx.x >> 4), d0 = (threadIdx.x & 15) * kPer;
-    if (c < g.columns) {
-      float most = kNoTop, all = 0.0f, o[kPer];
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) most = __builtin_fmaxf(most, sums[w][threadIdx.x >> 4][DIM]);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float* from = sums[w][threadIdx.x >> 4];
-        const float keep = __builtin_amdgcn_exp2f(from[DIM] - most);
-        all = __builtin_fmaf(from[DIM + 1], keep, all);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] = __builtin_fmaf(from[d0 + e], keep, o[e]);
+        for (int t = 0; t < VB; t += 2)
+          o[t / 2] = (uint32_t)from_f32<BF16>(acc[ct][t][e] * inv) | (uint32_t)from_f32<BF16>(acc[ct][t + 1][e] * inv) << 16;
+        __builtin_memcpy(__builtin_assume_aligned(to + VB * (4 * quad + e), VB * 2), o, VB * 2);
       }
-      const int64_t row = s.row0 + c / group;
-      const int head = kv_head * group + c % group;
-      if (alone) {
-        const float inv = all != 0.0f ? 1.0f / all : 0.0f;
-        uint16_t* to = a.out + row * a.a.out_stride + head * DIM + d0;
-        uint32_t packed[kPer / 2];
+    } else {
+      float* to = (float*)((uint8_t*)e_call.ws + parts_offset(plan)) +
+                  ((int64_t)(wave_id + unit_id) * plan.width + ct * 16 + col16) * kPitch;
 #pragma unroll
-        for (int e = 0; e < kPer / 2; ++e)
-          packed[e] = (uint32_t)from_f32<BF16>(o[2 * e] * inv) | (uint32_t)from_f32<BF16>(o[2 * e + 1] * inv) << 16;
-        __builtin_memcpy(__builtin_assume_aligned(to, kPer * 2), packed, kPer * 2);
-      } else {
-        float* to = (float*)a.ws + ((row * a.a.q_heads + head) * plan.splits + split) * kPitch;
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int e = 0; e < kPer; e += 4) *(f32x4*)(to + d0 + e) = f32x4{o[e], o[e + 1], o[e + 2], o[e + 3]};
-        if (d0 == 0) {
-          to[DIM] = most;
-          to[DIM + 1] = all;
-        }
+        for (int t = 0; t < VB; t += 4)
+          *(f32x4*)(to + VB * (4 * quad + e) + t) =
+              f32x4{acc[ct][t][e], acc[ct][t + 1][e], acc[ct][t + 2][e], acc[ct][t + 3][e]};
+      if (quad == 0) {
+        to[DIM] = top[ct];
+        to[DIM + 1] = sum;
       }
     }
   }
+  left -= steps;
+  skipped += steps;
+  }
 }
 
-// out = the runs' sums joined in order, one wave for a row and head (those that were split only).
-template <int BF16, int DIM>
-__global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, DecodePlan plan, int page_shift) {
-  constexpr int kPitch = DIM + 4, kPer = DIM / 64;
-  const int64_t wave = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  const int64_t row = wave / a.a.q_heads;
+// out = a unit's parts joined in order (those in more than one part only): THREADS for a row and
+// head, DIM / 4 of them hold a part, the groups take parts in turn and join at the end.
+template <int BF16, int DIM, int THREADS>
+__global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, DecodePlan plan) {
+  constexpr int kPitch = DIM + 4, kLanes = DIM / 4, kGroups = THREADS / kLanes;
+  __shared__ __align__(16) float sums[THREADS == kThreads ? kWaves : 1][kPitch];
+  const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / THREADS;
+  const int64_t row = item / a.a.q_heads;
   if (row >= a.b.rows) return;
-  const int head = (int)(wave % a.a.q_heads), group = a.a.q_heads / a.c.kv_heads;
+  const int head = (int)(item % a.a.q_heads), group = a.a.q_heads / a.c.kv_heads;
   const int seq = find_sequence(a.b.batch, row, [&](int i) { return (int64_t)a.b.cu[i]; });
   const SeqRows s = sequence_rows(a.b, seq);
-  const int64_t place = row - s.row0;
+  const int place = (int)row - s.row0;
   if (place < 0 || place >= s.rows) return;
-  const int width = 16 * plan.col_tiles, c = (int)place * group + head % group;
-  const GroupRange g = group_range(s, a, plan, c / width * width, page_shift);
-  const int64_t runs = (g.hi - g.lo + plan.run - 1) / plan.run;
-  if (runs <= 1) return;
-  const float* part = (const float*)a.ws + (row * a.a.q_heads + head) * plan.splits * kPitch;
-  float most = kNoTop;
-  for (int i = lane; i < runs; i += 64) most = __builtin_fmaxf(most, part[(int64_t)i * kPitch + DIM]);
-#pragma unroll
-  for (int d = 32; d; d >>= 1) most = __builtin_fmaxf(most, __shfl_xor(most, d));
-  float all = 0.0f, o[kPer] = {};
+  const int width = 16 * plan.col_tiles, c = place * group + head % group;
+  const UnitParts parts = ((const UnitParts*)a.ws)[(seq * a.c.kv_heads + head / group) * plan.col_groups + c / width];
+  if (parts.count <= 1) return;
+  const float* part = (const float*)((const uint8_t*)a.ws + parts_offset(plan)) +
+                      ((int64_t)parts.first * plan.width + c % width) * kPitch;
+  const int thread = threadIdx.x % THREADS, in_part = thread % kLanes;
+  float most = kNoTop, all = 0.0f;
+  f32x4 o{0, 0, 0, 0};
+  auto join = [&](float top, float sum, f32x4 v) {
+    const float now = __builtin_fmaxf(most, top);
+    const float keep = __builtin_amdgcn_exp2f(most - now), in = __builtin_amdgcn_exp2f(top - now);
+    all = all * keep + sum * in;
+    o = o * keep + v * in;
+    most = now;
+  };
 #pragma unroll 4
-  for (int i = 0; i < runs; ++i) {
-    const float* from = part + (int64_t)i * kPitch;
-    const float keep = __builtin_amdgcn_exp2f(from[DIM] - most);
-    all = __builtin_fmaf(from[DIM + 1], keep, all);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = __builtin_fmaf(from[lane * kPer + e], keep, o[e]);
+  for (int i = thread / kLanes; i < parts.count; i += kGroups) {
+    const float* from = part + (int64_t)i * plan.width * kPitch;
+    join(from[DIM], from[DIM + 1], *(const f32x4*)(from + in_part * 4));
   }
-  const float inv = all != 0.0f ? 1.0f / all : 0.0f;
-  uint16_t* to = a.out + row * a.a.out_stride + head * DIM + lane * kPer;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) to[e] = from_f32<BF16>(o[e] * inv);
+  for (int d = kLanes; d < 64; d <<= 1)
+    join(__shfl_xor(most, d), __shfl_xor(all, d),
+         f32x4{__shfl_xor(o[0], d), __shfl_xor(o[1], d), __shfl_xor(o[2], d), __shfl_xor(o[3], d)});
+  if constexpr (THREADS == kThreads) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) < kLanes) *(f32x4*)&sums[wave][in_part * 4] = o;
+    if ((threadIdx.x & 63) == 0) {
+      sums[wave][DIM] = most;
+      sums[wave][DIM + 1] = all;
+    }
+    __syncthreads();
+    if (threadIdx.x < kLanes)
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) join(sums[w][DIM], sums[w][DIM + 1], *(const f32x4*)&sums[w][in_part * 4]);
+  }
+  if (thread >= kLanes) return;
+  const float inv = all != 0.0f ? 1.0f / all : 0.0f;
+  uint2 w;
+  w.x = (uint32_t)from_f32<BF16>(o[0] * inv) | (uint32_t)from_f32<BF16>(o[1] * inv) << 16;
+  w.y = (uint32_t)from_f32<BF16>(o[2] * inv) | (uint32_t)from_f32<BF16>(o[3] * inv) << 16;
+  *(uint2*)(a.out + row * a.a.out_stride + head * DIM + in_part * 4) = w;
 }
 
-// Runs: enough workgroups to fill the card (256 CUs, three workgroups each) a few times over, but no
-// run shorter than a workgroup's step.
+// Two waves a SIMD (256 CUs): more bring nothing once each has two steps on their way.  No more than
+// there can be steps.
 DecodePlan plan_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   DecodePlan p;
   const int64_t columns = (int64_t)b.max_rows * (a.q_heads / c.kv_heads);
   p.col_tiles = columns <= 16 ? 1 : 2;
+  p.width = (int)(columns < 16 * p.col_tiles ? columns : 16 * p.col_tiles);
   p.col_groups = (int)((columns + 16 * p.col_tiles - 1) / (16 * p.col_tiles));
   const int64_t room = (int64_t)b.table_width * c.page_size;
   int64_t span = a.max_kv < room ? a.max_kv : room;
-  if (a.window > 0 && (int64_t)a.window + b.max_rows + 16 < span) span = (int64_t)a.window + b.max_rows + 16;
-  if (span < 1) span = 1;
+  if (a.causal && a.window > 0 && (int64_t)a.window + b.max_rows < span) span = (int64_t)a.window + b.max_rows;
+  const int64_t steps = (span + 15 + kStep - 1) / kStep;      // a range starts at 16: up to 15 more
   const int64_t units = (int64_t)b.batch * c.kv_heads * p.col_groups;
-  const int64_t steps = (span + kStride - 1) / kStride;
-  int64_t want = (2048 + units - 1) / units;
-  if (want > steps) want = steps;
-  int64_t per = (steps + want - 1) / want;
-  if (per > kMaxRun / kStride) per = kMaxRun / kStride;
-  p.run = (int)per * kStride;
-  p.splits = (int)((span + 15 + p.run - 1) / p.run);          // a range starts at a tile: up to 15 more
+  const int64_t fit = 256 * kWaves * 2;
+  p.split = steps > 1;
+  p.units = units > 0x7fffffff ? 0x7fffffff : (int)units;
+  p.many_parts = steps > 1024 || units < fit / 32;
+  p.waves = (int)(!p.split ? p.units : units * steps < fit ? units * steps : fit);
   return p;
 }
 
@@ -347,18 +469,21 @@ DecodePlan plan_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_at
 
 size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   const DecodePlan p = plan_of(c, b, a);
-  if (p.splits == 1) return 0;
-  return ((size_t)b.rows * a.q_heads * p.splits * (c.head_dim + 4) * 4 + 255) / 256 * 256;
+  return p.split ? parts_offset(p) + ((size_t)p.units + p.waves) * p.width * (c.head_dim + 4) * 4 : 0;
 }
 
 template <int BF16, int DIM>
 static hipError_t launch_dim(const KvAttentionCall& a, const DecodePlan& p, int page_shift, hipStream_t s) {
-  const int64_t blocks = (int64_t)a.b.batch * a.c.kv_heads * p.col_groups * p.splits;
-  const int64_t joins = (a.b.rows * a.a.q_heads + kWaves - 1) / kWaves;
-  if (blocks > 0x7fffffff || joins > 0x7fffffff) return hipErrorInvalidConfiguration;
-  if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1><<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(a, p, page_shift);
-  else kv_decode_kernel<BF16, DIM, 2><<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(a, p, page_shift);
-  if (p.splits > 1) kv_join_kernel<BF16, DIM><<<dim3((uint32_t)joins), dim3(kThreads), 0, s>>>(a, p, page_shift);
+  const int64_t joins = p.many_parts ? a.b.rows * a.a.q_heads : (a.b.rows * a.a.q_heads + kWaves - 1) / kWaves;
+  // all steps count in 32 bits
+  const int64_t steps = ((int64_t)a.b.table_width * a.c.page_size + kStep - 1) / kStep;
+  if (joins > 0x7fffffff || p.units == 0x7fffffff || (steps + 1) * p.units > 0x7fffffff)
+    return hipErrorInvalidConfiguration;
+  const dim3 grid((uint32_t)((p.waves + kWaves - 1) / kWaves)), block(kThreads);
+  if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1><<<grid, block, 0, s>>>(a, p, page_shift);
+  else kv_decode_kernel<BF16, DIM, 2><<<grid, block, 0, s>>>(a, p, page_shift);
+  if (p.split && p.many_parts) kv_join_kernel<BF16, DIM, kThreads><<<dim3((uint32_t)joins), block, 0, s>>>(a, p);
+  else if (p.split) kv_join_kernel<BF16, DIM, 64><<<dim3((uint32_t)joins), block, 0, s>>>(a, p);
   return hipGetLastError();
 }
 

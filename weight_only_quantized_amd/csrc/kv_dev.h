@@ -15,36 +15,37 @@ constexpr float kGrow = 14.0f, kAbove = 6.0f;
 constexpr float kNoTop = -1e30f;          // finite, so that hidden tokens (-inf) never meet -inf
 constexpr float kLog2e = 1.44269504088896f;
 
-// Rows of a sequence in a batch; a sequence whose rows leave the packed tensors has none.
+// Rows of a sequence in a batch; a sequence whose rows leave the packed tensors has none.  Rows and
+// tokens count in 32 bits (at most 2^24 rows and 2^30 tokens of table are taken).
 struct SeqRows {
-  int64_t row0;
-  int rows;          // handled: at most max_rows
-  int64_t length;    // tokens in the cache
-  int64_t before;    // position of row 0
+  int row0;
+  int rows;      // handled: at most max_rows
+  int length;    // tokens in the cache
+  int before;    // position of row 0: negative when there are more rows than tokens
 };
 __device__ __forceinline__ SeqRows sequence_rows(const gptq_kv_batch& b, int seq) {
-  const int64_t r0 = b.cu[seq], r1 = b.cu[seq + 1], n = r1 - r0, length = b.at[seq];
-  const bool good = n > 0 && r0 >= 0 && r1 <= b.rows;
-  return SeqRows{r0, good ? (int)(n < b.max_rows ? n : b.max_rows) : 0, length, length - n};
+  const int r0 = b.cu[seq], r1 = b.cu[seq + 1], at = b.at[seq], length = at > 0 ? at : 0;
+  const bool good = r0 >= 0 && r1 > r0 && r1 <= b.rows;
+  const int n = good ? r1 - r0 : 0;
+  return SeqRows{r0, n < b.max_rows ? n : b.max_rows, length, length - n};
 }
 
 // Tokens past the table's width or the stated largest length are absent.
-__device__ __forceinline__ int64_t key_room(const gptq_kv_batch& b, const gptq_attention& a, int page_shift) {
-  const int64_t room = (int64_t)b.table_width << page_shift;
+__device__ __forceinline__ int key_room(const gptq_kv_batch& b, const gptq_attention& a, int page_shift) {
+  const int room = b.table_width << page_shift;
   return a.max_kv < room ? a.max_kv : room;
 }
 
 // Tokens [begin, end) that row `row` sees; begin <= end.
 struct KeyRange {
-  int64_t begin, end;
+  int begin, end;
 };
-__device__ __forceinline__ KeyRange key_range(const SeqRows& s, int row, const gptq_attention& a, int64_t room) {
-  const int64_t at = s.before + row;
-  int64_t end = s.length < room ? s.length : room;
+__device__ __forceinline__ KeyRange key_range(const SeqRows& s, int row, const gptq_attention& a, int room) {
+  const int at = s.before + row;
+  int end = s.length < room ? s.length : room;
   if (a.causal && at + 1 < end) end = at + 1;
   if (end < 0) end = 0;
-  int64_t begin = a.window > 0 ? at - a.window + 1 : 0;
-  if (begin < 0) begin = 0;
+  int begin = a.window > 0 && at >= a.window ? at - a.window + 1 : 0;
   if (begin > end) begin = end;
   return KeyRange{begin, end};
 }
@@ -57,9 +58,9 @@ struct TilePage {
   float k_scale, v_scale;
 };
 __device__ __forceinline__ TilePage tile_page(const gptq_kv_cache& c, const gptq_kv_batch& b, int seq, int kv_head,
-                                              int64_t pos, bool wanted, int page_shift) {
+                                              int pos, bool wanted, int page_shift) {
   TilePage t{-1, 0.0f, 0.0f};
-  const int64_t j = pos >> page_shift;
+  const int j = pos >> page_shift;
   if (!wanted || pos < 0 || j >= b.table_width) return t;
   const int page = b.page_table[(int64_t)seq * b.table_width + j];
   if (page < 0 || page >= c.num_pages) return t;

@@ -57,10 +57,10 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
   const int64_t nth = slot - slot_edge(a.b, seq, group, kWidth);
   if (nth < 0 || nth * kWidth >= columns) return;
   const int first_col = (int)nth * kWidth;
-  const int64_t room = key_room(a.b, a.a, page_shift);
+  const int room = key_room(a.b, a.a, page_shift);
   const int last_col = first_col + kWidth < columns ? first_col + kWidth - 1 : columns - 1;
   const KeyRange all_first = key_range(s, first_col / group, a.a, room), all_last = key_range(s, last_col / group, a.a, room);
-  const int lo = (int)(all_first.begin & ~(int64_t)15), hi = (int)all_last.end;
+  const int lo = all_first.begin & ~15, hi = all_last.end;
   const int steps = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
 
   // this lane's columns
@@ -74,20 +74,20 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     c = c < columns ? c : columns - 1;
     const int row = c / group, head = kv_head * group + c % group;
     rows[ct] = row;
-    const uint16_t* at = a.q + (s.row0 + row) * a.a.q_stride + head * DIM + half * 8;
+    const uint16_t* at = a.q + (int64_t)(s.row0 + row) * a.a.q_stride + head * DIM + half * 8;
     q_scale[ct] = load_query<BF16, KS>(at, [](int i) { return i * 16; }, q[ct], 32, 0) * (a.a.scale * kLog2e);
     top[ct] = kNoTop;
     total[ct] = 0.0f;
   }
   // tokens that all of the wave's columns see
   const int wave_last = wave_col + 32 * CT <= columns ? wave_col + 32 * CT - 1 : columns - 1;
-  const int inner_lo = (int)key_range(s, wave_last / group, a.a, room).begin;
-  const int inner_hi = (int)key_range(s, (wave_col < columns ? wave_col : columns - 1) / group, a.a, room).end;
+  const int inner_lo = key_range(s, wave_last / group, a.a, room).begin;
+  const int inner_hi = key_range(s, (wave_col < columns ? wave_col : columns - 1) / group, a.a, room).end;
 
   // staging: wave w takes tokens [16 w, 16 w + 16) of each tile; lane u of `pages` holds tokens
   // [16 u, 16 u + 16) of a run of 16 tiles
   auto pages_of = [&](int run) {
-    const int64_t pos = (int64_t)lo + run * 1024 + lane * 16;
+    const int pos = lo + run * 1024 + lane * 16;
     return tile_page(a.c, a.b, seq, kv_head, pos, pos < hi, page_shift);
   };
   TilePage pages = pages_of(0), next_pages = pages_of(1);
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       const KeyRange r = key_range(s, rows[ct], a.a, room);
-      const int begin = (int)r.begin, end = (int)r.end;
+      const int begin = r.begin, end = r.end;
       float m = -__builtin_inff();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     // element e of tile t is row 32 t + 8 (e / 4) + 4 half + e % 4: elements e and e + 8 of all tiles are
     // VB values next to each other
-    uint16_t* to = a.out + (s.row0 + c / group) * a.a.out_stride + (kv_head * group + c % group) * DIM;
+    uint16_t* to = a.out + (int64_t)(s.row0 + c / group) * a.a.out_stride + (kv_head * group + c % group) * DIM;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       uint32_t o[VB / 2];

@@ -37,4 +37,20 @@ __device__ __forceinline__ int find_sequence(int batch, int64_t row, Edge edge) 
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// Sum over a wave, and the sum of a lane and all before it.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int other = __shfl_up(v, d);
+    if (lane >= d) v += other;
+  }
+  return v;
+}
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
 }  // namespace gq
