@@ -62,36 +62,60 @@ __device__ __forceinline__ void each_adapter(int id, int turn, int turns, F f) {
   }
 }
 
+// Memory is read a row by neighbouring lanes, 64 inputs (128 bytes) by eight of them: lanes that each
+// read their own row cost the address unit a cycle a lane.  The products want a row a lane: rows pass
+// through the wave's own LDS, 16-byte piece p of row r stored at p ^ (r & 7), so that eight rows'
+// pieces cover all banks.
+template <int RT, int CT>
+constexpr int kStage = (RT + CT) * 16 * 8;         // 16-byte pieces of a wave's x rows, then A rows
+
 // acc = A_i x over inputs [k0, k1) for CT tiles of 16 rows: ranks 16 r + 4 quad + e of row 16 t + col.
 // Rows and ranks past the last, and inputs past k1, read as 0.
 template <int BF16, int RT, int CT>
-__device__ __forceinline__ void low_product(rsrc_t x_rsrc, rsrc_t a_rsrc, int K, int k0, int k1, int lane,
+__device__ __forceinline__ void low_product(rsrc_t x_rsrc, rsrc_t a_rsrc, int K, int k0, int k1, int lane, u32x4* stage,
                                             f32x4 (&acc)[RT][CT]) {
-  const uint32_t voff = (uint32_t)((lane & 15) * K + (lane >> 4) * 8) * 2;
+  const int col = lane & 15, quad = lane >> 4, piece = lane & 7;
+  const uint32_t voff = (uint32_t)((lane >> 3) * K + piece * 8) * 2, next = (uint32_t)(8 * K) * 2;
+  const int put = (lane >> 3) * 8 + (piece ^ (lane >> 3)), get = col * 8 + (quad ^ (col & 7));
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int t = 0; t < CT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
-  constexpr int kDeep = RT + CT <= 3 ? 8 : RT + CT <= 6 ? 4 : 2;   // 32-value steps whose loads are in flight
-  for (int k = k0; k < k1; k += 32 * kDeep) {
-    u32x4 xs[kDeep][CT], ws[kDeep][RT];
+  constexpr int kDeep = RT + CT <= 3 ? 4 : RT + CT <= 6 ? 2 : 1;   // steps of 64 whose loads are in flight
+  u32x4 xs[kDeep][2 * CT], ws[kDeep][2 * RT];
+  auto load = [&](int d, int k) {
+    const uint32_t at = k + piece * 8 < k1 ? voff + (uint32_t)k * 2 : kOob;
+#pragma unroll
+    for (int n = 0; n < 2 * CT; ++n) xs[d][n] = load_b128(x_rsrc, at + n * next, 0);
+#pragma unroll
+    for (int n = 0; n < 2 * RT; ++n) ws[d][n] = load_b128(a_rsrc, at + n * next, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) load(d, k0 + d * 64);
+  for (int k = k0; k < k1; k += 64 * kDeep)
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
-      const int k_at = k + d * 32;
-      const uint32_t at = k_at < k1 ? voff + (uint32_t)k_at * 2 : kOob;
 #pragma unroll
-      for (int t = 0; t < CT; ++t) xs[d][t] = load_b128(x_rsrc, at + (uint32_t)(t * 16 * K) * 2, 0);
+      for (int n = 0; n < 2 * CT; ++n) stage[put + n * 64] = xs[d][n];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) ws[d][t] = load_b128(a_rsrc, at + (uint32_t)(t * 16 * K) * 2, 0);
+      for (int n = 0; n < 2 * RT; ++n) stage[CT * 128 + put + n * 64] = ws[d][n];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // the wave's LDS accesses stay in order
+      load(d, k + (d + kDeep) * 64);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 xr[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) xr[t] = stage[t * 128 + (get ^ h * 4)];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const u32x4 w = stage[CT * 128 + r * 128 + (get ^ h * 4)];
+#pragma unroll
+          for (int t = 0; t < CT; ++t) acc[r][t] = mfma16<BF16>(w, xr[t], acc[r][t]);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d)
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < CT; ++t) acc[r][t] = mfma16<BF16>(ws[d][r], xs[d][t], acc[r][t]);
-  }
 }
 
 __device__ __forceinline__ rsrc_t adapter_a(const LoraCall& c, int a) {
@@ -103,7 +127,9 @@ __device__ __forceinline__ rsrc_t adapter_a(const LoraCall& c, int a) {
 template <int BF16, int RT>   // rank tiles of 16
 __global__ void __launch_bounds__(kThreads, 2) lora_low_kernel(LoraCall c, LoraPlan p) {
   constexpr int kPitch = RT * 16 + 4;
-  __shared__ __align__(16) float sums[kWaves][16][kPitch];
+  __shared__ u32x4 stage[kWaves][kStage<RT, 1>];
+  float (*const sums)[16][kPitch] = (float (*)[16][kPitch])stage;     // of the waves, in the same place
+  static_assert(sizeof(float) * kWaves * 16 * kPitch <= sizeof(stage), "");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int id = blockIdx.x;
   const int slice = id % p.slices;
@@ -118,12 +144,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_low_kernel(LoraCall c, LoraP
   const rsrc_t x_rsrc = make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2);
   float* part = (float*)c.ws + (int64_t)slice * c.M * rank;
 
-  bool first = true;
   each_adapter(my_id, turn, p.turns, [&](int a) {
     f32x4 acc[RT][1];
-    low_product<BF16>(x_rsrc, adapter_a(c, a), K, k0, k1, lane, acc);
-    if (!first) __syncthreads();                       // the last adapter's sums are read
-    first = false;
+    low_product<BF16>(x_rsrc, adapter_a(c, a), K, k0, k1, lane, stage[wave], acc);
+    __syncthreads();                                   // all waves have read their rows
 #pragma unroll
     for (int r = 0; r < RT; ++r) *(f32x4*)&sums[wave][lane & 15][r * 16 + (lane >> 4) * 4] = acc[r][0];
     __syncthreads();
@@ -135,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_low_kernel(LoraCall c, LoraP
       for (int v = 0; v < kWaves; ++v) s += sums[v][row][r];
       part[(row0 + row) * rank + r] = s;
     }
+    __syncthreads();                                   // the sums are read: rows may come again
   });
 }
 
@@ -142,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_low_kernel(LoraCall c, LoraP
 template <int BF16, int RT>
 __global__ void __launch_bounds__(kThreads, 2) lora_low_rows_kernel(LoraCall c, LoraPlan p) {
   constexpr int CT = kManyRows / 16;
+  __shared__ u32x4 stage[kWaves][kStage<RT, CT>];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int slice = blockIdx.x % p.slices;
   const int64_t row0 = ((int64_t)(blockIdx.x / p.slices) * kWaves + wave) * kManyRows;
@@ -154,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_low_rows_kernel(LoraCall c, 
   float* part = (float*)c.ws + ((int64_t)slice * c.M + row0) * rank;
   each_adapter(my_id, 0, 1, [&](int a) {
     f32x4 acc[RT][CT];
-    low_product<BF16>(x_rsrc, adapter_a(c, a), K, k0, k1, lane, acc);
+    low_product<BF16>(x_rsrc, adapter_a(c, a), K, k0, k1, lane, stage[wave], acc);
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       const int row = t * 16 + (lane & 15);
@@ -233,55 +259,63 @@ __global__ void __launch_bounds__(kThreads) lora_join_kernel(LoraCall c, LoraPla
 }
 
 // out = y + B_i low.  The waves of a workgroup share low (two 16-bit numbers, in LDS) and take 64
-// outputs each of a run of 256.
+// outputs each of a run of 256.  B_i's 64 rows are one piece of memory, y and out 128 bytes of a row for
+// eight lanes: B_i and the products pass through the wave's own LDS between that order and the matrix
+// operands'.
 template <int BF16, int KS, int CT, bool JOINED>   // 32-value steps of the rank, row tiles of 16; low joined
-__global__ void __launch_bounds__(kThreads, KS == 4 ? 2 : 3) lora_up_kernel(LoraCall c, LoraPlan p) {
-  constexpr int kRows = 16 * CT, kPitch = KS * 4 + 1;      // 16-byte chunks of a row: no two of eight rows on a bank
+__global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(LoraCall c, LoraPlan p) {
+  constexpr int kRows = 16 * CT, kPitch = KS * 4 + 1;      // 16-byte pieces of a row: no two of eight rows on a bank
+  constexpr int kTilePitch = 64 + 4;                       // floats of a row of 64 outputs
+  constexpr int kAux = JOINED ? kAuxStream : 0;            // many rows of y and out pass the caches by (61.4 -> 59.4 us)
+  constexpr int kOwn = 64 * kPitch > 16 * kTilePitch / 4 ? 64 * kPitch : 16 * kTilePitch / 4;
   __shared__ __align__(16) u32x4 lows[2][kRows * kPitch];  // value, remainder
   __shared__ float scaled[kRows];                          // the power of two that a row was scaled by
+  __shared__ __align__(16) u32x4 own[kWaves][kOwn];        // a wave's B rows, then its 16 x 64 products
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, quad = lane >> 4;
+  const int col = lane & 15, quad = lane >> 4, piece = lane & 7;
   int id = blockIdx.x;
   const int block_n = id % p.blocks_n;
   id /= p.blocks_n;
   const int turn = id % p.turns;
   const int64_t row0 = (int64_t)(id / p.turns) * kRows;
-  const int N = c.bank.out_features, rank = c.bank.rank;
+  const int N = c.bank.out_features, rank = c.bank.rank, pieces = rank / 8;
   const int my_id = lane_id(c, row0, kRows, lane);
   const int n_first = block_n * p.per_n * 256 + wave * 64;
   const int rows = c.M - row0 < kRows ? (int)(c.M - row0) : kRows;
   const rsrc_t y_rsrc = make_rsrc(c.y + row0 * N, (uint32_t)rows * N * 2);
   const rsrc_t out_rsrc = make_rsrc(c.out + row0 * N, (uint32_t)rows * N * 2);
-  int ids[CT];
+  u32x4* const b_rows = own[wave];
+  float* const tile = (float*)own[wave];
+  // B: this lane's pieces of the 64 rows, in memory's order (past them: zeros into a row's spare piece)
+  int put[KS * 4];
 #pragma unroll
-  for (int t = 0; t < CT; ++t) ids[t] = __shfl(my_id, t * 16 + col);
+  for (int j = 0; j < KS * 4; ++j)
+    put[j] = j < pieces ? (j * 64 + lane) / pieces * kPitch + (j * 64 + lane) % pieces : kPitch - 1;
+  // y and out: rows 16 m + 8 s + lane / 8
+  int ids[CT][2];
+#pragma unroll
+  for (int m = 0; m < CT; ++m)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) ids[m][s] = __shfl(my_id, m * 16 + s * 8 + (lane >> 3));
 
   bool first = true;
   each_adapter(my_id, turn, p.turns, [&](int a) {
     const rsrc_t b_rsrc = make_rsrc((const uint16_t*)c.bank.b + (int64_t)a * N * rank, (uint32_t)N * rank * 2);
-    // a lane's outputs are n0 + 32 h + 8 quad .. + 7: row 4 q + e of tile t is output n0 + 32 (t / 2) + 8 q +
-    // 4 (t % 2) + e, so that four lanes read and write 64 bytes of a row at once (past N, and in rows of
-    // other adapters: past the resource, read as 0 and not written)
-    u32x4 w[4][KS], in[CT][2];
+    // past N, and in rows of other adapters: past the resource, read as 0 and not written
+    u32x4 b_in[KS * 4], in[CT][2];
     uint32_t at[CT][2];
     auto load = [&](int n0) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t of = (uint32_t)((t >> 1) * 32 + (col >> 2) * 8 + (t & 1) * 4 + (col & 3)) * rank * 2;
+      for (int j = 0; j < KS * 4; ++j)
+        b_in[j] = load_b128(b_rsrc, j < pieces ? (uint32_t)(j * 64 + lane) * 16 : kOob, (uint32_t)n0 * rank * 2);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const int r = k * 32 + quad * 8;
-          w[t][k] = load_b128(b_rsrc, r < rank ? of + r * 2 : kOob, (uint32_t)n0 * rank * 2);
+      for (int m = 0; m < CT; ++m)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          at[m][s] = ids[m][s] == a && n0 + piece * 8 < N
+                         ? (uint32_t)((m * 16 + s * 8 + (lane >> 3)) * N + n0 + piece * 8) * 2 : kOob;
+          in[m][s] = __builtin_amdgcn_raw_buffer_load_b128(y_rsrc, at[m][s], 0, kAux);
         }
-      }
-#pragma unroll
-      for (int m = 0; m < CT; ++m) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          at[m][h] = ids[m] == a && n0 + h * 32 < N ? (uint32_t)((m * 16 + col) * N + n0 + h * 32 + quad * 8) * 2 : kOob;
-          in[m][h] = load_b128(y_rsrc, at[m][h], 0);
-        }
-      }
       __builtin_amdgcn_sched_barrier(0);
     };
     if (n_first < N) load(n_first);                    // on its way while low is added up
@@ -323,17 +357,28 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 2 : 3) lora_up_kernel(Lora
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const int at = (t * 16 + col) * kPitch + k * 4 + quad;
-          split8<BF16>(low[k], down, &lows[0][at], &lows[1][at]);
+          const int to = (t * 16 + col) * kPitch + k * 4 + quad;
+          split8<BF16>(low[k], down, &lows[0][to], &lows[1][to]);
         }
       }
     }
     __syncthreads();
-    float back[CT];
-#pragma unroll
-    for (int m = 0; m < CT; ++m) back[m] = BF16 ? 1.0f : scaled[m * 16 + col];
 
     for (int i = 0; i < p.per_n && n_first + i * 256 < N; ++i) {
+#pragma unroll
+      for (int j = 0; j < KS * 4; ++j)
+        b_rows[put[j]] = b_in[j];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // the wave's LDS accesses stay in order
+      u32x4 w[4][KS];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          w[t][k] = b_rows[(t * 16 + col) * kPitch + k * 4 + quad];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[t][k][e] = k * 4 + quad < pieces ? w[t][k][e] : 0u;
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int m = 0; m < CT; ++m) {
         f32x4 acc[4];
@@ -347,18 +392,25 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 2 : 3) lora_up_kernel(Lora
 #pragma unroll
             for (int t = 0; t < 4; ++t) acc[t] = mfma16<BF16>(w[t][k], low, acc[t]);
           }
+        const float back = BF16 ? 1.0f : scaled[m * 16 + col];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int t = 0; t < 4; ++t) *(f32x4*)(tile + col * kTilePitch + t * 16 + quad * 4) = BF16 ? acc[t] : acc[t] * back;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const float* d = tile + (s * 8 + (lane >> 3)) * kTilePitch + piece * 8;
+          const f32x4 d0 = *(const f32x4*)d, d1 = *(const f32x4*)(d + 4);
           u32x4 o;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const f32x4& v = acc[2 * h + (e >> 1)];
-            const uint32_t y2 = in[m][h][e];
-            o[e] = (uint32_t)from_f32<BF16>(__builtin_fmaf(v[2 * (e & 1)], back[m], to_f32<BF16>((uint16_t)y2))) |
-                   (uint32_t)from_f32<BF16>(__builtin_fmaf(v[2 * (e & 1) + 1], back[m], to_f32<BF16>((uint16_t)(y2 >> 16)))) << 16;
+            const f32x4& v = e < 2 ? d0 : d1;
+            const uint32_t y2 = in[m][s][e];
+            o[e] = (uint32_t)from_f32<BF16>(to_f32<BF16>((uint16_t)y2) + v[2 * (e & 1)]) |
+                   (uint32_t)from_f32<BF16>(to_f32<BF16>((uint16_t)(y2 >> 16)) + v[2 * (e & 1) + 1]) << 16;
           }
-          __builtin_amdgcn_raw_buffer_store_b128(o, out_rsrc, at[m][h], 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(o, out_rsrc, at[m][s], 0, kAux);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
       if (i + 1 < p.per_n && n_first + (i + 1) * 256 < N) load(n_first + (i + 1) * 256);
     }
@@ -366,16 +418,17 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 2 : 3) lora_up_kernel(Lora
   // rows without an adapter
   if (turn != 0 || c.out == c.y) return;
 #pragma unroll
-  for (int m = 0; m < CT; ++m) {
-    const int64_t row = row0 + m * 16 + col;
-    if (ids[m] >= 0 || row >= c.M) continue;
-    for (int i = 0; i < p.per_n; ++i) {
-      const int n = n_first + i * 256 + quad * 16;
-      if (n >= N) break;
-      *(u32x4*)(c.out + row * N + n) = *(const u32x4*)(c.y + row * N + n);
-      *(u32x4*)(c.out + row * N + n + 8) = *(const u32x4*)(c.y + row * N + n + 8);
+  for (int m = 0; m < CT; ++m)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int64_t row = row0 + m * 16 + s * 8 + (lane >> 3);
+      if (ids[m][s] >= 0 || row >= c.M) continue;
+      for (int i = 0; i < p.per_n; ++i) {
+        const int n = n_first + i * 256 + piece * 8;
+        if (n >= N) break;
+        *(u32x4*)(c.out + row * N + n) = *(const u32x4*)(c.y + row * N + n);
+      }
     }
-  }
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -391,7 +444,7 @@ LoraPlan plan_of(const gptq_lora_bank& bank, int64_t M) {
   p.turns = (int)turns;
   // K: enough workgroups to fill the card, slices of at least 64 values a wave
   const int64_t units = p.low_tiles * turns, step = p.few ? 64 * kWaves : 64, steps = div_up(bank.in_features, step);
-  int64_t slices = div_up(512, units);
+  int64_t slices = div_up(256, units);
   if (slices > 16) slices = 16;
   if (slices > steps) slices = steps;
   p.slice_k = (int)(div_up(steps, slices) * step);
