@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
   constexpr int kKeyPitch = DIM / 8 + 1, kValuePitch = kTile / 8 + 1;
   __shared__ __align__(16) u32x4 keys[2][kTile * kKeyPitch];
   __shared__ __align__(16) u32x4 values[2][DIM * kValuePitch];
+  __shared__ float4 unused[64];           // where lanes write that have nothing to write (a branch would cut the step)
   __shared__ __align__(16) float scales[4][4][4];       // [tile & 3][16 tokens][key scale, log2 value scale, inverse]
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -91,8 +92,11 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     return tile_page(a.c, a.b, seq, kv_head, pos, pos < hi, page_shift);
   };
   TilePage pages = pages_of(0), next_pages = pages_of(1);
-  const int key_row = lane & 15, key_piece = lane >> 4;
-  const uint32_t k_off = key_row * DIM + key_piece * 16;
+  // keys: a row by neighbouring lanes (lanes that each read their own row cost the address unit a
+  // cycle a lane); the piece of 16 codes in k_codes[p] is of row key_row + p * 1024 / DIM
+  constexpr int kPieces = DIM / 16;
+  const int key_row = lane / kPieces, key_piece = lane % kPieces;
+  const uint32_t k_off = lane * 16;
   const int v_quad = (lane >> 5 & 1) | (lane >> 3 & 1) << 1;          // tokens 4 v_quad .. + 3 of the 16
   const int v_group = (lane & 7) | (lane >> 4 & 1) << 3;              // values VB v_group .. + VB - 1
   const uint32_t v_off = v_quad * 4 * DIM + v_group * VB;
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     st_v = lane_f32(pages.v_scale, u);
     const int8_t* kb = a.c.k_codes + k_base;
 #pragma unroll
-    for (int p = 0; p < KL; ++p) k_codes[p] = *(const u32x4*)(kb + k_off + p * 64);
+    for (int p = 0; p < KL; ++p) k_codes[p] = *(const u32x4*)(kb + k_off + p * 1024);
   };
   auto load_values = [&](uint64_t base) {
     const int8_t* vb = a.c.v_codes + base;
@@ -131,10 +135,11 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
   };
   auto store_scales = [&](int j) {        // of the tile in k_codes
     const float log = scale_log(st_v);
-    if (lane == 0) *(float4*)scales[j & 3][wave] = make_float4(st_k, log, scale_inv(log), 0.0f);
+    float4* to = lane == 0 ? (float4*)scales[j & 3][wave] : &unused[lane];
+    *to = make_float4(st_k, log, scale_inv(log), 0.0f);
   };
   auto store_key = [&](int j, int p) {
-    u32x4* to = keys[j & 1] + (wave * 16 + key_row) * kKeyPitch + (key_piece + 4 * p) * 2;
+    u32x4* to = keys[j & 1] + (wave * 16 + key_row + p * (1024 / DIM)) * kKeyPitch + key_piece * 2;
     to[0] = codes_f16(k_codes[p][0], k_codes[p][1]);
     to[1] = codes_f16(k_codes[p][2], k_codes[p][3]);
   };
@@ -241,15 +246,14 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
         for (int k = 0; k < kPer; ++k) {
           const int e = m * kPer % 8 + k;
           const float p = __builtin_amdgcn_exp2f(x[ct][u >> 1][(u & 1) * 8 + e]);
-          total[ct] = __builtin_fmaf(p, inv, total[ct]);
+          total[ct] = __builtin_fmaf(p, inv, total[ct]);   // in 32 bits: small against the top may be large here
           w[ct][u][e] = (_Float16)p;
         }
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) asm volatile("" : "+v"(total[ct]));   // here, not after the step
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (kMore) {
-      store_scales(i + 2);
-      most = -__builtin_inff();
-    }
+    if constexpr (kMore) most = -__builtin_inff();
 #pragma unroll
     for (int m = 0; m < kAhead; ++m) ring[m] = value_at(i, m);
     constexpr int kOut = 4 * DT, kPerOut = 32 / kOut;
@@ -281,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (kMore) store_scales(i + 3);
   };
 
   if (steps > 0) {
@@ -297,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
 #pragma unroll
     for (int p = 0; p < KL; ++p) store_key(1, p);
     load_keys(2);
+    store_scales(2);
     __syncthreads();
     score(0);
     most = __builtin_inff();               // the first tile always settles
