@@ -155,6 +155,27 @@ def test_attention_random_shapes(seed):
            scale=None if seed % 3 else 0.3)
 
 
+@pytest.mark.parametrize("case", [(4200, 0, 32, 1, 16, 0), (3000, 1500, 48, 3, 128, 0), (4500, 77, 32, 2, 32, 700)],
+                         ids=["prompt", "chunk", "window"])
+def test_long_prompts(case):
+    """Over 131072 (row, head) columns; sampled rows against the oracle, each as a call of its own."""
+    import torch
+    rows, start, hq, hkv, page, window = case
+    say("long prompt", case)
+    pool = Pool([rows + start], page, hkv, 128, seed=rows)
+    q = torch.empty((rows, hq, 128), dtype=torch.bfloat16, device="cuda")
+    q.normal_(0, 1.5)
+    out = pool.cache().attention(q, dev(pool.table), dev(np.asarray([rows + start], np.int32)), dev(offsets([rows])),
+                                 max_q=rows, window=window)
+    pick = np.unique(np.concatenate([[0, 1, 63, 64, 65, rows - 1], np.random.default_rng(1).integers(0, rows, 18)]))
+    some = Pool([], page, hkv, 128, seed=0)
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
+        setattr(some, name, getattr(pool, name))
+    some.table = np.repeat(pool.table, len(pick), 0)
+    check_attention(host(out[pick]), host(q[pick]), some, (pick + start + 1).astype(np.int32),
+                    np.arange(len(pick) + 1), "bf16", 128 ** -0.5, window=window)
+
+
 @pytest.mark.parametrize("ns", [[1, 1, 1], [40, 3, 90]], ids=["tokens", "rows"])
 def test_absent_pages_and_unused_memory(ns):
     """Pages missing in the middle are not seen; codes and scales that no visible token owns (unused

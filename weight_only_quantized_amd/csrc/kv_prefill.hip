@@ -4,15 +4,15 @@
 // only when a weight would pass 2^14, the value scale rides in the exponent, operands are float16
 // (codes and queries exact, weights rounded once to 11 bits), sums float32.
 //
-// What bounds it: the matrix cores, and the vector work beside them (a weight costs a fused
-// multiply-add, a maximum, an exponential, a sum and a conversion).  One workgroup takes 128 CT
-// (row, head) columns of one sequence and kv head, the heads that share keys side by side, so one
-// conversion of a tile's codes serves them all; each of its four waves holds 32 CT columns with their
-// queries and outputs in registers (v_mfma_f32_32x32x16_f16, rows = tokens or output values, columns
-// = queries, so a weight never leaves its lane).  A step takes 64 tokens: the waves turn 16 of
-// them each into float16 and put them into LDS, keys two steps ahead and values one, while the
-// products of the next tile's scores run under this tile's exponentials and the products with the
-// values under the next tile's exponents.  One barrier a step.
+// What bounds it: instruction issue, the matrix cores' and the vector units' together (a weight costs
+// a fused multiply-add, a maximum, an exponential, a sum and a conversion; a code four operations to
+// become float16).  One workgroup takes 32 (row, head) columns a wave of one sequence and kv head, the
+// heads that share keys side by side, so one conversion of a tile's codes serves them all; each
+// wave holds its columns' queries and outputs in registers (v_mfma_f32_32x32x16_f16, rows = tokens or
+// output values, columns = queries, so a weight never leaves its lane).  A step takes 64 tokens:
+// the waves turn their shares into float16 and put them into LDS, keys two steps ahead and values
+// one, while the products of the next tile's scores run under this tile's exponentials and the
+// products with the values under the next tile's exponents.  One barrier a step.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -22,7 +22,6 @@
 namespace gq {
 namespace {
 
-constexpr int kThreads = 256, kWaves = 4;
 constexpr int kTile = 64;                 // tokens of a step
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -31,15 +30,18 @@ __device__ __forceinline__ int64_t slot_edge(const gptq_kv_batch& b, int seq, in
   return (int64_t)b.cu[seq] * group / width + seq;
 }
 
-template <int BF16, int DIM, int CT>
-__global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(KvAttentionCall a, int slots, int page_shift) {
+template <int BF16, int DIM, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCall a, int slots, int page_shift) {
   constexpr int KS = DIM / 16;            // 16-value steps of a score
   constexpr int DT = DIM / 32;            // 32-value tiles of an output
-  constexpr int KL = DIM / 64;            // 16-byte loads of a lane for 16 tokens' keys
-  constexpr int VB = DIM / 16;            // bytes of a value row a lane stages
-  constexpr int VW = VB / 4;
+  constexpr int kWidth = 32 * WAVES;      // columns
+  // a wave's share of a tile: kShare tokens' keys in KL 16-byte loads a lane; the values of the quads of
+  // tokens that it takes, VB bytes of four rows a lane
+  constexpr int kShare = kTile / WAVES, KL = kShare * DIM / 1024;
+  constexpr int VB = DIM * kShare / 256, VW = VB / 4, kGroups = DIM / VB;
+  static_assert(KL >= 1 && VW >= 1 && kGroups * VB == DIM, "");
   // LDS rows of 16-byte chunks, one chunk longer than their data: eight rows' chunks cover all banks.
-  // keys: token by value; values: VB-th part by token, row 16 e + v holds value VB v + e
+  // keys: token by value; values: value by token, row kGroups e + v holds value VB v + e
   constexpr int kKeyPitch = DIM / 8 + 1, kValuePitch = kTile / 8 + 1;
   __shared__ __align__(16) u32x4 keys[2][kTile * kKeyPitch];
   __shared__ __align__(16) u32x4 values[2][DIM * kValuePitch];
@@ -51,7 +53,6 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
   const int kv_head = blockIdx.x % a.c.kv_heads;
   const int slot = slots - 1 - (int)(blockIdx.x / a.c.kv_heads);       // later rows see more: first
   const int group = a.a.q_heads / a.c.kv_heads;
-  constexpr int kWidth = 32 * CT * kWaves;
   const int seq = find_sequence(a.b.batch, slot, [&](int i) { return slot_edge(a.b, i, group, kWidth); });
   const SeqRows s = sequence_rows(a.b, seq);
   const int columns = s.rows * group;
@@ -60,33 +61,28 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
   const int first_col = (int)nth * kWidth;
   const int room = key_room(a.b, a.a, page_shift);
   const int last_col = first_col + kWidth < columns ? first_col + kWidth - 1 : columns - 1;
-  const KeyRange all_first = key_range(s, first_col / group, a.a, room), all_last = key_range(s, last_col / group, a.a, room);
-  const int lo = all_first.begin & ~15, hi = all_last.end;
+  const int lo = key_range(s, first_col / group, a.a, room).begin & ~15;
+  const int hi = key_range(s, last_col / group, a.a, room).end;
   const int steps = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
 
-  // this lane's columns
-  int rows[CT];
-  float q_scale[CT], top[CT], total[CT];
-  f16x8 q[CT][KS];
-  const int wave_col = first_col + wave * 32 * CT;
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    int c = wave_col + ct * 32 + col32;
-    c = c < columns ? c : columns - 1;
-    const int row = c / group, head = kv_head * group + c % group;
-    rows[ct] = row;
-    const uint16_t* at = a.q + (int64_t)(s.row0 + row) * a.a.q_stride + head * DIM + half * 8;
-    q_scale[ct] = load_query<BF16, KS>(at, [](int i) { return i * 16; }, q[ct], 32, 0) * (a.a.scale * kLog2e);
-    top[ct] = kNoTop;
-    total[ct] = 0.0f;
-  }
+  // this lane's column (columns past the last repeat it)
+  const int wave_col = first_col + wave * 32;
+  const int col = wave_col + col32 < columns ? wave_col + col32 : columns - 1;
+  const int row = col / group, head = kv_head * group + col % group;
+  f16x8 q[KS];
+  const float q_scale =
+      load_query<BF16, KS>(a.q + (int64_t)(s.row0 + row) * a.a.q_stride + head * DIM + half * 8,
+                           [](int i) { return i * 16; }, q, 32, 0) * (a.a.scale * kLog2e);
+  float top = kNoTop, total = 0.0f;
   // tokens that all of the wave's columns see
-  const int wave_last = wave_col + 32 * CT <= columns ? wave_col + 32 * CT - 1 : columns - 1;
+  const int wave_last = wave_col + 32 <= columns ? wave_col + 31 : columns - 1;
   const int inner_lo = key_range(s, wave_last / group, a.a, room).begin;
   const int inner_hi = key_range(s, (wave_col < columns ? wave_col : columns - 1) / group, a.a, room).end;
 
-  // staging: wave w takes tokens [16 w, 16 w + 16) of each tile; lane u of `pages` holds tokens
+  // staging: a wave's tokens lie in the 16 from 16 * part on; lane u of `pages` holds tokens
   // [16 u, 16 u + 16) of a run of 16 tiles
+  constexpr int kSplit = 16 / kShare;     // waves that share 16 tokens
+  const int part = wave / kSplit, in_part = wave % kSplit;
   auto pages_of = [&](int run) {
     const int pos = lo + run * 1024 + lane * 16;
     return tile_page(a.c, a.b, seq, kv_head, pos, pos < hi, page_shift);
@@ -95,10 +91,12 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
   // keys: a row by neighbouring lanes (lanes that each read their own row cost the address unit a
   // cycle a lane); the piece of 16 codes in k_codes[p] is of row key_row + p * 1024 / DIM
   constexpr int kPieces = DIM / 16;
-  const int key_row = lane / kPieces, key_piece = lane % kPieces;
-  const uint32_t k_off = lane * 16;
-  const int v_quad = (lane >> 5 & 1) | (lane >> 3 & 1) << 1;          // tokens 4 v_quad .. + 3 of the 16
-  const int v_group = (lane & 7) | (lane >> 4 & 1) << 3;              // values VB v_group .. + VB - 1
+  const int key_row = in_part * kShare + lane / kPieces, key_piece = lane % kPieces;
+  const uint32_t k_off = in_part * kShare * DIM + lane * 16;
+  // values: tokens 4 v_quad .. + 3 of the 16 (quads q and q + 2 are halves of a chunk: sixteen lanes that
+  // write together take eight groups of both), values VB v_group .. + VB - 1
+  const int v_quad = kSplit == 1 ? (lane >> 5 & 1) | (lane >> 3 & 1) << 1 : in_part | (lane >> 3 & 1) << 1;
+  const int v_group = kSplit == 1 ? (lane & 7) | (lane >> 4 & 1) << 3 : (lane & 7) | (lane >> 4 & 3) << 3;
   const uint32_t v_off = v_quad * 4 * DIM + v_group * VB;
   u32x4 k_codes[KL];
   uint32_t v_codes[4][VW];
@@ -111,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     }
   };
   auto load_keys = [&](int j) {
-    const int u = (j & 15) * 4 + wave;
-    k_base = tile_base(a.c, __builtin_amdgcn_readlane(pages.page, u), kv_head, lo + j * kTile + wave * 16, page_shift);
+    const int u = (j & 15) * 4 + part;
+    k_base = tile_base(a.c, __builtin_amdgcn_readlane(pages.page, u), kv_head, lo + j * kTile + part * 16, page_shift);
     st_k = lane_f32(pages.k_scale, u);
     st_v = lane_f32(pages.v_scale, u);
     const int8_t* kb = a.c.k_codes + k_base;
@@ -135,25 +133,23 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
   };
   auto store_scales = [&](int j) {        // of the tile in k_codes
     const float log = scale_log(st_v);
-    float4* to = lane == 0 ? (float4*)scales[j & 3][wave] : &unused[lane];
+    float4* to = lane == 0 && in_part == 0 ? (float4*)scales[j & 3][part] : &unused[lane];
     *to = make_float4(st_k, log, scale_inv(log), 0.0f);
   };
   auto store_key = [&](int j, int p) {
-    u32x4* to = keys[j & 1] + (wave * 16 + key_row + p * (1024 / DIM)) * kKeyPitch + key_piece * 2;
+    u32x4* to = keys[j & 1] + (part * 16 + key_row + p * (1024 / DIM)) * kKeyPitch + key_piece * 2;
     to[0] = codes_f16(k_codes[p][0], k_codes[p][1]);
     to[1] = codes_f16(k_codes[p][2], k_codes[p][3]);
   };
-  const int v_chunk = 2 * wave + (v_quad & 1);
+  const int v_chunk = 2 * part + (v_quad & 1);
   auto store_value = [&](int j, int e) {
     const uint2 w{pair_f16(v_codes[0][e >> 2], v_codes[1][e >> 2], e & 3), pair_f16(v_codes[2][e >> 2], v_codes[3][e >> 2], e & 3)};
-    ((uint2*)(values[j & 1] + (16 * e + v_group) * kValuePitch + v_chunk))[v_quad >> 1] = w;
+    ((uint2*)(values[j & 1] + (kGroups * e + v_group) * kValuePitch + v_chunk))[v_quad >> 1] = w;
   };
 
-  f32x16 acc[CT][DT], dot[2][CT];
+  f32x16 acc[DT], dot[2];
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-    for (int t = 0; t < DT; ++t) acc[ct][t] = f32x16{};
+  for (int t = 0; t < DT; ++t) acc[t] = f32x16{};
 
   // operand of micro-step m of a tile's scores (tokens 32 (m / KS) .., values 16 (m % KS) ..); element e
   // of the result is token 32 (m / KS) + 8 (e / 4) + 4 half + e % 4
@@ -165,21 +161,19 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     return values[j & 1][(m / 4 * 32 + col32) * kValuePitch + 2 * (m % 4) + half];
   };
   auto score_step = [&](int m, u32x4 key) {
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-      dot[m / KS][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, key), q[ct][m % KS],
-                                                               m % KS ? dot[m / KS][ct] : f32x16{}, 0, 0, 0);
+    dot[m / KS] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, key), q[m % KS],
+                                                         m % KS ? dot[m / KS] : f32x16{}, 0, 0, 0);
   };
   auto score = [&](int j) {
 #pragma unroll
     for (int m = 0; m < 2 * KS; ++m) score_step(m, key_at(j, m));
   };
-  float x[CT][2][16];
-  float by[CT], plus[CT], most;
+  float x[2][16];
+  float by, plus, most;
   // x = exponents of elements [8 u, 8 u + 8) of tile j relative to `from`
-  auto exponent_scale = [&](int j, int u, int ct, float from) {
-    by[ct] = q_scale[ct] * scales[j & 3][u][0];
-    plus[ct] = scales[j & 3][u][1] - from;
+  auto exponent_scale = [&](int j, int u, float from) {
+    by = q_scale * scales[j & 3][u][0];
+    plus = scales[j & 3][u][1] - from;
   };
   // settles x of tile j: hidden tokens, and a top that has to move (the scores are taken again)
   auto settle = [&](int j) {
@@ -187,35 +181,31 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     const bool edge = pos < inner_lo || pos + kTile > inner_hi;
     if (!edge && !__any(most > kGrow)) return;
     score(j);
+    const KeyRange r = key_range(s, row, a.a, room);
+    float m = -__builtin_inff();
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const KeyRange r = key_range(s, rows[ct], a.a, room);
-      const int begin = r.begin, end = r.end;
-      float m = -__builtin_inff();
+    for (int u = 0; u < 4; ++u) {
+      exponent_scale(j, u, 0.0f);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        exponent_scale(j, u, ct, 0.0f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int p = pos + u * 16 + (e >> 2) * 8 + half * 4 + (e & 3);
-          const float v = __builtin_fmaf(dot[u >> 1][ct][(u & 1) * 8 + e], by[ct], plus[ct]);
-          x[ct][u >> 1][(u & 1) * 8 + e] = p < begin || p >= end ? -__builtin_inff() : v;
-          m = __builtin_fmaxf(m, x[ct][u >> 1][(u & 1) * 8 + e]);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const int p = pos + u * 16 + (e >> 2) * 8 + half * 4 + (e & 3);
+        const float v = __builtin_fmaf(dot[u >> 1][(u & 1) * 8 + e], by, plus);
+        x[u >> 1][(u & 1) * 8 + e] = p < r.begin || p >= r.end ? -__builtin_inff() : v;
+        m = __builtin_fmaxf(m, x[u >> 1][(u & 1) * 8 + e]);
       }
-      m = __builtin_fmaxf(m, __shfl_xor(m, 32));                     // the two lanes of a column agree
-      if (m - top[ct] > kGrow) {
-        const float moved = m - kAbove, keep = __builtin_amdgcn_exp2f(top[ct] - moved);
-        top[ct] = moved;
-        total[ct] *= keep;
-#pragma unroll
-        for (int t = 0; t < DT; ++t) acc[ct][t] *= keep;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[ct][h][e] -= top[ct];
     }
+    m = __builtin_fmaxf(m, __shfl_xor(m, 32));                       // the two lanes of a column agree
+    if (m - top > kGrow) {
+      const float moved = m - kAbove, keep = __builtin_amdgcn_exp2f(top - moved);
+      top = moved;
+      total *= keep;
+#pragma unroll
+      for (int t = 0; t < DT; ++t) acc[t] *= keep;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[h][e] -= top;
   };
 
   // Step i: LDS holds keys of tile i + 1 and values of tile i, registers the keys of tile i + 2 and the
@@ -225,12 +215,12 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     constexpr bool kMore = decltype(more)::value;
     constexpr int kAhead = 3;
     u32x4 ring[kAhead];
-    f16x8 w[CT][4];
+    f16x8 w[4];
     if constexpr (kMore) {
 #pragma unroll
       for (int m = 0; m < kAhead; ++m) ring[m] = key_at(i + 1, m);
     }
-    constexpr int kPer = 32 / (2 * KS);           // weights of a column tile in a micro-step
+    constexpr int kPer = 32 / (2 * KS);           // weights of a micro-step
     float inv = 0.0f;
 #pragma unroll
     for (int m = 0; m < 2 * KS; ++m) {
@@ -241,16 +231,13 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
       const int u = m * kPer / 8;
       if (m * kPer % 8 == 0) inv = scales[i & 3][u][2];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int e = m * kPer % 8 + k;
-          const float p = __builtin_amdgcn_exp2f(x[ct][u >> 1][(u & 1) * 8 + e]);
-          total[ct] = __builtin_fmaf(p, inv, total[ct]);   // in 32 bits: small against the top may be large here
-          w[ct][u][e] = (_Float16)p;
-        }
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) asm volatile("" : "+v"(total[ct]));   // here, not after the step
+      for (int k = 0; k < kPer; ++k) {
+        const int e = m * kPer % 8 + k;
+        const float p = __builtin_amdgcn_exp2f(x[u >> 1][(u & 1) * 8 + e]);
+        total = __builtin_fmaf(p, inv, total);     // in 32 bits: small against the top may be large here
+        w[u][e] = (_Float16)p;
+      }
+      asm volatile("" : "+v"(total));              // here, not after the step
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (kMore) most = -__builtin_inff();
@@ -259,22 +246,17 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     constexpr int kOut = 4 * DT, kPerOut = 32 / kOut;
 #pragma unroll
     for (int m = 0; m < kOut; ++m) {
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        acc[ct][m / 4] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, ring[m % kAhead]), w[ct][m % 4],
-                                                                acc[ct][m / 4], 0, 0, 0);
+      acc[m / 4] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, ring[m % kAhead]), w[m % 4], acc[m / 4],
+                                                          0, 0, 0);
       if (m + kAhead < kOut) ring[m % kAhead] = value_at(i, m + kAhead);
       if constexpr (kMore) {
         const int u = m * kPerOut / 8;
+        if (m * kPerOut % 8 == 0) exponent_scale(i + 1, u, top);
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          if (m * kPerOut % 8 == 0) exponent_scale(i + 1, u, ct, top[ct]);
-#pragma unroll
-          for (int k = 0; k < kPerOut; ++k) {
-            const int e = (u & 1) * 8 + m * kPerOut % 8 + k;
-            x[ct][u >> 1][e] = __builtin_fmaf(dot[u >> 1][ct][e], by[ct], plus[ct]);
-            most = __builtin_fmaxf(most, x[ct][u >> 1][e]);
-          }
+        for (int k = 0; k < kPerOut; ++k) {
+          const int e = (u & 1) * 8 + m * kPerOut % 8 + k;
+          x[u >> 1][e] = __builtin_fmaf(dot[u >> 1][e], by, plus);
+          most = __builtin_fmaxf(most, x[u >> 1][e]);
         }
         if (m < VB) store_value(i + 1, m);
         else if (m < VB + KL) store_key(i + 2, m - VB);
@@ -319,48 +301,43 @@ __global__ void __launch_bounds__(kThreads, CT == 1 ? 2 : 1) kv_prefill_kernel(K
     step(steps - 1, std::false_type{});
   }
 
+  const float sum = total + __shfl_xor(total, 32);
+  if (wave_col + col32 >= columns) return;
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+  uint16_t* to = a.out + (int64_t)(s.row0 + row) * a.a.out_stride + head * DIM;
+  // element e of tile t is LDS row 32 t + 8 (e / 4) + 4 half + e % 4, which is value VB (row % kGroups) +
+  // row / kGroups: of one e the tiles (and, with 16 groups, element e + 8) are values next to each other
+  constexpr int kBoth = kGroups == 16 ? 2 : 1;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int c = wave_col + ct * 32 + col32;
-    const float sum = total[ct] + __shfl_xor(total[ct], 32);
-    if (c >= columns) continue;
-    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    // element e of tile t is row 32 t + 8 (e / 4) + 4 half + e % 4: elements e and e + 8 of all tiles are
-    // VB values next to each other
-    uint16_t* to = a.out + (int64_t)(s.row0 + c / group) * a.a.out_stride + (kv_head * group + c % group) * DIM;
+  for (int e = 0; e < 16 / kBoth; ++e) {
+    uint32_t o[VB / 2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t o[VB / 2];
-#pragma unroll
-      for (int t = 0; t < DT; ++t)
-        o[t] = (uint32_t)from_f32<BF16>(acc[ct][t][e] * inv) | (uint32_t)from_f32<BF16>(acc[ct][t][e + 8] * inv) << 16;
-      __builtin_memcpy(__builtin_assume_aligned(to + VB * (8 * (e >> 2) + 4 * half + (e & 3)), VB * 2), o, VB * 2);
+    for (int t = 0; t < VB / 2; ++t) {
+      const float v0 = kBoth == 2 ? acc[t][e] : acc[2 * t % DT][e], v1 = kBoth == 2 ? acc[t % DT][(e + 8) % 16] : acc[(2 * t + 1) % DT][e];
+      o[t] = (uint32_t)from_f32<BF16>(v0 * inv) | (uint32_t)from_f32<BF16>(v1 * inv) << 16;
     }
+    __builtin_memcpy(__builtin_assume_aligned(to + VB * (8 * (e >> 2) + 4 * half + (e & 3)), VB * 2), o, VB * 2);
   }
 }
 
-template <int BF16, int DIM, int CT>
-hipError_t launch_ct(const KvAttentionCall& a, int page_shift, hipStream_t s) {
+template <int BF16, int DIM, int WAVES>
+hipError_t launch_waves(const KvAttentionCall& a, int page_shift, hipStream_t s) {
   const int group = a.a.q_heads / a.c.kv_heads;
-  const int64_t slots = a.b.rows * group / (32 * CT * kWaves) + a.b.batch, blocks = slots * a.c.kv_heads;
+  const int64_t slots = a.b.rows * group / (32 * WAVES) + a.b.batch, blocks = slots * a.c.kv_heads;
   if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-  kv_prefill_kernel<BF16, DIM, CT><<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(a, (int)slots, page_shift);
+  kv_prefill_kernel<BF16, DIM, WAVES><<<dim3((uint32_t)blocks), dim3(64 * WAVES), 0, s>>>(a, (int)slots, page_shift);
   return hipGetLastError();
-}
-
-template <int BF16, int DIM>
-hipError_t launch_dim(const KvAttentionCall& a, int page_shift, hipStream_t s) {
-  const int64_t columns = a.b.rows * a.a.q_heads;
-  return launch_ct<BF16, DIM, 1>(a, page_shift, s);
 }
 
 }  // namespace
 
 hipError_t launch_kv_prefill(const KvAttentionCall& a, hipStream_t s) {
   const int page_shift = __builtin_ctz(a.c.page_size);
-  if (a.c.head_dim == 128)
-    return a.a.dtype == GPTQ_BF16 ? launch_dim<1, 128>(a, page_shift, s) : launch_dim<0, 128>(a, page_shift, s);
-  return a.a.dtype == GPTQ_BF16 ? launch_dim<1, 64>(a, page_shift, s) : launch_dim<0, 64>(a, page_shift, s);
+  const bool bf16 = a.a.dtype == GPTQ_BF16;
+  if (a.c.head_dim == 64) return bf16 ? launch_waves<1, 64, 4>(a, page_shift, s) : launch_waves<0, 64, 4>(a, page_shift, s);
+  if (a.b.rows * a.a.q_heads >= 256 * 512)
+    return bf16 ? launch_waves<1, 128, 8>(a, page_shift, s) : launch_waves<0, 128, 8>(a, page_shift, s);
+  return bf16 ? launch_waves<1, 128, 4>(a, page_shift, s) : launch_waves<0, 128, 4>(a, page_shift, s);
 }
 
 }  // namespace gq
