@@ -385,6 +385,35 @@ def test_append_against_oracle(case, big):
     check_append(pool, plain, starts, cu, host(k), host(v), case)
 
 
+@pytest.mark.parametrize("batch,many", [(65, False), (200, False), (300, True), (70, True)])
+def test_many_sequences(batch, many):
+    """More sequences than a wave has lanes: appended, read back and attended to, some without rows or
+    tokens."""
+    import torch
+    rng = np.random.default_rng(batch)
+    ns = [int(n) for n in (rng.integers(0, 6, batch) if many else rng.integers(0, 2, batch))]
+    starts = [int(s) for s in rng.integers(0, 80, batch)]
+    ns[0], ns[-1] = 1, 1
+    lens = [s + n for s, n in zip(starts, ns)]
+    pool = Pool(lens, 16, 2, 64, seed=batch)
+    cache, cu = pool.cache(), offsets(ns)
+    T, table = int(cu[-1]), dev(pool.table)
+    cos, sin = tables(100, 32)
+    k, v, q = (dev(rng.normal(0, 1, (T, h, 64)), torch.float16) for h in (2, 2, 6))
+    got = cache.append(k, v, table, dev(np.asarray(starts, np.int32)), dev(cu), max_new=max(ns), q=q, cos=dev(cos),
+                       sin=dev(sin))
+    pos = np.concatenate([np.arange(s, s + n) for s, n in zip(starts, ns)])
+    check_append(pool, cache, starts, cu, so.rotate(host(k), cos[pos], sin[pos], False), host(v), batch)
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
+        setattr(pool, name, getattr(cache, name).cpu().numpy())
+    out = cache.attention(got, table, dev(np.asarray(lens, np.int32)), dev(cu), max_q=max(ns))
+    check_attention(host(out), host(got), pool, lens, cu, "f16", 64 ** -0.5)
+    kk, _ = cache.read(table, dev(np.asarray(starts, np.int32)), dev(cu), rows=T, max_rows=max(ns), dtype=torch.float32)
+    want = np.concatenate([so.values(pool.k_codes, pool.k_scale, pool.table, b, s + n)[0][s:] for b, (s, n) in
+                           enumerate(zip(starts, ns))])
+    assert np.array_equal(host(kk), want.astype(np.float32).astype(np.float64))
+
+
 def test_append_again_changes_nothing_and_pages_fill_token_by_token():
     import torch
     pool = Pool([64, 64], 32, 2, 64, seed=51)

@@ -104,6 +104,11 @@ def _row_stride(t, shape):
     return row if one == 1 and (shape[1] == 1 or head == shape[2]) and row >= width and row % 8 == 0 else 0
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape and type (empty_like is the quicker call, but follows t's strides)."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _dense(t):
     """A contiguous 16-byte aligned tensor (copied if it is not)."""
     return t if t.is_contiguous() and not t.data_ptr() & 15 else t.clone(memory_format=torch.contiguous_format)
@@ -186,7 +191,7 @@ class KVCache:
                     raise ValueError("q must have k's rows")
                 heads = q.shape[1]
                 if q_out is None:
-                    q_out, o_stride = torch.empty((rows, heads, dim), dtype=dt, device=self.device), heads * dim
+                    q_out, o_stride = _like(q), heads * dim
                 elif q_out.shape != q.shape or q_out.dtype is not dt or q_out.get_device() != device:
                     raise ValueError("q_out must have q's shape, type and device")
                 else:
@@ -234,7 +239,7 @@ class KVCache:
             rows, heads = q.shape[0], q.shape[1]
             q, q_stride = _packed(q, "q", heads, dim, q.dtype, device)
             if out is None:
-                out, out_stride = torch.empty((rows, heads, dim), dtype=q.dtype, device=self.device), heads * dim
+                out, out_stride = _like(q), heads * dim
             elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != device:
                 raise ValueError("out must have q's shape, type and device")
             else:
@@ -319,7 +324,7 @@ class LoraBank:
         with _Queue(stream, device, x, y, ids, out, workspace, self.a, self.b, self.scale) as ptr:
             x, y = _dense(x), _dense(y)
             if out is None:
-                out = torch.empty((M, self.N), dtype=dt, device=self.device)
+                out = torch.empty_like(y)          # y is dense here
             if workspace is None:
                 size = self._sizes.get(M)
                 if size is None:
