@@ -435,7 +435,8 @@ typedef struct {
  *   overlap anything.  ids int32 [M].
  * Both products accumulate in float32; A_i x[m] is kept to 16 bits or more for the second, and out
  * is rounded once.  A call with the same arguments gives the same bits.
- * workspace: gptq_lora_workspace_size() bytes, 256-byte aligned.  M == 0: GPTQ_OK, nothing launched.
+ * workspace: gptq_lora_workspace_size() bytes (0 when one launch does all), 256-byte aligned.
+ * M == 0: GPTQ_OK, nothing launched.
  * Errors: GPTQ_E_INVALID_ARG, GPTQ_E_SHAPE (K or N, adapters, M > 2^24), GPTQ_E_UNSUPPORTED (rank),
  * GPTQ_E_WORKSPACE, GPTQ_E_DEVICE, GPTQ_E_HIP. */
 gptq_status gptq_lora_workspace_size(const gptq_lora_bank* bank, int64_t M, size_t* bytes);

@@ -155,6 +155,24 @@ def test_attention_random_shapes(seed):
            scale=None if seed % 3 else 0.3)
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_attention_few_rows_long(seed):
+    """A few rows each over thousands of tokens, sequences of very different lengths among them."""
+    rng = np.random.default_rng(500 + seed)
+    batch = int(rng.integers(1, 9))
+    ns = [int(rng.integers(0, 6 if seed % 3 == 0 else 2)) for _ in range(batch)]
+    ns[0] = 1
+    lens = [max(0, n + int(2 ** rng.uniform(0, 12))) for n in ns]
+    lens[0] = [1023, 1024, 1025, 1056, 2047, 2049, 4097][seed % 7]
+    page, dim = int(rng.choice([16, 32, 64, 128, 256])), int(rng.choice([64, 128]))
+    hkv, group = int(rng.integers(1, 12)), int(rng.choice([1, 2, 3, 4, 8]))
+    window = int(rng.choice([0, 0, 1100, 1500]))
+    tag = str(rng.choice(["f16", "bf16"]))
+    say("attention few rows", seed, ns, lens, page, dim, hkv, group, window, tag)
+    pool = Pool(lens, page, hkv, dim, seed=seed)
+    attend(pool, lens, ns, hkv * group, tag, seed=seed, window=window)
+
+
 @pytest.mark.parametrize("case", [(4200, 0, 32, 1, 16, 0), (3000, 1500, 48, 3, 128, 0), (4500, 77, 32, 2, 32, 700)],
                          ids=["prompt", "chunk", "window"])
 def test_long_prompts(case):

@@ -76,6 +76,8 @@ CASES = [
     (33, 4096, 416, 32, 40, "bf16"), (64, 512, 512, 8, 64, "f16"), (65, 544, 1056, 56, 7, "bf16"),
     (130, 256, 320, 104, 2, "f16"), (257, 1056, 288, 16, 5, "bf16"), (500, 128, 96, 64, 9, "f16"),
     (5, 14336, 128, 16, 2, "f16"), (1, 28672, 64, 128, 2, "bf16"),
+    (16, 5120, 480, 32, 16, "f16"), (16, 5152, 480, 24, 16, "bf16"), (9, 5088, 7328, 8, 9, "f16"), (8, 96, 8192, 32, 8, "bf16"),
+    (9, 96, 8192, 32, 9, "f16"), (127, 1024, 96, 32, 30, "bf16"), (128, 1056, 288, 40, 3, "f16"), (129, 1056, 288, 40, 3, "f16"),
 ]
 
 
@@ -97,6 +99,23 @@ def test_ids_outside_the_bank_keep_y(M):
     ids = np.random.default_rng(3).choice([-1, -100, 4, 5, 1 << 30, -(1 << 31)], M)
     bank, x, y, idt, ids = make(M, 256, 192, 16, 4, "bf16", seed=9, ids=ids)
     assert torch.equal(bank.add(y, x, idt), y)
+
+
+@pytest.mark.parametrize("tag", ["f16", "bf16"])
+@pytest.mark.parametrize("M,rank", [(1, 8), (40, 64), (300, 24)])
+def test_infinite_sums_stay_infinite(M, rank, tag):
+    """A row whose A x is infinite (one sign) gives infinities where B's values have one sign, and a row
+    beside it keeps its values."""
+    import torch
+    bank, x, y, idt, ids = make(M, 256, 192, rank, 2, tag, seed=21, ids=np.ones(M))
+    bank.a.abs_().add_(1e-3)
+    bank.b.abs_().add_(1e-3)
+    plain = bank.add(y, x, idt)
+    x[M // 2, 7] = float("inf")
+    got = bank.add(y, x, idt)
+    assert bool((got[M // 2] == float("inf")).all())
+    keep = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(got[keep], plain[keep])
 
 
 def test_in_place_streams_and_equal_bits():

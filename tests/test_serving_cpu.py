@@ -184,12 +184,17 @@ def test_lora_refusals():
     for kw, want in ((dict(x=None), "E_INVALID_ARG"), (dict(ids=None), "E_INVALID_ARG"), (dict(y=FREE + (1 << 20) + 4), "E_INVALID_ARG"),
                      (dict(M=-1), "E_SHAPE"), (dict(M=(1 << 24) + 1), "E_SHAPE"), (dict(out=FREE), "E_INVALID_ARG"),
                      (dict(out=FREE + (1 << 20) + 16), "E_INVALID_ARG"), (dict(out=A), "E_INVALID_ARG"),
-                     (dict(ws=None), "E_WORKSPACE"), (dict(size=0), "E_WORKSPACE"), (dict(ws=FREE + (4 << 20) + 8), "E_WORKSPACE"),
-                     (dict(ws=FREE), "E_INVALID_ARG"), (dict(M=0), "OK")):
+                     (dict(M=0), "OK")):
         assert call(**kw) == want, kw
+    for kw, want in ((dict(ws=None), "E_WORKSPACE"), (dict(size=0), "E_WORKSPACE"), (dict(ws=FREE + (4 << 20) + 8), "E_WORKSPACE"),
+                     (dict(ws=FREE), "E_INVALID_ARG")):
+        assert call(bank(rank=64), **kw) == want, kw
     assert call() in ("E_HIP", "E_DEVICE")
     assert call(out=FREE + (1 << 20)) in ("E_HIP", "E_DEVICE")          # in place
-    assert lib.gptq_lora_workspace_size(ctypes.byref(bank()), 5, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.gptq_lora_workspace_size(ctypes.byref(bank(rank=64)), 5, ctypes.byref(n)) == 0 and n.value > 0
+    # few rows of small adapters: one launch, no workspace
+    assert lib.gptq_lora_workspace_size(ctypes.byref(bank()), 5, ctypes.byref(n)) == 0 and n.value == 0
+    assert call(ws=None, size=0) in ("E_HIP", "E_DEVICE")
     assert lib.gptq_lora_workspace_size(ctypes.byref(bank()), 0, ctypes.byref(n)) == 0 and n.value == 0
     assert lib.gptq_lora_workspace_size(ctypes.byref(bank()), 5, None) == 1
 

@@ -16,7 +16,8 @@
 // Split.  The work is cut into steps of 32 tokens of a unit: up to 32 (row, head) columns of one
 // sequence and kv head.  All units' steps in order are dealt to as many waves as the card holds at
 // once, the same number to each: sequences of any lengths fill it evenly, and no wave waits for
-// another.  Units that cross waves leave unnormalised sums that a second launch joins in order.
+// another.  Units that cross waves leave unnormalised sums that a second launch joins in order.  Few
+// short units go to a workgroup each instead, which joins its waves' sums itself.
 // Products are computed as rows = tokens, columns = queries (v_mfma_f32_16x16x32_f16), which leaves
 // each lane with the weights of just those tokens whose values it holds as the second product's
 // operand: codes go from memory to the matrix cores without LDS.
@@ -31,6 +32,7 @@ namespace gq {
 namespace {
 
 constexpr int kThreads = 256, kWaves = 4;
+constexpr int kLocalWaves = 8;                     // of a workgroup that takes a whole unit: what its registers fit
 constexpr int kStep = 32;                          // tokens of a step: two tiles of 16
 constexpr int kMaxRun = 64 * 16;                   // a wave holds the pages of its tiles one a lane
 
@@ -40,6 +42,7 @@ struct DecodePlan {
   int waves;
   int units;        // batch * kv_heads * col_groups
   int width;        // columns of a part: those that a unit can have
+  int local;        // a workgroup of kLocalWaves takes a unit and joins it
   int split;        // units may cross waves: they leave parts
   int many_parts;   // few or very long units, of some 32 parts or more: a workgroup joins them, else a wave
 };
@@ -86,9 +89,20 @@ __device__ __forceinline__ KvAttentionCall call_again() {
   return *(const KvAttentionCall*)p;
 }
 
-template <int BF16, int DIM, int CT>
-__global__ void __launch_bounds__(kThreads, 2)
+// o / sum, four values; zeros where nothing was seen.
+template <int BF16>
+__device__ __forceinline__ void store_joined(uint16_t* to, f32x4 o, float sum) {
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+  uint2 w;
+  w.x = (uint32_t)from_f32<BF16>(o[0] * inv) | (uint32_t)from_f32<BF16>(o[1] * inv) << 16;
+  w.y = (uint32_t)from_f32<BF16>(o[2] * inv) | (uint32_t)from_f32<BF16>(o[3] * inv) << 16;
+  *(uint2*)to = w;
+}
+
+template <int BF16, int DIM, int CT, bool LOCAL>
+__global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     kv_decode_kernel(KvAttentionCall call, DecodePlan plan, int page_shift) {
+  constexpr int kWaves = LOCAL ? kLocalWaves : gq::kWaves;
   constexpr int KL = DIM / 64;      // 16-byte loads of a lane for a tile's keys
   constexpr int VB = DIM / 16;      // bytes of a value row that a lane holds, one for each output tile
   constexpr int VW = VB / 4;
@@ -97,22 +111,34 @@ __global__ void __launch_bounds__(kThreads, 2)
   // own row cost the address unit a cycle a lane), the product wants a row a lane.  16-byte pieces
   // of row r are stored at piece ^ kTurn(r): eight rows' pieces cover all banks.
   __shared__ __align__(16) u32x4 key_rows[kWaves][2][16 * (DIM / 16)];
+  __shared__ __align__(16) float sums[LOCAL ? kWaves : 1][LOCAL ? 16 : 1][kPitch];       // of the waves' columns
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col16 = lane & 15, quad = lane >> 4;
   const int room = key_room(call.b, call.a, page_shift);
   const int group = call.a.q_heads / call.c.kv_heads;
 
-  // this wave's steps [share w, share (w + 1)) of all, and the sequence where they start: a scan over
-  // 64 sequences at a time, one a lane
+  // this wave's steps [share w, share (w + 1)) of all (LOCAL: of its unit), and the sequence where they
+  // start: a scan over 64 sequences at a time, one a lane
   const int wave_id = blockIdx.x * kWaves + wave;
   SeqRows held;                                   // of sequence q + lane
+  int seq = 0, skipped = 0;                       // the sequence, and its steps that come before
+  int full = 0, dealt = 0;
+  const bool one_scan = !LOCAL && call.b.batch <= 64;       // then `held` stays
+  if constexpr (LOCAL) {
+    const int unit = blockIdx.x % (call.c.kv_heads * plan.col_groups);
+    seq = blockIdx.x / (call.c.kv_heads * plan.col_groups);
+    const SeqWork work = sequence_work<CT>(call, sequence_rows(call.b, seq), room);
+    if (unit >= work.groups * call.c.kv_heads) return;                       // of the whole workgroup
+    full = (work.steps + kWaves - 1) / kWaves;
+    skipped = unit * work.steps + wave * full;
+    dealt = work.steps - wave * full < full ? work.steps - wave * full : full;
+  } else {
   auto steps_of = [&](int q) {
     held = q < call.b.batch ? sequence_rows(call.b, q) : SeqRows{0, 0, 0, 0};
     const SeqWork w = sequence_work<CT>(call, held, room);
     return w.steps * w.groups * call.c.kv_heads;
   };
-  const bool one_scan = call.b.batch <= 64;       // then `held` stays
   int all = 0, mine = 0, upto = 0;
   if (one_scan) {
     mine = steps_of(lane);
@@ -121,10 +147,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else {
     for (int q = 0; q < call.b.batch; q += 64) all += wave_sum(steps_of(q + lane));
   }
-  const int full = (all + plan.waves - 1) / plan.waves;
+  full = (all + plan.waves - 1) / plan.waves;
   if ((int64_t)full * wave_id >= all) return;
-  const int pos0 = full * wave_id, dealt = all - pos0 < full ? all - pos0 : full;
-  int seq = 0, skipped = 0;                       // the sequence, and its steps that come before
+  const int pos0 = full * wave_id;
+  dealt = all - pos0 < full ? all - pos0 : full;
   for (int q = 0, before = 0; q < call.b.batch; q += 64) {
     if (!one_scan) {
       mine = steps_of(q + lane);
@@ -138,6 +164,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       break;
     }
     before = __builtin_amdgcn_readlane(upto, 63);
+  }
   }
   auto rows_of = [&](int q) {
     if (!one_scan) return sequence_rows(call.b, q);
@@ -160,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int steps = work.steps - step0 < left ? work.steps - step0 : left;
   const bool alone = steps == work.steps;        // the unit is all here
   const int unit_id = (seq * a.c.kv_heads + kv_head) * plan.col_groups + unit % work.groups;
-  if (plan.split && step0 == 0 && lane == 0)
+  if (!LOCAL && plan.split && step0 == 0 && lane == 0)
     ((UnitParts*)a.ws)[unit_id] = UnitParts{wave_id + unit_id, (dealt - left + work.steps - 1) / full + 1};
   const int run0 = work.lo + step0 * kStep;
   const int run1 = work.hi < run0 + steps * kStep ? work.hi : run0 + steps * kStep;
@@ -384,8 +411,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         __builtin_memcpy(__builtin_assume_aligned(to + VB * (4 * quad + e), VB * 2), o, VB * 2);
       }
     } else {
-      float* to = (float*)((uint8_t*)e_call.ws + parts_offset(plan)) +
-                  ((int64_t)(wave_id + unit_id) * plan.width + ct * 16 + col16) * kPitch;
+      float* to = LOCAL ? sums[wave][col16]
+                        : (float*)((uint8_t*)e_call.ws + parts_offset(plan)) +
+                              ((int64_t)(wave_id + unit_id) * plan.width + ct * 16 + col16) * kPitch;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -400,6 +428,26 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   left -= steps;
   skipped += steps;
+  }
+  if constexpr (LOCAL) {
+    // the waves' sums joined in order, four values of a column a thread
+    const KvAttentionCall a = call_again();
+    __syncthreads();
+    const SeqWork work = sequence_work<CT>(a, sequence_rows(a.b, seq), room);
+    const int count = (work.steps + full - 1) / full, unit = blockIdx.x % (a.c.kv_heads * plan.col_groups);
+    const int kv_head = unit / work.groups, first_col = unit % work.groups * 16;
+    const int c = first_col + threadIdx.x / (DIM / 4), d = threadIdx.x % (DIM / 4) * 4;
+    if (count <= 1 || threadIdx.x >= 16 * (DIM / 4) || c >= work.s.rows * group) return;
+    float most = kNoTop, all = 0.0f;
+    f32x4 o{0, 0, 0, 0};
+    for (int w = 0; w < count; ++w) most = __builtin_fmaxf(most, sums[w][c - first_col][DIM]);
+    for (int w = 0; w < count; ++w) {
+      const float* from = sums[w][c - first_col];
+      const float in = __builtin_amdgcn_exp2f(from[DIM] - most);
+      all = __builtin_fmaf(from[DIM + 1], in, all);
+      o += *(const f32x4*)(from + d) * in;
+    }
+    store_joined<BF16>(a.out + (int64_t)(work.s.row0 + c / group) * a.a.out_stride + (kv_head * group + c % group) * DIM + d, o, all);
   }
 }
 
@@ -454,11 +502,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, De
       for (int w = 1; w < kWaves; ++w) join(sums[w][DIM], sums[w][DIM + 1], *(const f32x4*)&sums[w][in_part * 4]);
   }
   if (thread >= kLanes) return;
-  const float inv = all != 0.0f ? 1.0f / all : 0.0f;
-  uint2 w;
-  w.x = (uint32_t)from_f32<BF16>(o[0] * inv) | (uint32_t)from_f32<BF16>(o[1] * inv) << 16;
-  w.y = (uint32_t)from_f32<BF16>(o[2] * inv) | (uint32_t)from_f32<BF16>(o[3] * inv) << 16;
-  *(uint2*)(a.out + row * a.a.out_stride + head * DIM + in_part * 4) = w;
+  store_joined<BF16>(a.out + row * a.a.out_stride + head * DIM + in_part * 4, o, all);
 }
 
 // Two waves a SIMD (256 CUs): more bring nothing once each has two steps on their way.  No more than
@@ -475,7 +519,14 @@ DecodePlan plan_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_at
   const int64_t steps = (span + 15 + kStep - 1) / kStep;      // a range starts at 16: up to 15 more
   const int64_t units = (int64_t)b.batch * c.kv_heads * p.col_groups;
   const int64_t fit = 256 * kWaves * 2;
-  p.split = steps > 1;
+  // A CU alone takes in some 50 GB/s, so short units only; fewer than 64 leave most of the card idle in
+  // exchange for the second launch (4.6 us of the device, 2.7 of the host).  Us on the device, local
+  // against split, 8 kv heads of 128: 1 sequence of 256 tokens 7.4 / 9.5, 512: 9.0 / 9.9, 1024: 11.4 /
+  // 10.0, 2048: 16.9 / 10.7; 16 sequences of 1024: 14.2 / 17.8, 2048: 20.3 / 22.2, 4096: 32.7 / 32.2;
+  // 64 sequences of 512: 22.5 / 20.7 (two workgroups for each CU take turns).
+  const int64_t bytes = steps * kStep * c.head_dim * 2;
+  p.local = p.col_tiles == 1 && units * c.head_dim <= 256 * 128 && bytes <= (units < 64 ? 256 << 10 : 512 << 10);
+  p.split = !p.local && steps > 1;
   p.units = units > 0x7fffffff ? 0x7fffffff : (int)units;
   p.many_parts = steps > 1024 || units < fit / 32;
   p.waves = (int)(!p.split ? p.units : units * steps < fit ? units * steps : fit);
@@ -497,8 +548,11 @@ static hipError_t launch_dim(const KvAttentionCall& a, const DecodePlan& p, int 
   if (joins > 0x7fffffff || p.units == 0x7fffffff || (steps + 1) * p.units > 0x7fffffff)
     return hipErrorInvalidConfiguration;
   const dim3 grid((uint32_t)((p.waves + kWaves - 1) / kWaves)), block(kThreads);
-  if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1><<<grid, block, 0, s>>>(a, p, page_shift);
-  else kv_decode_kernel<BF16, DIM, 2><<<grid, block, 0, s>>>(a, p, page_shift);
+  if (p.local) {
+    const dim3 units((uint32_t)p.units), threads(64 * kLocalWaves);
+    kv_decode_kernel<BF16, DIM, 1, true><<<units, threads, 0, s>>>(a, p, page_shift);
+  } else if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1, false><<<grid, block, 0, s>>>(a, p, page_shift);
+  else kv_decode_kernel<BF16, DIM, 2, false><<<grid, block, 0, s>>>(a, p, page_shift);
   if (p.split && p.many_parts) kv_join_kernel<BF16, DIM, kThreads><<<dim3((uint32_t)joins), block, 0, s>>>(a, p);
   else if (p.split) kv_join_kernel<BF16, DIM, 64><<<dim3((uint32_t)joins), block, 0, s>>>(a, p);
   return hipGetLastError();

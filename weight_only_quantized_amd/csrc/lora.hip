@@ -1,7 +1,8 @@
 // Low-rank adapters of many requests beside a shared projection.
 //
 // Mathematics: low[m] = scale_i A_i x[m] (rank values), out[m] = y[m] + B_i low[m], i = ids[m]: two
-// launches, since every output needs the whole sum over K.
+// launches, since every output needs the whole sum over K.  Where there is little of both, one launch
+// whose workgroups each compute all of low is quicker.
 //
 // What bounds it: bytes.  Single tokens of many requests read A_i and B_i of every adapter in use
 // once; prompts read x and y and write out.  Both products run on v_mfma_f32_16x16x32 with columns =
@@ -34,6 +35,7 @@ struct LoraPlan {
   bool few;                    // few rows: adapters of a tile over workgroups, low added by its readers
   int low_tiles;               // row tiles of the first launch: of 16 (few) or 4 * kManyRows rows
   int up_tiles, up_rows;       // of the second, of 16, 32 or 64 rows
+  bool here;                   // few and small: one launch, each workgroup computes low itself
   int turns;                   // workgroups that share a tile's adapters
   int slices, slice_k;         // parts of K
   int blocks_n, per_n;         // workgroups over N, each per_n times 256 outputs
@@ -219,7 +221,7 @@ __device__ __forceinline__ int row_exponent(float most) {
   const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127 - 13;
   return e < -120 ? -120 : e > 114 ? 114 : e;
 }
-// low * down as value and remainder
+// low * down as value and remainder (0 beside an infinity)
 template <int BF16>
 __device__ __forceinline__ void split8(const float* low, float down, u32x4* high, u32x4* rest) {
 #pragma unroll
@@ -227,7 +229,10 @@ __device__ __forceinline__ void split8(const float* low, float down, u32x4* high
     const float v0 = low[2 * e] * down, v1 = low[2 * e + 1] * down;
     const uint16_t h0 = from_f32<BF16>(v0), h1 = from_f32<BF16>(v1);
     (*high)[e] = (uint32_t)h0 | (uint32_t)h1 << 16;
-    (*rest)[e] = (uint32_t)from_f32<BF16>(v0 - to_f32<BF16>(h0)) | (uint32_t)from_f32<BF16>(v1 - to_f32<BF16>(h1)) << 16;
+    const float r0 = v0 - to_f32<BF16>(h0), r1 = v1 - to_f32<BF16>(h1);
+    constexpr uint32_t kInf = BF16 ? 0x7f80 : 0x7c00;
+    (*rest)[e] = ((h0 & 0x7fffu) == kInf ? 0u : (uint32_t)from_f32<BF16>(r0)) |
+                 ((h1 & 0x7fffu) == kInf ? 0u : (uint32_t)from_f32<BF16>(r1)) << 16;
   }
 }
 
@@ -262,15 +267,20 @@ __global__ void __launch_bounds__(kThreads) lora_join_kernel(LoraCall c, LoraPla
 // outputs each of a run of 256.  B_i's 64 rows are one piece of memory, y and out 128 bytes of a row for
 // eight lanes: B_i and the products pass through the wave's own LDS between that order and the matrix
 // operands'.
-template <int BF16, int KS, int CT, bool JOINED>   // 32-value steps of the rank, row tiles of 16; low joined
+enum { kLowParts, kLowJoined, kLowHere };            // low: the slices' parts, two numbers, not yet computed
+template <int BF16, int KS, int CT, int LOW>         // 32-value steps of the rank, row tiles of 16
 __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(LoraCall c, LoraPlan p) {
   constexpr int kRows = 16 * CT, kPitch = KS * 4 + 1;      // 16-byte pieces of a row: no two of eight rows on a bank
   constexpr int kTilePitch = 64 + 4;                       // floats of a row of 64 outputs
-  constexpr int kAux = JOINED ? kAuxStream : 0;            // many rows of y and out pass the caches by (61.4 -> 59.4 us)
+  constexpr int kAux = LOW == kLowJoined ? kAuxStream : 0;            // many rows of y and out pass the caches by (61.4 -> 59.4 us)
   constexpr int kOwn = 64 * kPitch > 16 * kTilePitch / 4 ? 64 * kPitch : 16 * kTilePitch / 4;
   __shared__ __align__(16) u32x4 lows[2][kRows * kPitch];  // value, remainder
   __shared__ float scaled[kRows];                          // the power of two that a row was scaled by
   __shared__ __align__(16) u32x4 own[kWaves][kOwn];        // a wave's B rows, then its 16 x 64 products
+  constexpr int kRanks = 2 * KS, kSumPitch = kRanks * 16 + 4;          // rank tiles of low computed here
+  __shared__ u32x4 stage[LOW == kLowHere ? kWaves : 1][LOW == kLowHere ? kStage<kRanks, 1> : 1];
+  float (*const sums)[16][kSumPitch] = (float (*)[16][kSumPitch])stage;
+  static_assert(LOW != kLowHere || (CT == 1 && sizeof(float) * kWaves * 16 * kSumPitch <= sizeof(stage)), "");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4, piece = lane & 7;
   int id = blockIdx.x;
@@ -322,7 +332,17 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
 
     if (!first) __syncthreads();
     first = false;
-    if constexpr (JOINED) {
+    if constexpr (LOW == kLowHere) {
+      // each wave its part of K
+      const int K = c.bank.in_features, k0 = wave * p.slice_k, k1 = k0 + p.slice_k < K ? k0 + p.slice_k : K;
+      f32x4 acc[kRanks][1];
+      low_product<BF16>(make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2), adapter_a(c, a), K, k0, k1, lane, stage[wave], acc);
+      __syncthreads();                                   // all waves have read their rows
+#pragma unroll
+      for (int r = 0; r < kRanks; ++r) *(f32x4*)&sums[wave][col][r * 16 + quad * 4] = acc[r][0];
+      __syncthreads();
+    }
+    if constexpr (LOW == kLowJoined) {
       // rows of other adapters hold zeros
       const uint16_t* from = (const uint16_t*)((const uint8_t*)c.ws + p.part_bytes);
       for (int i = threadIdx.x; i < kRows * KS * 4; i += kThreads) {
@@ -342,9 +362,13 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
         for (int k = 0; k < KS; ++k) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) low[k][e] = 0.0f;
-          if (mine && k * 32 + quad * 8 < rank)
-            add_parts((const float*)c.ws + (row0 + t * 16 + col) * rank + k * 32 + quad * 8, p.slices, c.M * rank,
-                      c.bank.scale[a], low[k]);
+          if (mine && k * 32 + quad * 8 < rank) {
+            if constexpr (LOW == kLowHere)
+              add_parts(&sums[0][col][k * 32 + quad * 8], kWaves, 16 * kSumPitch, c.bank.scale[a], low[k]);
+            else
+              add_parts((const float*)c.ws + (row0 + t * 16 + col) * rank + k * 32 + quad * 8, p.slices, c.M * rank,
+                        c.bank.scale[a], low[k]);
+          }
           most = __builtin_fmaxf(most, largest8(low[k]));
         }
         float down = 1.0f;
@@ -453,7 +477,13 @@ LoraPlan plan_of(const gptq_lora_bank& bank, int64_t M) {
   int64_t per = p.up_tiles * turns * blocks / 1536;
   p.per_n = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
   p.blocks_n = (int)div_up(blocks, p.per_n);
-  p.part_bytes = (size_t)div_up((int64_t)p.slices * M * bank.rank * 4, 256) * 256;
+  // One launch while its workgroups have a CU each and A_i is small, since each reads all of it.  Us on the
+  // device, one launch against two, rank 8, 1 row: K = 1024 4.9 / 6.8, 4096 7.1 / 8.0, 5120 7.8 / 7.6, 6144
+  // 8.6 / 7.8 (the second launch costs the host 2.7 more); K = 4096, N = 14336, 4 rows (224 workgroups)
+  // 7.4 / 8.2, 8 rows (448) 11.5 / 8.6.  Eight waves that share K instead of four: 7.9 at K = 4096.
+  p.here = p.few && bank.rank <= 32 && bank.in_features <= 5120 && p.up_tiles * turns * p.blocks_n <= 256;
+  if (p.here) p.slice_k = (int)(div_up(div_up(bank.in_features, 64), kWaves) * 64);
+  p.part_bytes = p.here ? 0 : (size_t)div_up((int64_t)p.slices * M * bank.rank * 4, 256) * 256;
   return p;
 }
 
@@ -467,11 +497,13 @@ void launch_low(const LoraCall& c, const LoraPlan& p, hipStream_t s) {
 template <int BF16, int KS>
 void launch_up(const LoraCall& c, const LoraPlan& p, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.up_tiles * p.turns * p.blocks_n)), block(kThreads);
-  if (p.few) {
-    lora_up_kernel<BF16, KS, 1, false><<<grid, block, 0, s>>>(c, p);
+  if (p.here) {
+    if constexpr (KS == 1) lora_up_kernel<BF16, KS, 1, kLowHere><<<grid, block, 0, s>>>(c, p);
+  } else if (p.few) {
+    lora_up_kernel<BF16, KS, 1, kLowParts><<<grid, block, 0, s>>>(c, p);
   } else {
     lora_join_kernel<BF16><<<dim3((uint32_t)div_up(c.M, kThreads / 16)), block, 0, s>>>(c, p);
-    lora_up_kernel<BF16, KS, KS == 4 ? 2 : 4, true><<<grid, block, 0, s>>>(c, p);
+    lora_up_kernel<BF16, KS, KS == 4 ? 2 : 4, kLowJoined><<<grid, block, 0, s>>>(c, p);
   }
 }
 
@@ -481,7 +513,8 @@ hipError_t launch_type(const LoraCall& c, hipStream_t s) {
   if ((int64_t)p.low_tiles * p.turns * p.slices > 0x7fffffff || (int64_t)p.up_tiles * p.turns * p.blocks_n > 0x7fffffff)
     return hipErrorInvalidConfiguration;
   const int rank = c.bank.rank;
-  if (rank <= 16) launch_low<BF16, 1>(c, p, s);
+  if (p.here) ;
+  else if (rank <= 16) launch_low<BF16, 1>(c, p, s);
   else if (rank <= 32) launch_low<BF16, 2>(c, p, s);
   else if (rank <= 64) launch_low<BF16, 4>(c, p, s);
   else launch_low<BF16, 8>(c, p, s);

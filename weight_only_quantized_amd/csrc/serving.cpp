@@ -245,7 +245,7 @@ gptq_status gptq_lora_add(const gptq_lora_bank* bank, const void* x, const void*
       overlaps(out, yb, bank->b, bb) || overlaps(out, yb, ids, (size_t)M * 4))
     return GPTQ_E_INVALID_ARG;
   const size_t need = lora_ws_bytes(*bank, M);
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return GPTQ_E_WORKSPACE;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return GPTQ_E_WORKSPACE;
   if (overlaps(workspace, need, x, xb) || overlaps(workspace, need, y, yb) || overlaps(workspace, need, out, yb) ||
       overlaps(workspace, need, bank->a, ab) || overlaps(workspace, need, bank->b, bb))
     return GPTQ_E_INVALID_ARG;

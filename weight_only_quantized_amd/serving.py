@@ -329,11 +329,12 @@ class LoraBank:
                 size = self._sizes.get(M)
                 if size is None:
                     size = self.workspace_size(M)
-                workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+                if size:
+                    workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
             else:
                 size = workspace.numel() * workspace.element_size()
             st = self._lib.gptq_lora_add(self._c, x.data_ptr(), y.data_ptr(), id_ptr, M, out.data_ptr(),
-                                         workspace.data_ptr(), size, ptr)
+                                         workspace.data_ptr() if workspace is not None else None, size, ptr)
         if st:
             raise GPTQError(st, "gptq_lora_add", self._lib)
         return out
