@@ -39,7 +39,7 @@ constexpr int kMaxRun = 64 * 16;                   // a wave holds the pages of 
 struct DecodePlan {
   int col_tiles;    // 16-column tiles of a unit: 1 or 2
   int col_groups;   // units of a sequence and kv head, at most
-  int waves;
+  int waves, wave_bits;    // a power of two
   int units;        // batch * kv_heads * col_groups
   int width;        // columns of a part: those that a unit can have
   int local;        // a workgroup of kLocalWaves takes a unit and joins it
@@ -47,10 +47,10 @@ struct DecodePlan {
   int many_parts;   // few or very long units, of some 32 parts or more: a workgroup joins them, else a wave
 };
 
-// A unit's parts, in the workspace: `count` of them from slot `first` on, one a wave.  Wave w
-// leaves its part of unit u in slot w + u, which no other pair shares since both only ascend.
+// A unit's parts, in the workspace: slots `first` to `last`, one a wave.  Wave w leaves its part of
+// unit u in slot w + u, which no other pair shares since both only ascend.
 struct UnitParts {
-  int first, count;
+  int first, last;
 };
 __host__ __device__ inline size_t parts_offset(const DecodePlan& p) { return ((size_t)p.units * sizeof(UnitParts) + 255) / 256 * 256; }
 
@@ -118,12 +118,12 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   const int room = key_room(call.b, call.a, page_shift);
   const int group = call.a.q_heads / call.c.kv_heads;
 
-  // this wave's steps [share w, share (w + 1)) of all (LOCAL: of its unit), and the sequence where they
+  // this wave's share of all steps (LOCAL: of its unit's), and the sequence where they
   // start: a scan over 64 sequences at a time, one a lane
   const int wave_id = blockIdx.x * kWaves + wave;
   SeqRows held;                                   // of sequence q + lane
   int seq = 0, skipped = 0;                       // the sequence, and its steps that come before
-  int full = 0, dealt = 0;
+  int dealt = 0, full = 0;                        // its steps; of LOCAL's first waves
   const bool one_scan = !LOCAL && call.b.batch <= 64;       // then `held` stays
   if constexpr (LOCAL) {
     const int unit = blockIdx.x % (call.c.kv_heads * plan.col_groups);
@@ -147,10 +147,11 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   } else {
     for (int q = 0; q < call.b.batch; q += 64) all += wave_sum(steps_of(q + lane));
   }
-  full = (all + plan.waves - 1) / plan.waves;
-  if ((int64_t)full * wave_id >= all) return;
-  const int pos0 = full * wave_id;
-  dealt = all - pos0 < full ? all - pos0 : full;
+  // shares differ by one step, the longer ones everywhere; no wave without a step between two that have one
+  const int dealers = all < plan.waves ? all : plan.waves;
+  if (wave_id >= dealers) return;
+  const int pos0 = dealers < plan.waves ? wave_id : (int)((int64_t)all * wave_id >> plan.wave_bits);
+  dealt = (dealers < plan.waves ? wave_id + 1 : (int)((int64_t)all * (wave_id + 1) >> plan.wave_bits)) - pos0;
   for (int q = 0, before = 0; q < call.b.batch; q += 64) {
     if (!one_scan) {
       mine = steps_of(q + lane);
@@ -187,8 +188,10 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   const int steps = work.steps - step0 < left ? work.steps - step0 : left;
   const bool alone = steps == work.steps;        // the unit is all here
   const int unit_id = (seq * a.c.kv_heads + kv_head) * plan.col_groups + unit % work.groups;
-  if (!LOCAL && plan.split && step0 == 0 && lane == 0)
-    ((UnitParts*)a.ws)[unit_id] = UnitParts{wave_id + unit_id, (dealt - left + work.steps - 1) / full + 1};
+  if (!LOCAL && plan.split && lane == 0) {
+    if (step0 == 0) ((UnitParts*)a.ws)[unit_id].first = wave_id + unit_id;
+    if (step0 + steps == work.steps) ((UnitParts*)a.ws)[unit_id].last = wave_id + unit_id;
+  }
   const int run0 = work.lo + step0 * kStep;
   const int run1 = work.hi < run0 + steps * kStep ? work.hi : run0 + steps * kStep;
   const int last_col = first_col + 16 * CT < columns ? first_col + 16 * CT - 1 : columns - 1;
@@ -197,6 +200,12 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   int begin[CT], end[CT];
   float q_scale[CT], top[CT], total[CT];
   f16x8 q[CT][2 * KL];
+  u32x4 query[CT][2 * KL];
+  auto page_id = [&](int base) {                  // 16 tokens a lane
+    const int my_pos = base + lane * 16;
+    return tile_page_id(a.c, a.b, seq, my_pos, my_pos < run1, page_shift);
+  };
+  int page = page_id(run0);                       // on its way with the query
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     int c = first_col + ct * 16 + col16;
@@ -206,8 +215,8 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     begin[ct] = r.begin;
     end[ct] = r.end;
     const uint16_t* at = a.q + (int64_t)(s.row0 + row) * a.a.q_stride + head * DIM + quad * 16;
-    q_scale[ct] = load_query<BF16, 2 * KL>(at, [](int i) { return (i >> 1) * 64 + (i & 1) * 8; }, q[ct], 16, 32) *
-                  (a.a.scale * kLog2e);
+#pragma unroll
+    for (int i = 0; i < 2 * KL; ++i) query[ct][i] = *(const u32x4*)(at + (i >> 1) * 64 + (i & 1) * 8);
     top[ct] = kNoTop;
     total[ct] = 0.0f;
   }
@@ -359,14 +368,11 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     if constexpr (decltype(more)::value) load_values(d, i + 2);
   };
 
-  for (; base < run1; base += kMaxRun) {
-    const int my_pos = base + lane * 16;
-    pages = tile_page(a.c, a.b, seq, kv_head, my_pos, my_pos < run1, page_shift);
-    my_log = scale_log(pages.v_scale);
-    my_inv = scale_inv(my_log);
-    const int n = run1 - base < kMaxRun ? (run1 - base + kStep - 1) / kStep : kMaxRun / kStep;
-    Step even, odd;
-    // in the order of the steps: a wait for one load waits for all before it
+  Step even, odd;
+  // a run's scales and first steps, in the order of the steps: a wait for one load waits for all before it
+  auto start_run = [&] {
+    pages = tile_scales(a.c, page, kv_head);
+    __builtin_amdgcn_sched_barrier(0);
     load_keys(even, 0);
     __builtin_amdgcn_sched_barrier(0);
     load_values(even, 0);
@@ -375,9 +381,26 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     __builtin_amdgcn_sched_barrier(0);
     load_values(odd, 1);
     __builtin_amdgcn_sched_barrier(0);
+  };
+  start_run();
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) q_scale[ct] = query_f16<BF16, 2 * KL>(query[ct], q[ct], 16, 32) * (a.a.scale * kLog2e);
+  for (;;) {
+    const TilePage there = settled(pages);
+    pages = there;
+    my_log = scale_log(there.v_scale);
+    my_inv = scale_inv(my_log);
+    const int n = run1 - base < kMaxRun ? (run1 - base + kStep - 1) / kStep : kMaxRun / kStep;
     if constexpr (CT == 1) {               // pairs, so that every wait in the loop is for what it needs
       int i = 0;
       for (; i + 1 < n; i += 2) {
+        // the older of a SIMD's waves would run ahead and leave the others alone at the end (64 sequences:
+        // ends spread over 28 .. 43 us, now 31 .. 38): the more a wave has left, the earlier its turn
+        const int togo = (left - i) * 8;
+        if (togo > dealt * 4) __builtin_amdgcn_s_setprio(3);
+        else if (togo > dealt * 2) __builtin_amdgcn_s_setprio(2);
+        else if (togo > dealt) __builtin_amdgcn_s_setprio(1);
+        else __builtin_amdgcn_s_setprio(0);
         compute(even, i, std::true_type{});
         compute(odd, i + 1, std::true_type{});
       }
@@ -388,6 +411,10 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
         if (i + 1 < n) compute(odd, i + 1, std::true_type{});
       }
     }
+    base += kMaxRun;
+    if (base >= run1) break;
+    page = page_id(base);
+    start_run();
   }
 
   // output tile t of lane (col16, quad) holds values VB (4 quad + e) + t
@@ -467,7 +494,8 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, De
   if (place < 0 || place >= s.rows) return;
   const int width = 16 * plan.col_tiles, c = place * group + head % group;
   const UnitParts parts = ((const UnitParts*)a.ws)[(seq * a.c.kv_heads + head / group) * plan.col_groups + c / width];
-  if (parts.count <= 1) return;
+  const int count = parts.last - parts.first + 1;
+  if (count <= 1) return;
   const float* part = (const float*)((const uint8_t*)a.ws + parts_offset(plan)) +
                       ((int64_t)parts.first * plan.width + c % width) * kPitch;
   const int thread = threadIdx.x % THREADS, in_part = thread % kLanes;
@@ -481,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, De
     most = now;
   };
 #pragma unroll 4
-  for (int i = thread / kLanes; i < parts.count; i += kGroups) {
+  for (int i = thread / kLanes; i < count; i += kGroups) {
     const float* from = part + (int64_t)i * plan.width * kPitch;
     join(from[DIM], from[DIM + 1], *(const f32x4*)(from + in_part * 4));
   }
@@ -521,15 +549,17 @@ DecodePlan plan_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_at
   const int64_t fit = 256 * kWaves * 2;
   // A CU alone takes in some 50 GB/s, so short units only; fewer than 64 leave most of the card idle in
   // exchange for the second launch (4.6 us of the device, 2.7 of the host).  Us on the device, local
-  // against split, 8 kv heads of 128: 1 sequence of 256 tokens 7.4 / 9.5, 512: 9.0 / 9.9, 1024: 11.4 /
-  // 10.0, 2048: 16.9 / 10.7; 16 sequences of 1024: 14.2 / 17.8, 2048: 20.3 / 22.2, 4096: 32.7 / 32.2;
-  // 64 sequences of 512: 22.5 / 20.7 (two workgroups for each CU take turns).
+  // against split, 8 kv heads of 128: 1 sequence of 256 tokens 7.2 / 9.4, 512: 8.7 / 9.7, 1024: 9.6 / 9.7,
+  // 2048: 16.9 / 10.5; 16 sequences of 1024: 13.3 / 17.6, 2048: 20.3 / 21.9, 4096: 32.7 / 31.1; 64
+  // sequences of 512: 22.5 / 20.2 (two workgroups for each CU take turns).
   const int64_t bytes = steps * kStep * c.head_dim * 2;
   p.local = p.col_tiles == 1 && units * c.head_dim <= 256 * 128 && bytes <= (units < 64 ? 256 << 10 : 512 << 10);
   p.split = !p.local && steps > 1;
   p.units = units > 0x7fffffff ? 0x7fffffff : (int)units;
   p.many_parts = steps > 1024 || units < fit / 32;
-  p.waves = (int)(!p.split ? p.units : units * steps < fit ? units * steps : fit);
+  p.wave_bits = 0;
+  while (1 << p.wave_bits < fit && 1 << p.wave_bits < units * steps) ++p.wave_bits;
+  p.waves = 1 << p.wave_bits;
   return p;
 }
 

@@ -57,18 +57,25 @@ struct TilePage {
   int page;
   float k_scale, v_scale;
 };
+// The same in parts, for a caller that has other loads to send between them: the page, its scales as they
+// are (page 0's for an absent tile), and what tile_page gives.  No branches.
+__device__ __forceinline__ int tile_page_id(const gptq_kv_cache& c, const gptq_kv_batch& b, int seq, int pos, bool wanted,
+                                            int page_shift) {
+  const int j = pos >> page_shift;
+  const bool in = wanted && pos >= 0 && j < b.table_width;
+  const int page = b.page_table[(int64_t)seq * b.table_width + (in ? j : 0)];
+  return in && page >= 0 && page < c.num_pages ? page : -1;
+}
+__device__ __forceinline__ TilePage tile_scales(const gptq_kv_cache& c, int page, int kv_head) {
+  const int64_t unit = (int64_t)(page < 0 ? 0 : page) * c.kv_heads + kv_head;
+  return TilePage{page, c.k_scale[unit], c.v_scale[unit]};
+}
+__device__ __forceinline__ TilePage settled(const TilePage& t) {
+  return TilePage{t.page, t.page < 0 ? 0.0f : t.k_scale, t.page < 0 ? 0.0f : __builtin_fmaxf(t.v_scale, 0x1p-64f)};
+}
 __device__ __forceinline__ TilePage tile_page(const gptq_kv_cache& c, const gptq_kv_batch& b, int seq, int kv_head,
                                               int pos, bool wanted, int page_shift) {
-  TilePage t{-1, 0.0f, 0.0f};
-  const int j = pos >> page_shift;
-  if (!wanted || pos < 0 || j >= b.table_width) return t;
-  const int page = b.page_table[(int64_t)seq * b.table_width + j];
-  if (page < 0 || page >= c.num_pages) return t;
-  const int64_t unit = (int64_t)page * c.kv_heads + kv_head;
-  t.page = page;
-  t.k_scale = c.k_scale[unit];
-  t.v_scale = __builtin_fmaxf(c.v_scale[unit], 0x1p-64f);
-  return t;
+  return settled(tile_scales(c, tile_page_id(c, b, seq, pos, wanted, page_shift), kv_head));
 }
 // Bytes before a tile's codes (page 0's for an absent tile, which is safe to read).
 __device__ __forceinline__ uint64_t tile_base(const gptq_kv_cache& c, int page, int kv_head, int pos, int page_shift) {
@@ -105,15 +112,12 @@ __device__ __forceinline__ uint32_t pair_f16(uint32_t first, uint32_t second, in
   return less_1152(__builtin_amdgcn_perm(second, first, sel) ^ 0x64806480u);
 }
 
-// A query row's float16 operands, N of eight values at at[offset(i)], from lanes that together hold
-// the row (xor `mask0`, `mask1` reach the others); returns the power of two that was taken out.
+// A query row's float16 operands, N of eight values (load_query: at at[offset(i)]), from lanes that together
+// hold the row (xor `mask0`, `mask1` reach the others); returns the power of two that was taken out.
 // float16 rows are exact as they are; bfloat16 rows are scaled so that the largest magnitude is in
 // [2^14, 2^15), where float16 holds their 8 bits exactly down to 2^-29 of it.
-template <int BF16, int N, typename Offset>
-__device__ __forceinline__ float load_query(const uint16_t* at, Offset offset, f16x8* q, int mask0, int mask1) {
-  u32x4 w[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) w[i] = *(const u32x4*)(at + offset(i));
+template <int BF16, int N>
+__device__ __forceinline__ float query_f16(const u32x4 (&w)[N], f16x8* q, int mask0, int mask1) {
   if constexpr (!BF16) {
 #pragma unroll
     for (int i = 0; i < N; ++i) q[i] = __builtin_bit_cast(f16x8, w[i]);
@@ -146,6 +150,13 @@ __device__ __forceinline__ float load_query(const uint16_t* at, Offset offset, f
       }
     return __builtin_ldexpf(1.0f, e - 14);
   }
+}
+template <int BF16, int N, typename Offset>
+__device__ __forceinline__ float load_query(const uint16_t* at, Offset offset, f16x8* q, int mask0, int mask1) {
+  u32x4 w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = *(const u32x4*)(at + offset(i));
+  return query_f16<BF16, N>(w, q, mask0, mask1);
 }
 
 }  // namespace gq
