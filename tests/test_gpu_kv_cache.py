@@ -403,6 +403,27 @@ def test_append_against_oracle(case, big):
     check_append(pool, plain, starts, cu, host(k), host(v), case)
 
 
+@pytest.mark.parametrize("tag", ["f16", "bf16"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_rounds_each_product(tag, inter):
+    """Products and sums of the rotation are float32 operations rounded one by one: the same bits as on
+    the CPU, so codes do not depend on how a compiler joins operations."""
+    import torch
+    rng = np.random.default_rng(31)
+    rows, heads, dim = 700, 4, 128
+    cos, sin = (torch.from_numpy(t) for t in tables(rows, dim // 2))
+    x = torch.from_numpy(rng.normal(0, 2, (rows, heads, dim))).to(torch.float16 if tag == "f16" else torch.bfloat16)
+    cache, kv = Pool([rows], 64, 1, dim, seed=1), torch.zeros((rows, 1, dim), dtype=x.dtype, device="cuda")
+    got = cache.cache().append(kv, kv, dev(cache.table), dev(np.zeros(1, np.int32)), dev(offsets([rows])), max_new=rows,
+                               q=x.cuda(), cos=cos.cuda(), sin=sin.cuda(), interleaved=inter)
+    f, c, s = x.float(), cos[:, None], sin[:, None]
+    a, b = (f[..., 0::2], f[..., 1::2]) if inter else (f[..., :dim // 2], f[..., dim // 2:])
+    ac, bs, bc, as_ = a * c, b * s, b * c, a * s
+    lo, hi = ac - bs, bc + as_
+    want = torch.stack((lo, hi), -1).flatten(-2) if inter else torch.cat((lo, hi), -1)
+    assert torch.equal(got.cpu(), want.to(x.dtype))
+
+
 @pytest.mark.parametrize("batch,many", [(65, False), (200, False), (300, True), (70, True)])
 def test_many_sequences(batch, many):
     """More sequences than a wave has lanes: appended, read back and attended to, some without rows or

@@ -40,6 +40,7 @@ __device__ __forceinline__ void load8(const uint16_t* at, float* x) {
 // The eight values [d, d + 8) of a head at `head`, rotated at table row `pos`.
 template <int BF16>
 __device__ __forceinline__ void rotated8(const uint16_t* head, int d, int64_t pos, const gptq_rope& r, float* x) {
+#pragma clang fp contract(off)
   load8<BF16>(head + d, x);
   if (d >= r.dim) return;
   const int half = r.dim >> 1;
@@ -50,8 +51,8 @@ __device__ __forceinline__ void rotated8(const uint16_t* head, int d, int64_t po
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-      x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+      x[2 * i] = a * c[i] - b * s[i];
+      x[2 * i + 1] = b * c[i] + a * s[i];
     }
   } else {
     const bool low = d < half;
@@ -62,8 +63,8 @@ __device__ __forceinline__ void rotated8(const uint16_t* head, int d, int64_t po
     const float* s = r.sin + row * half + i0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float t = __fmul_rn(y[i], s[i]);
-      x[i] = low ? __fsub_rn(__fmul_rn(x[i], c[i]), t) : __fadd_rn(__fmul_rn(x[i], c[i]), t);
+      const float t = y[i] * s[i], own = x[i] * c[i];
+      x[i] = low ? own - t : own + t;
     }
   }
 }
