@@ -45,8 +45,9 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
   constexpr int kKeyPitch = DIM / 8 + 1, kValuePitch = kTile / 8 + 1;
   __shared__ __align__(16) u32x4 keys[2][kTile * kKeyPitch];
   __shared__ __align__(16) u32x4 values[2][DIM * kValuePitch];
-  __shared__ float4 unused[64];           // where lanes write that have nothing to write (a branch would cut the step)
-  __shared__ __align__(16) float scales[4][4][4];       // [tile & 3][16 tokens][key scale, log2 value scale, inverse]
+  // [tile & 3][key scale, log2 value scale, inverse][16 tokens]; 64 more where lanes write that have nothing
+  // to write (a branch would cut the step: 8192 tokens 597 -> 590 us)
+  __shared__ __align__(16) float scales[48 + 64];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col32 = lane & 31, half = lane >> 5;
@@ -132,9 +133,12 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
     }
   };
   auto store_scales = [&](int j) {        // of the tile in k_codes
-    const float log = scale_log(st_v);
-    float4* to = lane == 0 && in_part == 0 ? (float4*)scales[j & 3][part] : &unused[lane];
-    *to = make_float4(st_k, log, scale_inv(log), 0.0f);
+    const float log = scale_log(st_v), inverse = scale_inv(log);
+    float one = st_k;
+    one = lane == 1 ? log : one;
+    one = lane == 2 ? inverse : one;
+    const int to = lane < 3 && in_part == 0 ? (j & 3) * 12 + lane * 4 + part : 48 + lane;
+    scales[to] = one;
   };
   auto store_key = [&](int j, int p) {
     u32x4* to = keys[j & 1] + (part * 16 + key_row + p * (1024 / DIM)) * kKeyPitch + key_piece * 2;
@@ -168,13 +172,8 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
 #pragma unroll
     for (int m = 0; m < 2 * KS; ++m) score_step(m, key_at(j, m));
   };
-  float x[2][16];
-  float by, plus, most;
-  // x = exponents of elements [8 u, 8 u + 8) of tile j relative to `from`
-  auto exponent_scale = [&](int j, int u, float from) {
-    by = q_scale * scales[j & 3][u][0];
-    plus = scales[j & 3][u][1] - from;
-  };
+  float x[2][16], most;
+  auto scale4 = [&](int j, int field) { return *(const f32x4*)(scales + (j & 3) * 12 + field * 4); };
   // settles x of tile j: hidden tokens, and a top that has to move (the scores are taken again)
   auto settle = [&](int j) {
     const int pos = lo + j * kTile;
@@ -183,13 +182,14 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
     score(j);
     const KeyRange r = key_range(s, row, a.a, room);
     float m = -__builtin_inff();
+    const f32x4 ks = scale4(j, 0), log = scale4(j, 1);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      exponent_scale(j, u, 0.0f);
+      const float by = q_scale * ks[u];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int p = pos + u * 16 + (e >> 2) * 8 + half * 4 + (e & 3);
-        const float v = __builtin_fmaf(dot[u >> 1][(u & 1) * 8 + e], by, plus);
+        const float v = __builtin_fmaf(dot[u >> 1][(u & 1) * 8 + e], by, log[u]);
         x[u >> 1][(u & 1) * 8 + e] = p < r.begin || p >= r.end ? -__builtin_inff() : v;
         m = __builtin_fmaxf(m, x[u >> 1][(u & 1) * 8 + e]);
       }
@@ -209,49 +209,63 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
   };
 
   // Step i: LDS holds keys of tile i + 1 and values of tile i, registers the keys of tile i + 2 and the
-  // values of tile i + 1, x tile i's exponents.  Micro-steps of one operand keep the vector work
-  // between the matrix instructions; a fence after each keeps the order.
+  // values of tile i + 1, x tile i's exponents, inv its inverse scales.  Micro-steps of one operand keep
+  // the vector work between the matrix instructions; a fence after each keeps the order.  Nothing is read
+  // from LDS shortly before its use: operands run through a ring, kAhead ahead and over the middle of the
+  // step, the first weights come before the first product, scales a phase early.
+  f32x4 inv;
   auto step = [&](int i, auto more) {
     constexpr bool kMore = decltype(more)::value;
-    constexpr int kAhead = 3;
-    u32x4 ring[kAhead];
-    f16x8 w[4];
-    if constexpr (kMore) {
-#pragma unroll
-      for (int m = 0; m < kAhead; ++m) ring[m] = key_at(i + 1, m);
-    }
+    constexpr int kAhead = 3, kKeys = kMore ? 2 * KS : 0, kOut = 4 * DT;
     constexpr int kPer = 32 / (2 * KS);           // weights of a micro-step
-    float inv = 0.0f;
+    constexpr int kLead = kMore ? 2 : 0;          // micro-steps of weights before the first product
+    u32x4 ring[kAhead];
+    auto operand = [&](int n) { return n < kKeys ? key_at(i + 1, n) : value_at(i, n - kKeys); };
+    f16x8 w[4];
+    f32x4 ks, log;
 #pragma unroll
-    for (int m = 0; m < 2 * KS; ++m) {
-      if constexpr (kMore) {
-        score_step(m, ring[m % kAhead]);
-        if (m + kAhead < 2 * KS) ring[m % kAhead] = key_at(i + 1, m + kAhead);
-      }
-      const int u = m * kPer / 8;
-      if (m * kPer % 8 == 0) inv = scales[i & 3][u][2];
+    for (int m = 0; m < kAhead; ++m) ring[m] = operand(m);
+    if constexpr (kMore) {
+      ks = scale4(i + 1, 0);
+      log = scale4(i + 1, 1);
+    }
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int e = m * kPer % 8 + k;
-        const float p = __builtin_amdgcn_exp2f(x[u >> 1][(u & 1) * 8 + e]);
-        total = __builtin_fmaf(p, inv, total);     // in 32 bits: small against the top may be large here
-        w[u][e] = (_Float16)p;
+    for (int m = 0; m < 2 * KS + kLead; ++m) {
+      if (kMore && m >= kLead) {
+        score_step(m - kLead, ring[(m - kLead) % kAhead]);
+        ring[(m - kLead) % kAhead] = operand(m - kLead + kAhead);
       }
-      asm volatile("" : "+v"(total));              // here, not after the step
+      if (m < 2 * KS) {
+        const int u = m * kPer / 8;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int e = m * kPer % 8 + k;
+          const float p = __builtin_amdgcn_exp2f(x[u >> 1][(u & 1) * 8 + e]);
+          total = __builtin_fmaf(p, inv[u], total);     // in 32 bits: small against the top may be large here
+          w[u][e] = (_Float16)p;
+        }
+        asm volatile("" : "+v"(total));              // here, not after the step
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (kMore) most = -__builtin_inff();
-#pragma unroll
-    for (int m = 0; m < kAhead; ++m) ring[m] = value_at(i, m);
-    constexpr int kOut = 4 * DT, kPerOut = 32 / kOut;
+    if constexpr (kMore) {
+      most = -__builtin_inff();
+      inv = scale4(i + 1, 2);
+    }
+    constexpr int kPerOut = 32 / kOut;
+    float by, plus;
 #pragma unroll
     for (int m = 0; m < kOut; ++m) {
-      acc[m / 4] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, ring[m % kAhead]), w[m % 4], acc[m / 4],
-                                                          0, 0, 0);
-      if (m + kAhead < kOut) ring[m % kAhead] = value_at(i, m + kAhead);
+      constexpr int kFrom = kKeys;
+      acc[m / 4] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, ring[(kFrom + m) % kAhead]), w[m % 4],
+                                                          acc[m / 4], 0, 0, 0);
+      if (m + kAhead < kOut) ring[(kFrom + m) % kAhead] = operand(kFrom + m + kAhead);
       if constexpr (kMore) {
         const int u = m * kPerOut / 8;
-        if (m * kPerOut % 8 == 0) exponent_scale(i + 1, u, top);
+        if (m * kPerOut % 8 == 0) {
+          by = q_scale * ks[u];
+          plus = log[u] - top;
+        }
 #pragma unroll
         for (int k = 0; k < kPerOut; ++k) {
           const int e = (u & 1) * 8 + m * kPerOut % 8 + k;
@@ -263,11 +277,12 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
         else if (m == VB + KL) {
           load_values(k_base);
           load_keys(i + 3);
+        } else if (m == VB + KL + 1) {
+          store_scales(i + 3);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (kMore) store_scales(i + 3);
   };
 
   if (steps > 0) {
@@ -289,6 +304,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
     score(0);
     most = __builtin_inff();               // the first tile always settles
     settle(0);
+    inv = scale4(0, 2);
   }
   for (int i = 0; i + 1 < steps; ++i) {
     turn_pages(i + 3);
@@ -303,7 +319,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
 
   const float sum = total + __shfl_xor(total, 32);
   if (wave_col + col32 >= columns) return;
-  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+  const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
   uint16_t* to = a.out + (int64_t)(s.row0 + row) * a.a.out_stride + head * DIM;
   // element e of tile t is LDS row 32 t + 8 (e / 4) + 4 half + e % 4, which is value VB (row % kGroups) +
   // row / kGroups: of one e the tiles (and, with 16 groups, element e + 8) are values next to each other
@@ -314,7 +330,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
 #pragma unroll
     for (int t = 0; t < VB / 2; ++t) {
       const float v0 = kBoth == 2 ? acc[t][e] : acc[2 * t % DT][e], v1 = kBoth == 2 ? acc[t % DT][(e + 8) % 16] : acc[(2 * t + 1) % DT][e];
-      o[t] = (uint32_t)from_f32<BF16>(v0 * inv) | (uint32_t)from_f32<BF16>(v1 * inv) << 16;
+      o[t] = (uint32_t)from_f32<BF16>(v0 * norm) | (uint32_t)from_f32<BF16>(v1 * norm) << 16;
     }
     __builtin_memcpy(__builtin_assume_aligned(to + VB * (8 * (e >> 2) + 4 * half + (e & 3)), VB * 2), o, VB * 2);
   }
