@@ -33,10 +33,10 @@ constexpr int kManyRows = 32;  // rows of a wave of the first launch when there 
 
 struct LoraPlan {
   bool few;                    // few rows: adapters of a tile over workgroups, low added by its readers
-  int low_tiles;               // row tiles of the first launch: of 16 (few) or 4 * kManyRows rows
-  int up_tiles, up_rows;       // of the second, of 16, 32 or 64 rows
+  int groups;                  // few: groups of one adapter's rows, at most
+  int low_tiles;               // tiles of the first launch: groups, or 4 * kManyRows rows
+  int up_tiles;                // of the second: groups, or 32 or 64 rows
   bool here;                   // few and small: one launch, each workgroup computes low itself
-  int turns;                   // workgroups that share a tile's adapters
   int slices, slice_k;         // parts of K
   int blocks_n, per_n;         // workgroups over N, each per_n times 256 outputs
   size_t part_bytes;           // of the parts; then low's two numbers and the rows' powers of two
@@ -50,18 +50,71 @@ __device__ __forceinline__ int lane_id(const LoraCall& c, int64_t row0, int rows
   return id >= 0 && id < c.bank.adapters ? id : -1;
 }
 
-// Calls f(adapter) for the adapters among `id`, in the order of their first rows: every turns-th
-// one, starting at `turn`.
+// Calls f(adapter) for the adapters among `id`, in the order of their first rows.
 template <typename F>
-__device__ __forceinline__ void each_adapter(int id, int turn, int turns, F f) {
+__device__ __forceinline__ void each_adapter(int id, F f) {
   uint64_t left = __ballot(id >= 0);
-  int nth = 0;
   while (left) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
     left &= ~__ballot(id == a);
-    if (nth % turns == turn) f(a);
-    ++nth;
+    f(a);
   }
+}
+
+// Few rows (at most kFewRows): up to sixteen of one adapter, which need not be neighbours, make a group.
+constexpr int kFewRows = 128;
+struct FewIds {
+  int id[2];      // adapters of rows `lane` and 64 + lane
+};
+__device__ __forceinline__ FewIds few_ids(const LoraCall& c, int lane) {
+  return FewIds{lane_id(c, 0, 64, lane), c.M > 64 ? lane_id(c, 64, 64, lane) : -1};
+}
+struct RowGroup {
+  int adapter;    // -1: there is no such group
+  int row;        // of place lane & 15, -1: none
+};
+// Group `nth`, in the order of the rows that open one: the 1st, 17th, .. of each adapter's.
+__device__ __forceinline__ RowGroup row_group(const LoraCall& c, const FewIds& ids, int lane, int nth) {
+  if (c.M <= 16) {                                   // a row's place is its number
+    uint64_t left = __ballot(ids.id[0] >= 0);
+    for (; left; --nth) {
+      const int a = __builtin_amdgcn_readlane(ids.id[0], __builtin_ctzll(left));
+      if (nth == 0) return RowGroup{a, __shfl(ids.id[0], lane & 15) == a ? lane & 15 : -1};
+      left &= ~__ballot(ids.id[0] == a);
+    }
+    return RowGroup{-1, -1};
+  }
+  // rows of this lane's adapters: among rows 0 .. 63 for row `lane`, among both halves for row 64 + lane
+  const uint64_t below = (1ull << lane) - 1;
+  uint64_t own = __ballot(ids.id[0] >= 0), low = own, high = __ballot(ids.id[1] >= 0);
+  const bool both = high != 0;
+  for (int bit = 0; (c.bank.adapters - 1) >> bit; ++bit) {
+    const uint64_t set0 = __ballot(ids.id[0] >> bit & 1);
+    own &= ids.id[0] >> bit & 1 ? set0 : ~set0;
+    if (both) {
+      const uint64_t set1 = __ballot(ids.id[1] >> bit & 1);
+      low &= ids.id[1] >> bit & 1 ? set0 : ~set0;
+      high &= ids.id[1] >> bit & 1 ? set1 : ~set1;
+    }
+  }
+  const int rank0 = __builtin_popcountll(own & below), rank1 = __builtin_popcountll(low) + __builtin_popcountll(high & below);
+  const bool opens0 = ids.id[0] >= 0 && rank0 % 16 == 0, opens1 = ids.id[1] >= 0 && rank1 % 16 == 0;
+  const uint64_t open0 = __ballot(opens0), open1 = __ballot(opens1);
+  const int n0 = __builtin_popcountll(open0);
+  if (nth >= n0 + __builtin_popcountll(open1)) return RowGroup{-1, -1};
+  const bool here = nth < n0 ? opens0 && __builtin_popcountll(open0 & below) == nth
+                             : opens1 && n0 + __builtin_popcountll(open1 & below) == nth;
+  const int at = __builtin_ctzll(__ballot(here));
+  const int a = __builtin_amdgcn_readlane(nth < n0 ? ids.id[0] : ids.id[1], at);
+  const int first = __builtin_amdgcn_readlane(nth < n0 ? rank0 : rank1, at);
+  // each row's lane sends it to the lane of its place (others to lane 63, which nobody reads)
+  const bool is0 = ids.id[0] == a, is1 = ids.id[1] == a;
+  const int in0 = __builtin_popcountll(__ballot(is0)), n = in0 + __builtin_popcountll(__ballot(is1));
+  const int to0 = is0 && rank0 >= first && rank0 < first + 16 ? rank0 - first : 63;
+  const int to1 = is1 && rank1 >= first && rank1 < first + 16 ? rank1 - first : 63;
+  const int from0 = __builtin_amdgcn_ds_permute(to0 * 4, lane), from1 = __builtin_amdgcn_ds_permute(to1 * 4, 64 + lane);
+  const int place = lane & 15, row = __shfl(lane < in0 - first ? from0 : from1, place);
+  return RowGroup{a, place < n - first ? row : -1};
 }
 
 // Memory is read a row by neighbouring lanes, 64 inputs (128 bytes) by eight of them: lanes that each
@@ -72,10 +125,11 @@ template <int RT, int CT>
 constexpr int kStage = (RT + CT) * 16 * 8;         // 16-byte pieces of a wave's x rows, then A rows
 
 // acc = A_i x over inputs [k0, k1) for CT tiles of 16 rows: ranks 16 r + 4 quad + e of row 16 t + col.
-// Rows and ranks past the last, and inputs past k1, read as 0.
+// x_at[n]: bytes before this lane's piece of row 8 n + lane / 8 (kOob: none; it stays past every resource).  Absent rows, ranks past the
+// last and inputs past k1 read as 0.
 template <int BF16, int RT, int CT>
-__device__ __forceinline__ void low_product(rsrc_t x_rsrc, rsrc_t a_rsrc, int K, int k0, int k1, int lane, u32x4* stage,
-                                            f32x4 (&acc)[RT][CT]) {
+__device__ __forceinline__ void low_product(rsrc_t x_rsrc, const uint32_t (&x_at)[2 * CT], rsrc_t a_rsrc, int K, int k0, int k1,
+                                            int lane, u32x4* stage, f32x4 (&acc)[RT][CT]) {
   const int col = lane & 15, quad = lane >> 4, piece = lane & 7;
   const uint32_t voff = (uint32_t)((lane >> 3) * K + piece * 8) * 2, next = (uint32_t)(8 * K) * 2;
   const int put = (lane >> 3) * 8 + (piece ^ (lane >> 3)), get = col * 8 + (quad ^ (col & 7));
@@ -86,12 +140,31 @@ __device__ __forceinline__ void low_product(rsrc_t x_rsrc, rsrc_t a_rsrc, int K,
   constexpr int kDeep = RT + CT <= 3 ? 4 : RT + CT <= 6 ? 2 : 1;   // steps of 64 whose loads are in flight
   u32x4 xs[kDeep][2 * CT], ws[kDeep][2 * RT];
   auto load = [&](int d, int k) {
-    const uint32_t at = k + piece * 8 < k1 ? voff + (uint32_t)k * 2 : kOob;
+    const bool in = k + piece * 8 < k1;
+    const uint32_t at = in ? voff + (uint32_t)k * 2 : kOob;
 #pragma unroll
-    for (int n = 0; n < 2 * CT; ++n) xs[d][n] = load_b128(x_rsrc, at + n * next, 0);
+    for (int n = 0; n < 2 * CT; ++n) xs[d][n] = load_b128(x_rsrc, in ? x_at[n] + (uint32_t)k * 2 : kOob, 0);
 #pragma unroll
     for (int n = 0; n < 2 * RT; ++n) ws[d][n] = load_b128(a_rsrc, at + n * next, 0);
     __builtin_amdgcn_sched_barrier(0);
+  };
+  // where registers allow, a step's operands are read while the step before is multiplied (first: zeros)
+  constexpr bool kLate = RT + CT <= 3;
+  u32x4 xr[2][CT], wr[2][RT];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int t = 0; t < CT; ++t) xr[h][t] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int r = 0; r < RT; ++r) wr[h][r] = u32x4{0, 0, 0, 0};
+  }
+  auto multiply = [&] {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < CT; ++t) acc[r][t] = mfma16<BF16>(wr[h][r], xr[h][t], acc[r][t]);
   };
 #pragma unroll
   for (int d = 0; d < kDeep; ++d) load(d, k0 + d * 64);
@@ -104,25 +177,45 @@ __device__ __forceinline__ void low_product(rsrc_t x_rsrc, rsrc_t a_rsrc, int K,
       for (int n = 0; n < 2 * RT; ++n) stage[CT * 128 + put + n * 64] = ws[d][n];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // the wave's LDS accesses stay in order
       load(d, k + (d + kDeep) * 64);
+      u32x4 xn[2][CT], wn[2][RT];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        u32x4 xr[CT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t) xr[t] = stage[t * 128 + (get ^ h * 4)];
+        for (int t = 0; t < CT; ++t) xn[h][t] = stage[t * 128 + (get ^ h * 4)];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const u32x4 w = stage[CT * 128 + r * 128 + (get ^ h * 4)];
-#pragma unroll
-          for (int t = 0; t < CT; ++t) acc[r][t] = mfma16<BF16>(w, xr[t], acc[r][t]);
-        }
+        for (int r = 0; r < RT; ++r) wn[h][r] = stage[CT * 128 + r * 128 + (get ^ h * 4)];
       }
+      if constexpr (kLate) multiply();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int t = 0; t < CT; ++t) xr[h][t] = xn[h][t];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) wr[h][r] = wn[h][r];
+      }
+      if constexpr (!kLate) multiply();
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+  if constexpr (kLate) multiply();
 }
 
 __device__ __forceinline__ rsrc_t adapter_a(const LoraCall& c, int a) {
   const int64_t n = (int64_t)c.bank.rank * c.bank.in_features;
   return make_rsrc((const uint16_t*)c.bank.a + a * n, (uint32_t)n * 2);
+}
+
+// x offsets of a lane's two rows (low_product) from the row of lane & 15.
+struct RowOffsets {
+  uint32_t at[2];
+};
+__device__ __forceinline__ RowOffsets row_offsets(int my_row, int lane, int K) {
+  RowOffsets o;
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int row = __shfl(my_row, n * 8 + (lane >> 3));
+    o.at[n] = row < 0 ? kOob : (uint32_t)(row * K + (lane & 7) * 8) * 2;
+  }
+  return o;
 }
 
 // Few rows: part[slice][row][rank] = the slice's share of A_i x, the slice's K over the four waves.
@@ -133,36 +226,28 @@ __global__ void __launch_bounds__(kThreads, 2) lora_low_kernel(LoraCall c, LoraP
   float (*const sums)[16][kPitch] = (float (*)[16][kPitch])stage;     // of the waves, in the same place
   static_assert(sizeof(float) * kWaves * 16 * kPitch <= sizeof(stage), "");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int id = blockIdx.x;
-  const int slice = id % p.slices;
-  id /= p.slices;
-  const int turn = id % p.turns;
-  const int64_t row0 = (int64_t)(id / p.turns) * 16;
+  const int slice = blockIdx.x % p.slices;
   const int K = c.bank.in_features, rank = c.bank.rank;
-  const int my_id = lane_id(c, row0, 16, lane);
   const int k0 = slice * p.slice_k + wave * (p.slice_k / kWaves);
   const int k1 = k0 + p.slice_k / kWaves < K ? k0 + p.slice_k / kWaves : K;
-  const int rows = c.M - row0 < 16 ? (int)(c.M - row0) : 16;
-  const rsrc_t x_rsrc = make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2);
+  const rsrc_t x_rsrc = make_rsrc(c.x, (uint32_t)c.M * K * 2);
   float* part = (float*)c.ws + (int64_t)slice * c.M * rank;
-
-  each_adapter(my_id, turn, p.turns, [&](int a) {
-    f32x4 acc[RT][1];
-    low_product<BF16>(x_rsrc, adapter_a(c, a), K, k0, k1, lane, stage[wave], acc);
-    __syncthreads();                                   // all waves have read their rows
+  const RowGroup g = row_group(c, few_ids(c, lane), lane, blockIdx.x / p.slices);
+  if (g.adapter < 0) return;
+  f32x4 acc[RT][1];
+  low_product<BF16>(x_rsrc, row_offsets(g.row, lane, K).at, adapter_a(c, g.adapter), K, k0, k1, lane, stage[wave], acc);
+  __syncthreads();                                     // all waves have read their rows
 #pragma unroll
-    for (int r = 0; r < RT; ++r) *(f32x4*)&sums[wave][lane & 15][r * 16 + (lane >> 4) * 4] = acc[r][0];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * RT * 16; i += kThreads) {
-      const int row = i / (RT * 16), r = i % (RT * 16);
-      if (__shfl(my_id, row) != a || r >= rank) continue;
-      float s = 0.0f;
+  for (int r = 0; r < RT; ++r) *(f32x4*)&sums[wave][lane & 15][r * 16 + (lane >> 4) * 4] = acc[r][0];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * RT * 16; i += kThreads) {
+    const int at = i / (RT * 16), r = i % (RT * 16), row = __shfl(g.row, at);
+    if (row < 0 || r >= rank) continue;
+    float s = 0.0f;
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) s += sums[v][row][r];
-      part[(row0 + row) * rank + r] = s;
-    }
-    __syncthreads();                                   // the sums are read: rows may come again
-  });
+    for (int v = 0; v < kWaves; ++v) s += sums[v][at][r];
+    part[(int64_t)row * rank + r] = s;
+  }
 }
 
 // Many rows: the same, each wave its own kManyRows rows over all of the slice.
@@ -180,9 +265,12 @@ __global__ void __launch_bounds__(kThreads, 2) lora_low_rows_kernel(LoraCall c, 
   const int rows = c.M - row0 < kManyRows ? (int)(c.M - row0) : kManyRows;
   const rsrc_t x_rsrc = make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2);
   float* part = (float*)c.ws + ((int64_t)slice * c.M + row0) * rank;
-  each_adapter(my_id, 0, 1, [&](int a) {
+  uint32_t x_at[2 * CT];
+#pragma unroll
+  for (int n = 0; n < 2 * CT; ++n) x_at[n] = (uint32_t)((n * 8 + (lane >> 3)) * K + (lane & 7) * 8) * 2;
+  each_adapter(my_id, [&](int a) {
     f32x4 acc[RT][CT];
-    low_product<BF16>(x_rsrc, adapter_a(c, a), K, k0, k1, lane, stage[wave], acc);
+    low_product<BF16>(x_rsrc, x_at, adapter_a(c, a), K, k0, k1, lane, stage[wave], acc);
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       const int row = t * 16 + (lane & 15);
@@ -283,15 +371,15 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
   static_assert(LOW != kLowHere || (CT == 1 && sizeof(float) * kWaves * 16 * kSumPitch <= sizeof(stage)), "");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4, piece = lane & 7;
-  int id = blockIdx.x;
-  const int block_n = id % p.blocks_n;
-  id /= p.blocks_n;
-  const int turn = id % p.turns;
-  const int64_t row0 = (int64_t)(id / p.turns) * kRows;
+  constexpr bool kFew = LOW != kLowJoined;                 // one tile of an adapter's rows, else neighbouring rows
+  static_assert(!kFew || CT == 1, "");
+  const int block_n = blockIdx.x % p.blocks_n, tile_id = blockIdx.x / p.blocks_n;
+  const int64_t row0 = kFew ? 0 : (int64_t)tile_id * kRows;
   const int N = c.bank.out_features, rank = c.bank.rank, pieces = rank / 8;
-  const int my_id = lane_id(c, row0, kRows, lane);
+  const FewIds few = kFew ? few_ids(c, lane) : FewIds{-1, -1};
+  const int my_id = kFew ? -1 : lane_id(c, row0, kRows, lane);
   const int n_first = block_n * p.per_n * 256 + wave * 64;
-  const int rows = c.M - row0 < kRows ? (int)(c.M - row0) : kRows;
+  const int rows = kFew || c.M - row0 < kRows ? (int)(c.M - row0) : kRows;
   const rsrc_t y_rsrc = make_rsrc(c.y + row0 * N, (uint32_t)rows * N * 2);
   const rsrc_t out_rsrc = make_rsrc(c.out + row0 * N, (uint32_t)rows * N * 2);
   u32x4* const b_rows = own[wave];
@@ -301,15 +389,21 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
 #pragma unroll
   for (int j = 0; j < KS * 4; ++j)
     put[j] = j < pieces ? (j * 64 + lane) / pieces * kPitch + (j * 64 + lane) % pieces : kPitch - 1;
-  // y and out: rows 16 m + 8 s + lane / 8
+  // y and out: a lane's rows are 16 m + 8 s + lane / 8 of the tile
   int ids[CT][2];
 #pragma unroll
   for (int m = 0; m < CT; ++m)
 #pragma unroll
-    for (int s = 0; s < 2; ++s) ids[m][s] = __shfl(my_id, m * 16 + s * 8 + (lane >> 3));
+    for (int s = 0; s < 2; ++s) ids[m][s] = kFew ? -1 : __shfl(my_id, m * 16 + s * 8 + (lane >> 3));
 
-  bool first = true;
-  each_adapter(my_id, turn, p.turns, [&](int a) {
+  [[maybe_unused]] bool first = true;
+  auto adapter_rows = [&](int a, int my_row) {             // my_row (few): the row of lane & 15, -1: none
+    int my_rows[CT][2];                                    // this lane's, -1: not the adapter's
+#pragma unroll
+    for (int m = 0; m < CT; ++m)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        my_rows[m][s] = kFew ? __shfl(my_row, s * 8 + (lane >> 3)) : ids[m][s] == a ? m * 16 + s * 8 + (lane >> 3) : -1;
     const rsrc_t b_rsrc = make_rsrc((const uint16_t*)c.bank.b + (int64_t)a * N * rank, (uint32_t)N * rank * 2);
     // past N, and in rows of other adapters: past the resource, read as 0 and not written
     u32x4 b_in[KS * 4], in[CT][2];
@@ -322,21 +416,21 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
       for (int m = 0; m < CT; ++m)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          at[m][s] = ids[m][s] == a && n0 + piece * 8 < N
-                         ? (uint32_t)((m * 16 + s * 8 + (lane >> 3)) * N + n0 + piece * 8) * 2 : kOob;
+          at[m][s] = my_rows[m][s] >= 0 && n0 + piece * 8 < N ? (uint32_t)(my_rows[m][s] * N + n0 + piece * 8) * 2 : kOob;
           in[m][s] = __builtin_amdgcn_raw_buffer_load_b128(y_rsrc, at[m][s], 0, kAux);
         }
       __builtin_amdgcn_sched_barrier(0);
     };
     if (n_first < N) load(n_first);                    // on its way while low is added up
 
-    if (!first) __syncthreads();
+    if (!kFew && !first) __syncthreads();
     first = false;
     if constexpr (LOW == kLowHere) {
       // each wave its part of K
       const int K = c.bank.in_features, k0 = wave * p.slice_k, k1 = k0 + p.slice_k < K ? k0 + p.slice_k : K;
       f32x4 acc[kRanks][1];
-      low_product<BF16>(make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2), adapter_a(c, a), K, k0, k1, lane, stage[wave], acc);
+      low_product<BF16>(make_rsrc(c.x, (uint32_t)rows * K * 2), row_offsets(my_row, lane, K).at, adapter_a(c, a), K, k0, k1, lane,
+                        stage[wave], acc);
       __syncthreads();                                   // all waves have read their rows
 #pragma unroll
       for (int r = 0; r < kRanks; ++r) *(f32x4*)&sums[wave][col][r * 16 + quad * 4] = acc[r][0];
@@ -354,19 +448,17 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
         if (!BF16 && r == 0) scaled[row] = mine ? ((const float*)(from + 2 * c.M * rank))[row0 + row] : 1.0f;
       }
     } else {
-      // wave w takes row tiles w, w + 4
-      for (int t = wave; t < CT; t += kWaves) {
+      if (wave == 0) {
         float low[KS][8], most = 0.0f;
-        const bool mine = __shfl(my_id, t * 16 + col) == a;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) low[k][e] = 0.0f;
-          if (mine && k * 32 + quad * 8 < rank) {
+          if (my_row >= 0 && k * 32 + quad * 8 < rank) {
             if constexpr (LOW == kLowHere)
               add_parts(&sums[0][col][k * 32 + quad * 8], kWaves, 16 * kSumPitch, c.bank.scale[a], low[k]);
             else
-              add_parts((const float*)c.ws + (row0 + t * 16 + col) * rank + k * 32 + quad * 8, p.slices, c.M * rank,
+              add_parts((const float*)c.ws + (int64_t)my_row * rank + k * 32 + quad * 8, p.slices, c.M * rank,
                         c.bank.scale[a], low[k]);
           }
           most = __builtin_fmaxf(most, largest8(low[k]));
@@ -377,11 +469,11 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
           most = __builtin_fmaxf(most, __shfl_xor(most, 32));
           const int e = row_exponent(most);
           down = __builtin_ldexpf(1.0f, -e);
-          if (quad == 0) scaled[t * 16 + col] = __builtin_ldexpf(1.0f, e);
+          if (quad == 0) scaled[col] = __builtin_ldexpf(1.0f, e);
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const int to = (t * 16 + col) * kPitch + k * 4 + quad;
+          const int to = col * kPitch + k * 4 + quad;
           split8<BF16>(low[k], down, &lows[0][to], &lows[1][to]);
         }
       }
@@ -438,50 +530,56 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
       }
       if (i + 1 < p.per_n && n_first + (i + 1) * 256 < N) load(n_first + (i + 1) * 256);
     }
-  });
-  // rows without an adapter
-  if (turn != 0 || c.out == c.y) return;
-#pragma unroll
-  for (int m = 0; m < CT; ++m)
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int64_t row = row0 + m * 16 + s * 8 + (lane >> 3);
-      if (ids[m][s] >= 0 || row >= c.M) continue;
-      for (int i = 0; i < p.per_n; ++i) {
-        const int n = n_first + i * 256 + piece * 8;
-        if (n >= N) break;
-        *(u32x4*)(c.out + row * N + n) = *(const u32x4*)(c.y + row * N + n);
-      }
+  };
+  if constexpr (kFew) {
+    const RowGroup g = row_group(c, few, lane, tile_id);
+    if (g.adapter >= 0) adapter_rows(g.adapter, g.row);
+  } else {
+    each_adapter(my_id, [&](int a) { adapter_rows(a, -1); });
+  }
+
+  // rows without an adapter, eight at a time
+  if (c.out == c.y) return;
+  for (int j = kFew ? tile_id : 0; j * 8 < rows; j += kFew ? p.groups : 1) {
+    const int r = j * 8 + (lane >> 3);
+    const int id = kFew ? __shfl(j < 8 ? few.id[0] : few.id[1], r & 63) : __shfl(my_id, r);
+    if (id >= 0 || r >= rows) continue;
+    for (int i = 0; i < p.per_n; ++i) {
+      const int n = n_first + i * 256 + piece * 8;
+      if (n >= N) break;
+      *(u32x4*)(c.out + (row0 + r) * N + n) = *(const u32x4*)(c.y + (row0 + r) * N + n);
     }
+  }
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 LoraPlan plan_of(const gptq_lora_bank& bank, int64_t M) {
   LoraPlan p;
-  p.few = M <= 128;
-  p.up_rows = p.few ? 16 : bank.rank > 64 ? 32 : 64;
-  p.low_tiles = (int)div_up(M, p.few ? 16 : kWaves * kManyRows);
-  p.up_tiles = (int)div_up(M, p.up_rows);
-  int64_t turns = p.few ? (M < 16 ? M : 16) : 1;
-  if (turns > bank.adapters) turns = bank.adapters;
-  p.turns = (int)turns;
+  p.few = M <= kFewRows;
+  // groups of rows, at most: each row may open one, and each adapter has one that is not full
+  const int64_t most = M / 16 + bank.adapters, groups = M < most ? M : most;
+  p.groups = (int)groups;
+  p.low_tiles = (int)(p.few ? groups : div_up(M, kWaves * kManyRows));
+  p.up_tiles = (int)(p.few ? groups : div_up(M, bank.rank > 64 ? 32 : 64));
   // K: enough workgroups to fill the card, slices of at least 64 values a wave
-  const int64_t units = p.low_tiles * turns, step = p.few ? 64 * kWaves : 64, steps = div_up(bank.in_features, step);
+  const int64_t units = p.low_tiles, step = p.few ? 64 * kWaves : 64, steps = div_up(bank.in_features, step);
   int64_t slices = div_up(256, units);
   if (slices > 16) slices = 16;
   if (slices > steps) slices = steps;
   p.slice_k = (int)(div_up(steps, slices) * step);
   p.slices = (int)div_up(bank.in_features, p.slice_k);
   const int64_t blocks = div_up(bank.out_features, 256);
-  int64_t per = p.up_tiles * turns * blocks / 1536;
+  // few: all workgroups on the card at once; many: half as many again as there is room for
+  const int64_t fit = bank.rank <= 32 ? 1024 : bank.rank <= 64 ? 768 : 512;
+  int64_t per = p.few ? div_up(p.up_tiles * blocks, fit) : p.up_tiles * blocks / 1536;
   p.per_n = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
   p.blocks_n = (int)div_up(blocks, p.per_n);
   // One launch while its workgroups have a CU each and A_i is small, since each reads all of it.  Us on the
   // device, one launch against two, rank 8, 1 row: K = 1024 4.9 / 6.8, 4096 7.1 / 8.0, 5120 7.8 / 7.6, 6144
   // 8.6 / 7.8 (the second launch costs the host 2.7 more); K = 4096, N = 14336, 4 rows (224 workgroups)
   // 7.4 / 8.2, 8 rows (448) 11.5 / 8.6.  Eight waves that share K instead of four: 7.9 at K = 4096.
-  p.here = p.few && bank.rank <= 32 && bank.in_features <= 5120 && p.up_tiles * turns * p.blocks_n <= 256;
+  p.here = p.few && bank.rank <= 32 && bank.in_features <= 5120 && groups * p.blocks_n <= 256;
   if (p.here) p.slice_k = (int)(div_up(div_up(bank.in_features, 64), kWaves) * 64);
   p.part_bytes = p.here ? 0 : (size_t)div_up((int64_t)p.slices * M * bank.rank * 4, 256) * 256;
   return p;
@@ -489,14 +587,14 @@ LoraPlan plan_of(const gptq_lora_bank& bank, int64_t M) {
 
 template <int BF16, int RT>
 void launch_low(const LoraCall& c, const LoraPlan& p, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)p.low_tiles * p.turns * p.slices)), block(kThreads);
+  const dim3 grid((uint32_t)((int64_t)p.low_tiles * p.slices)), block(kThreads);
   if (p.few) lora_low_kernel<BF16, RT><<<grid, block, 0, s>>>(c, p);
   else lora_low_rows_kernel<BF16, RT><<<grid, block, 0, s>>>(c, p);
 }
 
 template <int BF16, int KS>
 void launch_up(const LoraCall& c, const LoraPlan& p, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)p.up_tiles * p.turns * p.blocks_n)), block(kThreads);
+  const dim3 grid((uint32_t)((int64_t)p.up_tiles * p.blocks_n)), block(kThreads);
   if (p.here) {
     if constexpr (KS == 1) lora_up_kernel<BF16, KS, 1, kLowHere><<<grid, block, 0, s>>>(c, p);
   } else if (p.few) {
@@ -510,7 +608,7 @@ void launch_up(const LoraCall& c, const LoraPlan& p, hipStream_t s) {
 template <int BF16>
 hipError_t launch_type(const LoraCall& c, hipStream_t s) {
   const LoraPlan p = plan_of(c.bank, c.M);
-  if ((int64_t)p.low_tiles * p.turns * p.slices > 0x7fffffff || (int64_t)p.up_tiles * p.turns * p.blocks_n > 0x7fffffff)
+  if ((int64_t)p.low_tiles * p.slices > 0x7fffffff || (int64_t)p.up_tiles * p.blocks_n > 0x7fffffff)
     return hipErrorInvalidConfiguration;
   const int rank = c.bank.rank;
   if (p.here) ;
