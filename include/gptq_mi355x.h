@@ -430,7 +430,7 @@ typedef struct {
 
 /* out[m] = y[m] + scale[i] * B_i (A_i x[m]) with i = ids[m]: y is the shared projection's output
  * (gptq_gemm), x its input.  Rows whose id is outside [0, adapters) keep y (-1: no adapter).  The
- * rows' adapters may come in any order; rows of one adapter next to each other share its reads.
+ * rows' adapters may come in any order (calls of more than 1024 rows are quick when they come in runs).
  *   x [M, K], y and out [M, N], row-major, 16-byte aligned; out may be y, and must not otherwise
  *   overlap anything.  ids int32 [M].
  * Both products accumulate in float32; A_i x[m] is kept to 16 bits or more for the second, and out

@@ -124,6 +124,11 @@ ATTENTION = [
     ([257], [257], 256, 1, 1, 64, "bf16", True, 1),                   # a window of the token itself
     ([520, 64, 511], [260, 64, 1], 16, 1, 4, 128, "f16", True, 300),
     ([1025], [33], 16, 1, 32, 64, "f16", True, 0),
+    ([5000, 3000, 0, 1500], [40, 70, 0, 3], 16, 2, 8, 128, "bf16", True, 0),     # many columns, keys split
+    ([2200, 90], [300, 90], 64, 1, 4, 64, "f16", True, 0),
+    ([4000, 2500], [65, 64], 32, 2, 12, 128, "f16", True, 1700),
+    ([1800], [200], 128, 1, 2, 128, "bf16", False, 0),
+    ([600, 500, 40], [90, 200, 40], 16, 3, 12, 128, "bf16", True, 0),            # short: not split
 ]
 
 

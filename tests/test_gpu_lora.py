@@ -78,6 +78,7 @@ CASES = [
     (5, 14336, 128, 16, 2, "f16"), (1, 28672, 64, 128, 2, "bf16"),
     (16, 5120, 480, 32, 16, "f16"), (16, 5152, 480, 24, 16, "bf16"), (9, 5088, 7328, 8, 9, "f16"), (8, 96, 8192, 32, 8, "bf16"),
     (9, 96, 8192, 32, 9, "f16"), (127, 1024, 96, 32, 30, "bf16"), (128, 1056, 288, 40, 3, "f16"), (129, 1056, 288, 40, 3, "f16"),
+    (192, 512, 320, 16, 90, "bf16"), (255, 288, 1056, 72, 4, "f16"), (256, 1024, 544, 64, 300, "bf16"), (256, 256, 128, 8, 1, "f16"),
 ]
 
 

@@ -13,6 +13,13 @@
 // the waves turn their shares into float16 and put them into LDS, keys two steps ahead and values
 // one, while the products of the next tile's scores run under this tile's exponentials and the
 // products with the values under the next tile's exponents.  One barrier a step.
+//
+// Measured: one prompt of 8192 tokens, 32 query heads of 128 on 8 kv heads: 594 us, 925 TFLOP/s of the 1275
+// that a large float16 product reaches; chunks of five prompts (115 GFLOP): 157 us.  The matrix cores are
+// busy 43 % of the time, the vector units 55 %, LDS 32 %; waves wait for their turn to issue 32 % and for
+// memory, LDS or the barrier 29 %.  Without reads of operands the same work takes 317 us, with them 484
+// without staging, barrier and the test for hidden tokens, which cost 90, 30 and 38.  A wave with twice the
+// columns (half the operand reads, one wave a SIMD): 667.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -351,6 +358,8 @@ hipError_t launch_kv_prefill(const KvAttentionCall& a, hipStream_t s) {
   const int page_shift = __builtin_ctz(a.c.page_size);
   const bool bf16 = a.a.dtype == GPTQ_BF16;
   if (a.c.head_dim == 64) return bf16 ? launch_waves<1, 64, 4>(a, page_shift, s) : launch_waves<0, 64, 4>(a, page_shift, s);
+  // eight waves share the conversion of a tile: with a workgroup for every CU or more (us, 8 waves / 4: 8192
+  // tokens, 32 heads 594 / 615), and the smaller workgroups fill the card better before (2048 tokens 62 / 59)
   if (a.b.rows * a.a.q_heads >= 256 * 512)
     return bf16 ? launch_waves<1, 128, 8>(a, page_shift, s) : launch_waves<0, 128, 8>(a, page_shift, s);
   return bf16 ? launch_waves<1, 128, 4>(a, page_shift, s) : launch_waves<0, 128, 4>(a, page_shift, s);

@@ -8,16 +8,21 @@
 // once; prompts read x and y and write out.  Both products run on v_mfma_f32_16x16x32 with columns =
 // rows of x, straight from memory to registers: rows of A_i (or B_i) are the other operand.
 //
-// Rows in any order: a wave or workgroup takes 16 to 64 neighbouring rows and goes through the
-// adapters that occur among them, keeping each product for its own adapter's rows (so no row meets
-// another's values, not even times zero).  With few rows the adapters of a tile go to several
-// workgroups.
+// Rows in any order.  Up to 1024 rows (tokens of many requests): a workgroup takes up to sixteen rows
+// of one adapter, gathered from wherever they stand among 128.  More (prompts): a wave or workgroup takes
+// 32 or 64 neighbouring rows and goes through the adapters that occur among them, keeping each product
+// for its own adapter's rows (so no row meets another's values, not even times zero).
 //
 // Sums over K are split: with few rows over the waves of a workgroup and over workgroups, whose
 // parts the second launch adds in order; with many rows over workgroups only, whose waves take
 // different rows and meet in the first-level cache over A_i, and a small launch in between adds the
 // parts once.  low goes into the second product as two 16-bit numbers (value and remainder, float16
 // after a power-of-two scaling of the row): 16 bits or more for one more product.
+//
+// Measured (the device's time): 1 row, rank 16, 4096 x 14336, one launch: 7.8 us, most of it two trips to
+// memory and the pass over A_i.  61 rows of 48 adapters, rank 32, 8192 x 28672 (86 MB): 6.6 + 15.8 us, 4.4
+// TB/s in the second launch.  4001 rows in 9 runs, rank 64, 4096 x 14336 (271 MB): 12.5 + 4.7 + 59 us, 3.9
+// TB/s of y and out against 4.9 of a copy.
 #include <hip/hip_runtime.h>
 
 #include "bufmem.h"
@@ -33,7 +38,7 @@ constexpr int kManyRows = 32;  // rows of a wave of the first launch when there 
 
 struct LoraPlan {
   bool few;                    // few rows: adapters of a tile over workgroups, low added by its readers
-  int groups;                  // few: groups of one adapter's rows, at most
+  int groups;                  // few: groups of a chunk's rows, at most
   int low_tiles;               // tiles of the first launch: groups, or 4 * kManyRows rows
   int up_tiles;                // of the second: groups, or 32 or 64 rows
   bool here;                   // few and small: one launch, each workgroup computes low itself
@@ -61,60 +66,74 @@ __device__ __forceinline__ void each_adapter(int id, F f) {
   }
 }
 
-// Few rows (at most kFewRows): up to sixteen of one adapter, which need not be neighbours, make a group.
-constexpr int kFewRows = 128;
-struct FewIds {
-  int id[2];      // adapters of rows `lane` and 64 + lane
-};
-__device__ __forceinline__ FewIds few_ids(const LoraCall& c, int lane) {
-  return FewIds{lane_id(c, 0, 64, lane), c.M > 64 ? lane_id(c, 64, 64, lane) : -1};
-}
+// Few rows, in chunks of kChunk: up to sixteen rows of one adapter, which need not be neighbours, make a
+// group.  (Chunks of 256 read an adapter less often, but looking for groups among so many, and the code
+// for it, cost all calls: rank 64, 4096 x 14336, us with 128 / 256: 4 rows 11.3 / 12.1, 256 in runs 19.5 /
+// 19.9, 256 of 48 adapters 47 / 38.)
+constexpr int kChunk = 128;
 struct RowGroup {
   int adapter;    // -1: there is no such group
-  int row;        // of place lane & 15, -1: none
+  int row;        // within the chunk, of place lane & 15, -1: none
 };
-// Group `nth`, in the order of the rows that open one: the 1st, 17th, .. of each adapter's.
-__device__ __forceinline__ RowGroup row_group(const LoraCall& c, const FewIds& ids, int lane, int nth) {
-  if (c.M <= 16) {                                   // a row's place is its number
-    uint64_t left = __ballot(ids.id[0] >= 0);
-    for (; left; --nth) {
-      const int a = __builtin_amdgcn_readlane(ids.id[0], __builtin_ctzll(left));
-      if (nth == 0) return RowGroup{a, __shfl(ids.id[0], lane & 15) == a ? lane & 15 : -1};
-      left &= ~__ballot(ids.id[0] == a);
-    }
-    return RowGroup{-1, -1};
-  }
-  // rows of this lane's adapters: among rows 0 .. 63 for row `lane`, among both halves for row 64 + lane
+// Group `nth` of rows [row0, row0 + rows), in the order of the rows that open one: the 1st, 17th, .. of each
+// adapter's.  rows <= 64 PARTS.
+template <int PARTS>
+__device__ __forceinline__ RowGroup group_among(const LoraCall& c, int64_t row0, int rows, int lane, int nth) {
+  int id[PARTS];
+#pragma unroll
+  for (int h = 0; h < PARTS; ++h) id[h] = lane_id(c, row0 + h * 64, rows - h * 64, lane);
+  // same[h][g]: rows 64 g + .. that have the adapter of this lane's row 64 h + lane
   const uint64_t below = (1ull << lane) - 1;
-  uint64_t own = __ballot(ids.id[0] >= 0), low = own, high = __ballot(ids.id[1] >= 0);
-  const bool both = high != 0;
-  for (int bit = 0; (c.bank.adapters - 1) >> bit; ++bit) {
-    const uint64_t set0 = __ballot(ids.id[0] >> bit & 1);
-    own &= ids.id[0] >> bit & 1 ? set0 : ~set0;
-    if (both) {
-      const uint64_t set1 = __ballot(ids.id[1] >> bit & 1);
-      low &= ids.id[1] >> bit & 1 ? set0 : ~set0;
-      high &= ids.id[1] >> bit & 1 ? set1 : ~set1;
+  uint64_t same[PARTS][PARTS];
+#pragma unroll
+  for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+    for (int g = 0; g <= h; ++g) same[h][g] = __ballot(id[g] >= 0);
+  for (int bit = 0; (c.bank.adapters - 1) >> bit; ++bit)
+#pragma unroll
+    for (int g = 0; g < PARTS; ++g) {
+      const uint64_t set = __ballot(id[g] >> bit & 1);
+#pragma unroll
+      for (int h = g; h < PARTS; ++h) same[h][g] &= id[h] >> bit & 1 ? set : ~set;
+    }
+  int rank[PARTS], opened = 0, a = -1, first = 0;
+#pragma unroll
+  for (int h = 0; h < PARTS; ++h) {
+    rank[h] = __builtin_popcountll(same[h][h] & below);
+#pragma unroll
+    for (int g = 0; g < h; ++g) rank[h] += __builtin_popcountll(same[h][g]);
+    const bool opens = id[h] >= 0 && rank[h] % 16 == 0;
+    const uint64_t open = __ballot(opens), it = __ballot(opens && opened + __builtin_popcountll(open & below) == nth);
+    opened += __builtin_popcountll(open);
+    if (it) {
+      a = __builtin_amdgcn_readlane(id[h], __builtin_ctzll(it));
+      first = __builtin_amdgcn_readlane(rank[h], __builtin_ctzll(it));
     }
   }
-  const int rank0 = __builtin_popcountll(own & below), rank1 = __builtin_popcountll(low) + __builtin_popcountll(high & below);
-  const bool opens0 = ids.id[0] >= 0 && rank0 % 16 == 0, opens1 = ids.id[1] >= 0 && rank1 % 16 == 0;
-  const uint64_t open0 = __ballot(opens0), open1 = __ballot(opens1);
-  const int n0 = __builtin_popcountll(open0);
-  if (nth >= n0 + __builtin_popcountll(open1)) return RowGroup{-1, -1};
-  const bool here = nth < n0 ? opens0 && __builtin_popcountll(open0 & below) == nth
-                             : opens1 && n0 + __builtin_popcountll(open1 & below) == nth;
-  const int at = __builtin_ctzll(__ballot(here));
-  const int a = __builtin_amdgcn_readlane(nth < n0 ? ids.id[0] : ids.id[1], at);
-  const int first = __builtin_amdgcn_readlane(nth < n0 ? rank0 : rank1, at);
+  if (a < 0) return RowGroup{-1, -1};
   // each row's lane sends it to the lane of its place (others to lane 63, which nobody reads)
-  const bool is0 = ids.id[0] == a, is1 = ids.id[1] == a;
-  const int in0 = __builtin_popcountll(__ballot(is0)), n = in0 + __builtin_popcountll(__ballot(is1));
-  const int to0 = is0 && rank0 >= first && rank0 < first + 16 ? rank0 - first : 63;
-  const int to1 = is1 && rank1 >= first && rank1 < first + 16 ? rank1 - first : 63;
-  const int from0 = __builtin_amdgcn_ds_permute(to0 * 4, lane), from1 = __builtin_amdgcn_ds_permute(to1 * 4, 64 + lane);
-  const int place = lane & 15, row = __shfl(lane < in0 - first ? from0 : from1, place);
-  return RowGroup{a, place < n - first ? row : -1};
+  int row = -1, before = 0;
+#pragma unroll
+  for (int h = 0; h < PARTS; ++h) {
+    const bool mine = id[h] == a && rank[h] >= first && rank[h] < first + 16;
+    const int from = __builtin_amdgcn_ds_permute((mine ? rank[h] - first : 63) * 4, h * 64 + lane);
+    const int n = __builtin_popcountll(__ballot(mine));
+    row = lane >= before && lane < before + n ? from : row;
+    before += n;
+  }
+  return RowGroup{a, __shfl(row, lane & 15)};
+}
+__device__ __forceinline__ RowGroup row_group(const LoraCall& c, int64_t row0, int rows, int lane, int nth) {
+  if (rows > 64) return group_among<2>(c, row0, rows, lane, nth);
+  if (rows > 16) return group_among<1>(c, row0, rows, lane, nth);
+  // a row's place is its number
+  const int id = lane_id(c, row0, rows, lane);
+  for (uint64_t left = __ballot(id >= 0); left; --nth) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    if (nth == 0) return RowGroup{a, __shfl(id, lane & 15) == a ? lane & 15 : -1};
+    left &= ~__ballot(id == a);
+  }
+  return RowGroup{-1, -1};
 }
 
 // Memory is read a row by neighbouring lanes, 64 inputs (128 bytes) by eight of them: lanes that each
@@ -230,9 +249,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_low_kernel(LoraCall c, LoraP
   const int K = c.bank.in_features, rank = c.bank.rank;
   const int k0 = slice * p.slice_k + wave * (p.slice_k / kWaves);
   const int k1 = k0 + p.slice_k / kWaves < K ? k0 + p.slice_k / kWaves : K;
-  const rsrc_t x_rsrc = make_rsrc(c.x, (uint32_t)c.M * K * 2);
-  float* part = (float*)c.ws + (int64_t)slice * c.M * rank;
-  const RowGroup g = row_group(c, few_ids(c, lane), lane, blockIdx.x / p.slices);
+  const int tile_id = blockIdx.x / p.slices;
+  const int chunk = c.M <= kChunk ? 0 : tile_id / p.groups;
+  const int64_t row0 = (int64_t)chunk * kChunk;
+  const int rows = c.M - row0 < kChunk ? (int)(c.M - row0) : kChunk;
+  const rsrc_t x_rsrc = make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2);
+  float* part = (float*)c.ws + ((int64_t)slice * c.M + row0) * rank;
+  const RowGroup g = row_group(c, row0, rows, lane, tile_id - chunk * p.groups);
   if (g.adapter < 0) return;
   f32x4 acc[RT][1];
   low_product<BF16>(x_rsrc, row_offsets(g.row, lane, K).at, adapter_a(c, g.adapter), K, k0, k1, lane, stage[wave], acc);
@@ -374,12 +397,12 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
   constexpr bool kFew = LOW != kLowJoined;                 // one tile of an adapter's rows, else neighbouring rows
   static_assert(!kFew || CT == 1, "");
   const int block_n = blockIdx.x % p.blocks_n, tile_id = blockIdx.x / p.blocks_n;
-  const int64_t row0 = kFew ? 0 : (int64_t)tile_id * kRows;
+  const int chunk = !kFew || c.M <= kChunk ? 0 : tile_id / p.groups, nth = tile_id - chunk * p.groups;
+  const int64_t row0 = kFew ? (int64_t)chunk * kChunk : (int64_t)tile_id * kRows;
   const int N = c.bank.out_features, rank = c.bank.rank, pieces = rank / 8;
-  const FewIds few = kFew ? few_ids(c, lane) : FewIds{-1, -1};
   const int my_id = kFew ? -1 : lane_id(c, row0, kRows, lane);
   const int n_first = block_n * p.per_n * 256 + wave * 64;
-  const int rows = kFew || c.M - row0 < kRows ? (int)(c.M - row0) : kRows;
+  const int rows = c.M - row0 < (kFew ? kChunk : kRows) ? (int)(c.M - row0) : kFew ? kChunk : kRows;
   const rsrc_t y_rsrc = make_rsrc(c.y + row0 * N, (uint32_t)rows * N * 2);
   const rsrc_t out_rsrc = make_rsrc(c.out + row0 * N, (uint32_t)rows * N * 2);
   u32x4* const b_rows = own[wave];
@@ -429,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
       // each wave its part of K
       const int K = c.bank.in_features, k0 = wave * p.slice_k, k1 = k0 + p.slice_k < K ? k0 + p.slice_k : K;
       f32x4 acc[kRanks][1];
-      low_product<BF16>(make_rsrc(c.x, (uint32_t)rows * K * 2), row_offsets(my_row, lane, K).at, adapter_a(c, a), K, k0, k1, lane,
+      low_product<BF16>(make_rsrc(c.x + row0 * K, (uint32_t)rows * K * 2), row_offsets(my_row, lane, K).at, adapter_a(c, a), K, k0, k1, lane,
                         stage[wave], acc);
       __syncthreads();                                   // all waves have read their rows
 #pragma unroll
@@ -458,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
             if constexpr (LOW == kLowHere)
               add_parts(&sums[0][col][k * 32 + quad * 8], kWaves, 16 * kSumPitch, c.bank.scale[a], low[k]);
             else
-              add_parts((const float*)c.ws + (int64_t)my_row * rank + k * 32 + quad * 8, p.slices, c.M * rank,
+              add_parts((const float*)c.ws + (row0 + my_row) * rank + k * 32 + quad * 8, p.slices, c.M * rank,
                         c.bank.scale[a], low[k]);
           }
           most = __builtin_fmaxf(most, largest8(low[k]));
@@ -532,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
     }
   };
   if constexpr (kFew) {
-    const RowGroup g = row_group(c, few, lane, tile_id);
+    const RowGroup g = row_group(c, row0, rows, lane, nth);
     if (g.adapter >= 0) adapter_rows(g.adapter, g.row);
   } else {
     each_adapter(my_id, [&](int a) { adapter_rows(a, -1); });
@@ -540,10 +563,10 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
 
   // rows without an adapter, eight at a time
   if (c.out == c.y) return;
-  for (int j = kFew ? tile_id : 0; j * 8 < rows; j += kFew ? p.groups : 1) {
+  for (int j = kFew ? nth : 0; j * 8 < rows; j += kFew ? p.groups : 1) {
     const int r = j * 8 + (lane >> 3);
-    const int id = kFew ? __shfl(j < 8 ? few.id[0] : few.id[1], r & 63) : __shfl(my_id, r);
-    if (id >= 0 || r >= rows) continue;
+    const int id = kFew ? r < rows ? c.ids[row0 + r] : -1 : __shfl(my_id, r);
+    if ((id >= 0 && id < c.bank.adapters) || r >= rows) continue;
     for (int i = 0; i < p.per_n; ++i) {
       const int n = n_first + i * 256 + piece * 8;
       if (n >= N) break;
@@ -556,10 +579,15 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 LoraPlan plan_of(const gptq_lora_bank& bank, int64_t M) {
   LoraPlan p;
-  p.few = M <= kFewRows;
-  // groups of rows, at most: each row may open one, and each adapter has one that is not full
-  const int64_t most = M / 16 + bank.adapters, groups = M < most ? M : most;
-  p.groups = (int)groups;
+  // Few: every adapter of a chunk is read once for each sixteen of its rows, in whatever order they come.
+  // Many: a tile goes through the adapters among its rows, good for long runs only.  Us, few / many, rank
+  // 64, 4096 x 14336: 129 rows, 48 adapters 36 / 219, 6 in runs 17 / 28; 1024 rows 127 / 374, 32 / 33; 2048
+  // rows 241 / 631, 66 / 49; 4001 rows 453 / 1092, 102 / 71: over 1024 rows are taken to be prompts.
+  p.few = M <= 1024;
+  // groups of a chunk, at most: each row may open one, and each adapter has one that is not full
+  const int64_t chunk = M < kChunk ? M : kChunk, most = chunk / 16 + bank.adapters;
+  p.groups = (int)(chunk < most ? chunk : most);
+  const int64_t groups = div_up(M, kChunk) * p.groups;
   p.low_tiles = (int)(p.few ? groups : div_up(M, kWaves * kManyRows));
   p.up_tiles = (int)(p.few ? groups : div_up(M, bank.rank > 64 ? 32 : 64));
   // K: enough workgroups to fill the card, slices of at least 64 values a wave

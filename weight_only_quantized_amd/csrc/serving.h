@@ -33,6 +33,12 @@ struct KvAttentionCall {
   uint16_t* out;
   void* ws;
 };
+// Tokens that the rows of one sequence can see, at most.
+inline int64_t kv_span(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  const int64_t room = (int64_t)b.table_width * c.page_size, span = a.max_kv < room ? a.max_kv : room;
+  const int64_t windowed = (int64_t)a.window + b.max_rows;
+  return a.causal && a.window > 0 && windowed < span ? windowed : span;
+}
 // Few rows a sequence (kv_decode.hip): split over the keys, joined by a second launch.
 size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
 hipError_t launch_kv_decode(const KvAttentionCall& a, hipStream_t s);
