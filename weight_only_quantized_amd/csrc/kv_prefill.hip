@@ -16,7 +16,7 @@
 //
 // Measured: one prompt of 8192 tokens, 32 query heads of 128 on 8 kv heads: 594 us, 925 TFLOP/s of the 1275
 // that a large float16 product reaches; chunks of five prompts (115 GFLOP): 157 us.  The matrix cores are
-// busy 43 % of the time, the vector units 55 %, LDS 32 %; waves wait for their turn to issue 32 % and for
+// busy 44 % of the time, the vector units 50 %, LDS 33 %; waves wait for their turn to issue 32 % and for
 // memory, LDS or the barrier 29 %.  Without reads of operands the same work takes 317 us, with them 484
 // without staging, barrier and the test for hidden tokens, which cost 90, 30 and 38.  A wave with twice the
 // columns (half the operand reads, one wave a SIMD): 667.
