@@ -160,6 +160,18 @@ def test_attention_random_shapes(seed):
            scale=None if seed % 3 else 0.3)
 
 
+def test_calls_that_differ_in_causality_only():
+    """With a window the keys that a call may see, and its workspace with them, follow from causality too."""
+    import torch
+    pool = Pool([6000, 2000], 16, 2, 64, seed=8)
+    for causal in (True, False, True):
+        cache = pool.cache() if causal else cache  # the same object for the first two calls
+        cu, lens = offsets([1, 1]), [6000, 2000]
+        q = dev(np.random.default_rng(1).normal(0, 1, (2, 4, 64)), torch.float16)
+        out = cache.attention(q, dev(pool.table), dev(np.asarray(lens, np.int32)), dev(cu), max_q=1, window=40, causal=causal)
+        check_attention(host(out), host(q), pool, lens, cu, "f16", 64 ** -0.5, causal, 40)
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_attention_few_rows_long(seed):
     """A few rows each over thousands of tokens, sequences of very different lengths among them."""

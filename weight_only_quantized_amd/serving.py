@@ -35,32 +35,24 @@ _ATTENTION = struct.Struct("iifiiiqq")     # gptq_attention
 _BANK = struct.Struct("PPPiiiiii")         # gptq_lora_bank
 
 
-def _on(stream, index, tensors):
-    """The hipStream_t to queue on, and the context to queue in (None: the current stream of the
-    current device, where nothing has to wait or be recorded)."""
-    if stream is None and torch._C._cuda_getDevice() == index:
-        return torch._C._cuda_getCurrentRawStream(index), None
-    on = _OnStream(stream, torch.device("cuda", index))
-    on.tensors = tensors
-    return on.stream.cuda_stream, on
+def _here(stream, index):
+    """The hipStream_t to queue on when nothing has to wait or be recorded: no stream given, and the
+    tensors' device is the current one.  Else None."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None and torch._C._cuda_getDevice() == index else None
 
 
-class _Queue:
+class _Queue(_OnStream):
     """`with _Queue(stream, index, *tensors) as ptr`: ptr is the stream, and everything inside is
     allocated and queued on it after the current stream's work."""
-    __slots__ = ("ptr", "on")
 
     def __init__(self, stream, index, *tensors):
-        self.ptr, self.on = _on(stream, index, tensors)
+        super().__init__(stream, torch.device("cuda", index))
+        self.tensors = tensors
 
     def __enter__(self):
-        if self.on is not None:
-            self.on.__enter__()
-            self.on.keep(*self.on.tensors)
-        return self.ptr
-
-    def __exit__(self, *exc):
-        return self.on.__exit__(*exc) if self.on is not None else None
+        super().__enter__()
+        self.keep(*self.tensors)
+        return self.stream.cuda_stream
 
 
 def _index(t, name, shape, device):
@@ -84,6 +76,8 @@ def _packed(t, name, heads, dim, dtype, device):
         raise ValueError(f"{name} must be [rows, {heads}, {dim}]")
     if t.dtype is not dtype or t.get_device() != device:
         raise TypeError(f"{name} must be {dtype} on cuda:{device}")
+    if t.is_contiguous() and not t.data_ptr() & 15:
+        return t, heads * dim
     stride = _row_stride(t, shape)
     if stride:
         return t, stride
@@ -149,9 +143,9 @@ class KVCache:
         device, shape = self._index, page_table.shape
         if len(shape) != 2:
             raise ValueError("page_table must be [batch, pages]")
-        n = shape[0]
+        n, width = shape
         return _BATCH.pack(_index(page_table, "page_table", shape, device), _index(at, "lengths", (n,), device),
-                           _index(cu, "cu", (n + 1,), device), rows, n, shape[1], max_rows if max_rows < rows else rows, 0)
+                           _index(cu, "cu", (n + 1,), device), rows, n, width, max_rows if max_rows < rows else rows, 0)
 
     def _raise(self, st, where):
         raise GPTQError(st, where, self._lib)
@@ -163,46 +157,52 @@ class KVCache:
         [positions, rot / 2]) k is rotated at its position, and q [rows, q_heads, head_dim] too; the
         rotated q is returned (in q_out when given, which may be q).  Rotated pairs are halves of the
         first rot values, or neighbours when interleaved (gptq_kv_append)."""
+        ptr = _here(stream, self._index)
+        if ptr is not None:
+            return self._append(ptr, k, v, page_table, start, cu, max_new, q, cos, sin, interleaved, q_out)
+        with _Queue(stream, self._index, k, v, q, q_out, page_table, start, cu, cos, sin, self.k_codes, self.v_codes,
+                    self.k_scale, self.v_scale) as ptr:
+            return self._append(ptr, k, v, page_table, start, cu, max_new, q, cos, sin, interleaved, q_out)
+
+    def _append(self, ptr, k, v, page_table, start, cu, max_new, q, cos, sin, interleaved, q_out):
         dt, device, dim = k.dtype, self._index, self.head_dim
         code = _code(k, "k")
-        with _Queue(stream, device, k, v, q, q_out, page_table, start, cu, cos, sin, self.k_codes, self.v_codes,
-                    self.k_scale, self.v_scale) as ptr:
-            k, k_stride = _packed(k, "k", self.kv_heads, dim, dt, device)
-            v, v_stride = _packed(v, "v", self.kv_heads, dim, dt, device)
-            rows = k.shape[0]
-            if v.shape[0] != rows:
-                raise ValueError("k and v must have the same rows")
-            rope = None
-            if cos is not None and sin is not None:
-                shape = cos.shape
-                if (cos.dtype is not _FLOAT32 or sin.dtype is not _FLOAT32 or len(shape) != 2 or sin.shape != shape
-                        or not cos.is_contiguous() or not sin.is_contiguous() or cos.get_device() != device
-                        or sin.get_device() != device):
-                    raise ValueError("cos and sin must be contiguous float32 [positions, rot / 2] tensors on "
-                                     f"cuda:{device}")
-                rope = _ROPE.pack(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if interleaved else 0, 0)
-            elif cos is not None or sin is not None:
-                raise ValueError("cos and sin come together")
-            q_ptr, q_stride, heads, o_ptr, o_stride = None, 0, 0, None, 0
-            if q is not None:
-                if rope is None:
-                    raise ValueError("q is taken to be rotated: pass cos and sin")
-                if q.dim() != 3 or q.shape[0] != rows:
-                    raise ValueError("q must have k's rows")
-                heads = q.shape[1]
-                if q_out is None:
-                    q_out, o_stride = _like(q), heads * dim
-                elif q_out.shape != q.shape or q_out.dtype is not dt or q_out.get_device() != device:
-                    raise ValueError("q_out must have q's shape, type and device")
-                else:
-                    o_stride = _row_stride(q_out, q_out.shape)
-                    if not o_stride:
-                        raise ValueError("q_out must have dense heads and aligned rows")
-                q, q_stride = _packed(q, "q", heads, dim, dt, device)
-                q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
-            st = self._lib.gptq_kv_append(self._c, self._batch(page_table, start, cu, rows, max_new), k.data_ptr(),
-                                          k_stride, v.data_ptr(), v_stride, q_ptr, q_stride, heads, o_ptr, o_stride,
-                                          code, rope, ptr)
+        k, k_stride = _packed(k, "k", self.kv_heads, dim, dt, device)
+        v, v_stride = _packed(v, "v", self.kv_heads, dim, dt, device)
+        rows = k.shape[0]
+        if v.shape[0] != rows:
+            raise ValueError("k and v must have the same rows")
+        rope = None
+        if cos is not None and sin is not None:
+            shape = cos.shape
+            if (cos.dtype is not _FLOAT32 or sin.dtype is not _FLOAT32 or len(shape) != 2 or sin.shape != shape
+                    or not cos.is_contiguous() or not sin.is_contiguous() or cos.get_device() != device
+                    or sin.get_device() != device):
+                raise ValueError("cos and sin must be contiguous float32 [positions, rot / 2] tensors on "
+                                 f"cuda:{device}")
+            rope = _ROPE.pack(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], 1 if interleaved else 0, 0)
+        elif cos is not None or sin is not None:
+            raise ValueError("cos and sin come together")
+        q_ptr, q_stride, heads, o_ptr, o_stride = None, 0, 0, None, 0
+        if q is not None:
+            if rope is None:
+                raise ValueError("q is taken to be rotated: pass cos and sin")
+            if q.dim() != 3 or q.shape[0] != rows:
+                raise ValueError("q must have k's rows")
+            heads = q.shape[1]
+            if q_out is None:
+                q_out, o_stride = _like(q), heads * dim
+            elif q_out.shape != q.shape or q_out.dtype is not dt or q_out.get_device() != device:
+                raise ValueError("q_out must have q's shape, type and device")
+            else:
+                o_stride = _row_stride(q_out, q_out.shape)
+                if not o_stride:
+                    raise ValueError("q_out must have dense heads and aligned rows")
+            q, q_stride = _packed(q, "q", heads, dim, dt, device)
+            q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
+        st = self._lib.gptq_kv_append(self._c, self._batch(page_table, start, cu, rows, max_new), k.data_ptr(),
+                                      k_stride, v.data_ptr(), v_stride, q_ptr, q_stride, heads, o_ptr, o_stride,
+                                      code, rope, ptr)
         if st:
             self._raise(st, "gptq_kv_append")
         return q_out if q is not None else None
@@ -213,12 +213,18 @@ class KVCache:
         code = F32 if dtype is _FLOAT32 else _CODES.get(dtype)
         if code is None:
             raise TypeError("dtype must be float16, bfloat16 or float32")
+        ptr = _here(stream, self._index)
+        if ptr is not None:
+            return self._read(ptr, page_table, start, cu, rows, max_rows, dtype, code)
         with _Queue(stream, self._index, page_table, start, cu, self.k_codes, self.v_codes, self.k_scale,
                     self.v_scale) as ptr:
-            k = torch.empty((rows, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
-            v = torch.empty_like(k)
-            st = self._lib.gptq_kv_read(self._c, self._batch(page_table, start, cu, rows, max_rows), k.data_ptr(),
-                                        v.data_ptr(), code, ptr)
+            return self._read(ptr, page_table, start, cu, rows, max_rows, dtype, code)
+
+    def _read(self, ptr, page_table, start, cu, rows, max_rows, dtype, code):
+        k = torch.empty((rows, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
+        v = torch.empty_like(k)
+        st = self._lib.gptq_kv_read(self._c, self._batch(page_table, start, cu, rows, max_rows), k.data_ptr(),
+                                    v.data_ptr(), code, ptr)
         if st:
             self._raise(st, "gptq_kv_read")
         return k, v
@@ -230,39 +236,45 @@ class KVCache:
         last token.  max_q is at least the rows of every sequence, max_kv at least every length (default:
         what the table holds).  scale defaults to head_dim ** -0.5; window > 0 hides tokens that are
         window or more before the query.  A query that sees nothing gives zeros (gptq_kv_attention)."""
+        ptr = _here(stream, self._index)
+        if ptr is not None:
+            return self._attention(ptr, q, page_table, kv_len, cu, max_q, max_kv, scale, causal, window, out, workspace)
+        with _Queue(stream, self._index, q, out, workspace, page_table, kv_len, cu, self.k_codes, self.v_codes, self.k_scale,
+                    self.v_scale) as ptr:
+            return self._attention(ptr, q, page_table, kv_len, cu, max_q, max_kv, scale, causal, window, out, workspace)
+
+    def _attention(self, ptr, q, page_table, kv_len, cu, max_q, max_kv, scale, causal, window, out, workspace):
         device, dim = self._index, self.head_dim
         code = _code(q, "q")
-        with _Queue(stream, device, q, out, workspace, page_table, kv_len, cu, self.k_codes, self.v_codes, self.k_scale,
-                    self.v_scale) as ptr:
-            if q.dim() != 3:
-                raise ValueError(f"q must be [rows, heads, {dim}]")
-            rows, heads = q.shape[0], q.shape[1]
-            q, q_stride = _packed(q, "q", heads, dim, q.dtype, device)
-            if out is None:
-                out, out_stride = _like(q), heads * dim
-            elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != device:
-                raise ValueError("out must have q's shape, type and device")
-            else:
-                out_stride = _row_stride(out, out.shape)
-                if not out_stride:
-                    raise ValueError("out must have dense heads and aligned rows")
-            batch = self._batch(page_table, kv_len, cu, rows, max_q)
-            if max_kv is None:
-                max_kv = page_table.shape[1] * self.page_size
-            call = _ATTENTION.pack(heads, code, dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, max_kv,
-                                   q_stride, out_stride)
-            key = (rows, page_table.shape, max_q, heads, max_kv, window)
-            need = self._sizes.get(key)
-            if need is None:
-                need = self._workspace_size(batch, call, key)
-            if workspace is not None:
-                ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-            elif need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-                ws = workspace.data_ptr()
-            else:
-                ws = None
-            st = self._lib.gptq_kv_attention(self._c, batch, call, q.data_ptr(), out.data_ptr(), ws, need, ptr)
+        if q.dim() != 3:
+            raise ValueError(f"q must be [rows, heads, {dim}]")
+        rows, heads = q.shape[0], q.shape[1]
+        q, q_stride = _packed(q, "q", heads, dim, q.dtype, device)
+        if out is None:
+            out, out_stride = _like(q), heads * dim
+        elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != device:
+            raise ValueError("out must have q's shape, type and device")
+        else:
+            out_stride = _row_stride(out, out.shape)
+            if not out_stride:
+                raise ValueError("out must have dense heads and aligned rows")
+        batch = self._batch(page_table, kv_len, cu, rows, max_q)
+        if max_kv is None:
+            max_kv = page_table.shape[1] * self.page_size
+        call = _ATTENTION.pack(heads, code, dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, max_kv,
+                               q_stride, out_stride)
+        key = (rows, page_table.shape, max_q, heads, max_kv, causal, window)
+        need = self._sizes.get(key)
+        if need is None:
+            need = self._workspace_size(batch, call, key)
+        if workspace is not None:
+            ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            ws = workspace.data_ptr()
+        else:
+            ws = None
+        st = self._lib.gptq_kv_attention(self._c, batch, call, q.data_ptr(), out.data_ptr(), ws, need, ptr)
         if st:
             self._raise(st, "gptq_kv_attention")
         return out
@@ -321,20 +333,26 @@ class LoraBank:
         if out is not None and (out.shape != y.shape or out.dtype is not dt or out.get_device() != device
                                 or not out.is_contiguous()):
             raise ValueError("out must be a contiguous [M, N] tensor of y's dtype")
+        ptr = _here(stream, device)
+        if ptr is not None:
+            return self._add(ptr, y, x, id_ptr, M, out, workspace)
         with _Queue(stream, device, x, y, ids, out, workspace, self.a, self.b, self.scale) as ptr:
-            x, y = _dense(x), _dense(y)
-            if out is None:
-                out = torch.empty_like(y)          # y is dense here
-            if workspace is None:
-                size = self._sizes.get(M)
-                if size is None:
-                    size = self.workspace_size(M)
-                if size:
-                    workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
-            else:
-                size = workspace.numel() * workspace.element_size()
-            st = self._lib.gptq_lora_add(self._c, x.data_ptr(), y.data_ptr(), id_ptr, M, out.data_ptr(),
-                                         workspace.data_ptr() if workspace is not None else None, size, ptr)
+            return self._add(ptr, y, x, id_ptr, M, out, workspace)
+
+    def _add(self, ptr, y, x, id_ptr, M, out, workspace):
+        x, y = _dense(x), _dense(y)
+        if out is None:
+            out = torch.empty_like(y)          # y is dense here
+        if workspace is None:
+            size = self._sizes.get(M)
+            if size is None:
+                size = self.workspace_size(M)
+            if size:
+                workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+        else:
+            size = workspace.numel() * workspace.element_size()
+        st = self._lib.gptq_lora_add(self._c, x.data_ptr(), y.data_ptr(), id_ptr, M, out.data_ptr(),
+                                     workspace.data_ptr() if workspace is not None else None, size, ptr)
         if st:
             raise GPTQError(st, "gptq_lora_add", self._lib)
         return out
