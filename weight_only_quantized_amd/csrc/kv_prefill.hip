@@ -14,12 +14,12 @@
 // one, while the products of the next tile's scores run under this tile's exponentials and the
 // products with the values under the next tile's exponents.  One barrier a step.
 //
-// Measured: one prompt of 8192 tokens, 32 query heads of 128 on 8 kv heads: 594 us, 925 TFLOP/s of the 1275
-// that a large float16 product reaches; chunks of five prompts (115 GFLOP): 157 us.  The matrix cores are
-// busy 44 % of the time, the vector units 50 %, LDS 33 %; waves wait for their turn to issue 32 % and for
-// memory, LDS or the barrier 29 %.  Without reads of operands the same work takes 317 us, with them 484
-// without staging, barrier and the test for hidden tokens, which cost 90, 30 and 38.  A wave with twice the
-// columns (half the operand reads, one wave a SIMD): 667.
+// Measured: one prompt of 8192 tokens, 32 query heads of 128 on 8 kv heads: 557 us, 988 TFLOP/s of the 1275
+// that a large float16 product reaches; chunks of five prompts (115 GFLOP): 148 us.  The matrix cores are
+// busy 48 % of the time, the vector units 57 %, LDS 36 %; waves wait for their turn to issue 29 % and for
+// memory, LDS or the barrier 27 %.  An earlier form (594 us) took 317 us without reads of operands, with
+// them 484 without staging, barrier and the test for hidden tokens, which cost 90, 30 and 38.  A wave with
+// twice the columns (half the operand reads, one wave a SIMD): 667.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -181,12 +181,11 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
   };
   float x[2][16], most;
   auto scale4 = [&](int j, int field) { return *(const f32x4*)(scales + (j & 3) * 12 + field * 4); };
-  // settles x of tile j: hidden tokens, and a top that has to move (the scores are taken again)
+  // settles x of tile j, from its scores: hidden tokens, and a top that has to move
   auto settle = [&](int j) {
     const int pos = lo + j * kTile;
     const bool edge = pos < inner_lo || pos + kTile > inner_hi;
-    if (!edge && !__any(most > kGrow)) return;
-    score(j);
+    if (__builtin_expect(!edge && !__any(most > kGrow), 1)) return;
     const KeyRange r = key_range(s, row, a.a, room);
     float m = -__builtin_inff();
     const f32x4 ks = scale4(j, 0), log = scale4(j, 1);
@@ -219,44 +218,45 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
   // values of tile i + 1, x tile i's exponents, inv its inverse scales.  Micro-steps of one operand keep
   // the vector work between the matrix instructions; a fence after each keeps the order.  Nothing is read
   // from LDS shortly before its use: operands run through a ring, kAhead ahead and over the middle of the
-  // step, the first weights come before the first product, scales a phase early.
+  // step.  Scores stay until the next step, which settles them (test for hidden tokens and tops) while its
+  // first operands are on their way (8192 tokens: 594 -> 570 us; a window of 1000 over 4096: 98 -> 89).
   f32x4 inv;
   auto step = [&](int i, auto more) {
     constexpr bool kMore = decltype(more)::value;
-    constexpr int kAhead = 3, kKeys = kMore ? 2 * KS : 0, kOut = 4 * DT;
+    constexpr int kAhead = WAVES == 4 && DIM == 128 ? 2 : 3, kKeys = kMore ? 2 * KS : 0, kOut = 4 * DT;
     constexpr int kPer = 32 / (2 * KS);           // weights of a micro-step
-    constexpr int kLead = kMore ? 2 : 0;          // micro-steps of weights before the first product
     u32x4 ring[kAhead];
     auto operand = [&](int n) { return n < kKeys ? key_at(i + 1, n) : value_at(i, n - kKeys); };
     f16x8 w[4];
     f32x4 ks, log;
 #pragma unroll
     for (int m = 0; m < kAhead; ++m) ring[m] = operand(m);
-    if constexpr (kMore) {
-      ks = scale4(i + 1, 0);
-      log = scale4(i + 1, 1);
-    }
+    // waves of this phase before those of the next (us: five chunks 155.6 -> 151.6, heads of 64 110 -> 107.7,
+    // one of 2048 57.1 -> 58.6)
+    __builtin_amdgcn_s_setprio(1);
+    settle(i);                                    // while these are on their way
 #pragma unroll
-    for (int m = 0; m < 2 * KS + kLead; ++m) {
-      if (kMore && m >= kLead) {
-        score_step(m - kLead, ring[(m - kLead) % kAhead]);
-        ring[(m - kLead) % kAhead] = operand(m - kLead + kAhead);
+    for (int m = 0; m < 2 * KS; ++m) {
+      if constexpr (kMore) {
+        score_step(m, ring[m % kAhead]);
+        ring[m % kAhead] = operand(m + kAhead);
       }
-      if (m < 2 * KS) {
-        const int u = m * kPer / 8;
+      const int u = m * kPer / 8;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int e = m * kPer % 8 + k;
-          const float p = __builtin_amdgcn_exp2f(x[u >> 1][(u & 1) * 8 + e]);
-          total = __builtin_fmaf(p, inv[u], total);     // in 32 bits: small against the top may be large here
-          w[u][e] = (_Float16)p;
-        }
-        asm volatile("" : "+v"(total));              // here, not after the step
+      for (int k = 0; k < kPer; ++k) {
+        const int e = m * kPer % 8 + k;
+        const float p = __builtin_amdgcn_exp2f(x[u >> 1][(u & 1) * 8 + e]);
+        total = __builtin_fmaf(p, inv[u], total);    // in 32 bits: small against the top may be large here
+        w[u][e] = (_Float16)p;
       }
+      asm volatile("" : "+v"(total));                // here, not after the step
       __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
     if constexpr (kMore) {
       most = -__builtin_inff();
+      ks = scale4(i + 1, 0);
+      log = scale4(i + 1, 1);
       inv = scale4(i + 1, 2);
     }
     constexpr int kPerOut = 32 / kOut;
@@ -310,14 +310,12 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
     __syncthreads();
     score(0);
     most = __builtin_inff();               // the first tile always settles
-    settle(0);
     inv = scale4(0, 2);
   }
   for (int i = 0; i + 1 < steps; ++i) {
     turn_pages(i + 3);
     __syncthreads();
     step(i, std::true_type{});
-    settle(i + 1);
   }
   if (steps > 0) {
     __syncthreads();
@@ -358,8 +356,9 @@ hipError_t launch_kv_prefill(const KvAttentionCall& a, hipStream_t s) {
   const int page_shift = __builtin_ctz(a.c.page_size);
   const bool bf16 = a.a.dtype == GPTQ_BF16;
   if (a.c.head_dim == 64) return bf16 ? launch_waves<1, 64, 4>(a, page_shift, s) : launch_waves<0, 64, 4>(a, page_shift, s);
-  // eight waves share the conversion of a tile: with a workgroup for every CU or more (us, 8 waves / 4: 8192
-  // tokens, 32 heads 594 / 615), and the smaller workgroups fill the card better before (2048 tokens 62 / 59)
+  // eight waves share the conversion of a tile: with two workgroups for every CU or more (us, 8 waves / 4, 32
+  // heads: 8192 tokens 561 / 609, 4096: 152 / 167); the smaller workgroups fill the card better before (3000
+  // tokens 96 / 95, 2048: 64 / 60)
   if (a.b.rows * a.a.q_heads >= 256 * 512)
     return bf16 ? launch_waves<1, 128, 8>(a, page_shift, s) : launch_waves<0, 128, 8>(a, page_shift, s);
   return bf16 ? launch_waves<1, 128, 4>(a, page_shift, s) : launch_waves<0, 128, 4>(a, page_shift, s);

@@ -20,8 +20,8 @@
 // after a power-of-two scaling of the row): 16 bits or more for one more product.
 //
 // Measured (the device's time): 1 row, rank 16, 4096 x 14336, one launch: 7.8 us, most of it two trips to
-// memory and the pass over A_i.  61 rows of 48 adapters, rank 32, 8192 x 28672 (86 MB): 6.6 + 15.8 us, 4.4
-// TB/s in the second launch.  4001 rows in 9 runs, rank 64, 4096 x 14336 (271 MB): 12.5 + 4.7 + 59 us, 3.9
+// memory and the pass over A_i.  61 rows of 48 adapters, rank 32, 8192 x 28672 (86 MB): 7.0 + 15.9 us, 4.3
+// TB/s in the second launch.  4001 rows in 9 runs, rank 64, 4096 x 14336 (271 MB): 12.5 + 4.7 + 58.5 us, 3.9
 // TB/s of y and out against 4.9 of a copy.
 #include <hip/hip_runtime.h>
 
