@@ -160,6 +160,18 @@ def test_attention_random_shapes(seed):
            scale=None if seed % 3 else 0.3)
 
 
+@pytest.mark.parametrize("case", [(120, 4, 8, 128, 16, "bf16", 0, 1), (90, 6, 6, 64, 32, "f16", 0, 2),
+                                  (130, 3, 12, 128, 64, "f16", 50, 5), (70, 8, 16, 64, 16, "bf16", 90, 1)])
+def test_many_short_sequences(case):
+    """Batches whose sequences are short and many, some without rows or tokens."""
+    batch, hkv, hq, dim, page, tag, window, most = case
+    rng = np.random.default_rng(batch)
+    ns = [int(n) for n in rng.integers(0, most + 1, batch)]
+    lens = [max(0, int(n + rng.choice([0, 0, 1, 15, 33, 100, 190]) + rng.integers(-1, 40))) for n in ns]
+    say("short sequences", case)
+    attend(Pool(lens, page, hkv, dim, seed=batch), lens, ns, hq, tag, window=window)
+
+
 def test_calls_that_differ_in_causality_only():
     """With a window the keys that a call may see, and its workspace with them, follow from causality too."""
     import torch
