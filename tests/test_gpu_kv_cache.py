@@ -172,6 +172,24 @@ def test_many_short_sequences(case):
     attend(Pool(lens, page, hkv, dim, seed=batch), lens, ns, hq, tag, window=window)
 
 
+@pytest.mark.parametrize("batch", [0, 3])
+def test_calls_without_rows(batch):
+    """No rows, with and without sequences: empty outputs, and the cache as it was."""
+    import torch
+    pool = Pool([5, 9, 16], 16, 2, 64, seed=2)
+    cache, table = pool.cache(), dev(pool.table[:batch])
+    at, cu = dev(np.zeros(batch, np.int32)), dev(np.zeros(batch + 1, np.int32))
+    k, q = (torch.zeros((0, h, 64), dtype=torch.float16, device="cuda") for h in (2, 4))
+    cos, sin = tables(16, 32)
+    before = cache.k_codes.clone()
+    cache.append(k, k, table, at, cu, max_new=0)
+    got = cache.append(k, k, table, at, cu, max_new=0, q=q, cos=dev(cos), sin=dev(sin))
+    assert got.shape == q.shape
+    assert [t.shape for t in cache.read(table, at, cu, rows=0, max_rows=0)] == [k.shape, k.shape]
+    assert cache.attention(q, table, at, cu, max_q=0).shape == q.shape
+    assert torch.equal(cache.k_codes, before)
+
+
 def test_calls_that_differ_in_causality_only():
     """With a window the keys that a call may see, and its workspace with them, follow from causality too."""
     import torch

@@ -119,6 +119,12 @@ def test_infinite_sums_stay_infinite(M, rank, tag):
     assert torch.equal(got[keep], plain[keep])
 
 
+def test_no_rows():
+    import torch
+    bank, x, y, idt, ids = make(1, 256, 192, 16, 2, "f16", seed=1)
+    assert bank.add(y[:0], x[:0], idt[:0]).shape == (0, 192)
+
+
 def test_in_place_streams_and_equal_bits():
     import torch
     bank, x, y, idt, ids = make(37, 1024, 512, 16, 6, "f16", seed=5)

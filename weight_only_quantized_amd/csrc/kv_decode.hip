@@ -1,4 +1,5 @@
-// Attention over the paged 8-bit cache for few query rows a sequence (single tokens, drafts).
+// Attention over the paged 8-bit cache with the keys split over the card: single tokens, drafts, and pieces
+// of prompts that are short for the tokens they see.
 //
 // Mathematics.  For the queries c of one sequence and kv head and its visible tokens j,
 //     t_cj = log2(e) scale k_scale(j) <q_c, kc_j> + log2 v_scale(j),    w_cj = 2^(t_cj - m_c),
@@ -47,7 +48,7 @@ constexpr int kMaxRun = 64 * 16;                   // a wave holds the pages of 
 struct DecodePlan {
   int col_tiles;    // 16-column tiles of a unit: 1 or 2
   int col_groups;   // units of a sequence and kv head, at most
-  int waves, wave_bits;    // a power of two
+  int waves, wave_bits;    // when split a power of two
   int units;        // batch * kv_heads * col_groups
   int width;        // columns of a part: those that a unit can have
   int local;        // a workgroup of kLocalWaves takes a unit and joins it

@@ -184,9 +184,9 @@ gptq_status gptq_kv_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch,
   if (st == GPTQ_OK) st = check_batch(batch);
   if (st != GPTQ_OK) return st;
   if (!is_16bit(dtype) && dtype != GPTQ_F32) return GPTQ_E_INVALID_ARG;
+  if (batch->rows == 0 || batch->batch == 0) return GPTQ_OK;
   if (!k_out && !v_out) return GPTQ_E_INVALID_ARG;
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return GPTQ_E_INVALID_ARG;
-  if (batch->rows == 0 || batch->batch == 0) return GPTQ_OK;
   const size_t n = (size_t)batch->rows * cache->kv_heads * cache->head_dim * (dtype == GPTQ_F32 ? 4 : 2);
   if (overlaps(k_out, n, v_out, n) || overlaps_cache(cache, k_out, n) || overlaps_cache(cache, v_out, n))
     return GPTQ_E_INVALID_ARG;
