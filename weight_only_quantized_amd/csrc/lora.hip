@@ -602,11 +602,13 @@ LoraPlan plan_of(const gptq_lora_bank& bank, int64_t M) {
   p.slice_k = (int)(div_up(steps, slices) * step);
   p.slices = (int)div_up(bank.in_features, p.slice_k);
   const int64_t blocks = div_up(bank.out_features, 256);
-  // few: all workgroups on the card at once; many: half as many again as there is room for
+  // few: all workgroups on the card at once; many: about 1536 of them, 768 when only one fits a CU (rank 128,
+  // us with 768 / 1536: 2048 rows of 14336 outputs 74.5 / 79.3, 4001: 125 / 124, 4001 of 4096: 53 / 63)
   const int64_t fit = bank.rank <= 32 ? 1024 : bank.rank <= 64 ? 768 : 512;
-  int64_t per = p.few ? div_up(p.up_tiles * blocks, fit) : p.up_tiles * blocks / 1536;
+  int64_t per = p.few ? div_up(p.up_tiles * blocks, fit) : p.up_tiles * blocks / (bank.rank > 64 ? 768 : 1536);
   p.per_n = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
   p.blocks_n = (int)div_up(blocks, p.per_n);
+  p.per_n = (int)div_up(blocks, p.blocks_n);         // no workgroup with a short remainder
   // One launch while its workgroups have a CU each and A_i is small, since each reads all of it.  Us on the
   // device, one launch against two, rank 8, 1 row: K = 1024 4.9 / 6.8, 4096 7.1 / 8.0, 5120 7.8 / 7.6, 6144
   // 8.6 / 7.8 (the second launch costs the host 2.7 more); K = 4096, N = 14336, 4 rows (224 workgroups)
