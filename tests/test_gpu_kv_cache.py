@@ -202,6 +202,24 @@ def test_calls_that_differ_in_causality_only():
         check_attention(host(out), host(q), pool, lens, cu, "f16", 64 ** -0.5, causal, 40)
 
 
+@pytest.mark.parametrize("seed", range(16))
+def test_attention_prompts_random(seed):
+    """Prompts with enough (row, head) columns to go through the keys a workgroup each, ragged, with
+    contexts, windows and pages of all sizes."""
+    rng = np.random.default_rng(900 + seed)
+    batch, hkv, group = int(rng.integers(2, 6)), int(rng.integers(4, 7)), int(rng.choice([3, 4, 5, 8]))
+    ns = [int(rng.integers(0, 220)) for _ in range(batch)]
+    ns[0] = int(rng.integers(180, 330))
+    lens = [max(0, n + int(rng.integers(-3, 500))) for n in ns]
+    page, dim = int(rng.choice([16, 32, 64, 128, 256])), int(rng.choice([64, 128]))
+    window = int(rng.choice([0, 0, 1, 65, 200]))
+    tag, causal = str(rng.choice(["f16", "bf16"])), bool(rng.random() < 0.8)
+    say("prompts", seed, ns, lens, page, dim, hkv, group, window, tag, causal)
+    assert batch * hkv * -(-ns[0] * group // 16) > 256
+    pool = Pool(lens, page, hkv, dim, seed=seed)
+    attend(pool, lens, ns, hkv * group, tag, seed=seed, causal=causal, window=window)
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_attention_few_rows_long(seed):
     """A few rows each over thousands of tokens, sequences of very different lengths among them."""

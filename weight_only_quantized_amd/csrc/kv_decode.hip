@@ -555,21 +555,13 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, De
 DecodePlan plan_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   DecodePlan p;
   const int64_t columns = (int64_t)b.max_rows * (a.q_heads / c.kv_heads);
-  p.col_tiles = columns <= 16 ? 1 : 2;
+  p.local = kv_local(c, b, a);
+  p.col_tiles = columns <= 16 || p.local ? 1 : 2;
   p.width = (int)(columns < 16 * p.col_tiles ? columns : 16 * p.col_tiles);
   p.col_groups = (int)((columns + 16 * p.col_tiles - 1) / (16 * p.col_tiles));
   const int64_t steps = (kv_span(c, b, a) + 15 + kStep - 1) / kStep;      // a range starts at 16: up to 15 more
   const int64_t units = (int64_t)b.batch * c.kv_heads * p.col_groups;
   const int64_t fit = 256 * kWaves * 2;
-  // A CU alone takes in some 50 GB/s, so short units only; fewer than 64 leave most of the card idle in
-  // exchange for the second launch (4.6 us of the device, 2.7 of the host).  Us on the device, local
-  // against split, 8 kv heads of 128: 1 sequence of 256 tokens 7.2 / 9.4, 512: 8.7 / 9.7, 1024: 9.6 / 9.7,
-  // 2048: 16.9 / 10.5; 16 sequences of 1024: 13.3 / 17.6, 2048: 20.3 / 21.9, 4096: 32.7 / 31.1; 64
-  // sequences of 512: 22.5 / 20.2 (two workgroups for each CU take turns).  Heads of 64 leave room for two
-  // workgroups on a CU; 384 of them, 1000 tokens: 13.0 / 15.7, 2000: 23.2 / 22.5.
-  const int64_t bytes = steps * kStep * c.head_dim * 2;
-  const int64_t most = units < 64 ? 256 << 10 : units <= 256 ? 512 << 10 : 160 << 10;
-  p.local = p.col_tiles == 1 && units * c.head_dim <= 256 * 128 && bytes <= most;
   // Many short units: a wave takes a whole one, so that nothing is joined and no wave looks for its share.
   // Us, a wave a unit / split, 8 kv heads of 128, sequences of very different lengths up to: 64 of 128 8.7 /
   // 10.3, 512: 18.8 / 18.2; 128 of 64: 7.5 / 14.1, 1000: 32.9 / 32.9; 256 of 256: 18.3 / 31.7, 1500: 70 / 72,

@@ -100,12 +100,12 @@ gptq_status check_attention(const gptq_kv_cache* c, const gptq_kv_batch* b, cons
 // Whether the keys are split over the card (kv_decode.hip) or each workgroup goes through all that its
 // columns see (kv_prefill.hip).  Splitting takes about 27 + 0.029 U n us for U units of 32 (row, head) columns
 // over n thousand tokens (less for a few units), going through 6 + 21 n while every workgroup has a CU.
-// Us, split / not, 8 kv heads of 128, 32 query heads: 1 sequence, 8 rows, 700 tokens (U = 8) 14 / 20; 64 rows
-// (64), 1000 tokens 37 / 30, 1500: 37 / 40, 16000: 51 / 345; 4 sequences of 64 rows (256), 16000: 145 / 349;
-// 16 of 32 rows (512), 2500: 72 / 70; 32 of 32 rows (1024), 4000: 155 / 144.
+// Us, split / not, 8 kv heads of 128, 32 query heads: 1 sequence of 64 rows (U = 64), 2500 tokens 37 / 61,
+// 16000: 51 / 345; 4 of 64 rows (256), 16000: 145 / 349; 16 of 32 rows (512), 2500: 72 / 70; 32 of 32 rows
+// (1024), 4000: 155 / 144.  Few short units (kv_local) come before both.
 bool few_rows(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   const int64_t columns = (int64_t)b.max_rows * (a.q_heads / c.kv_heads);
-  if (columns <= 16) return true;
+  if (columns <= 16 || kv_local(c, b, a)) return true;
   const int64_t units = (int64_t)b.batch * c.kv_heads * ((columns + 31) / 32), span = kv_span(c, b, a);
   return units <= 24 || (units <= 700 && units * span <= 700 * (span - 1000));
 }

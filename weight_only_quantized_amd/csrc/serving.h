@@ -39,6 +39,22 @@ inline int64_t kv_span(const gptq_kv_cache& c, const gptq_kv_batch& b, const gpt
   const int64_t windowed = (int64_t)a.window + b.max_rows;
   return a.causal && a.window > 0 && windowed < span ? windowed : span;
 }
+// Whether units of 16 (row, head) columns are few and short enough for a workgroup each (kv_decode.hip).
+inline bool kv_local(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  const int64_t columns = (int64_t)b.max_rows * (a.q_heads / c.kv_heads);
+  const int64_t units = (int64_t)b.batch * c.kv_heads * ((columns + 15) / 16);
+  // A CU alone takes in some 50 GB/s, so short units only; fewer than 64 leave most of the card idle in
+  // exchange for the second launch (4.6 us of the device, 2.7 of the host).  Us on the device, local
+  // against split, 8 kv heads of 128: 1 sequence of 256 tokens 7.2 / 9.4, 512: 8.7 / 9.7, 1024: 9.6 / 9.7,
+  // 2048: 16.9 / 10.5; 16 sequences of 1024: 13.3 / 17.6, 2048: 20.3 / 21.9, 4096: 32.7 / 31.1; 64
+  // sequences of 512: 22.5 / 20.2 (two workgroups for each CU take turns).  Heads of 64 leave room for two
+  // workgroups on a CU; 384 of them, 1000 tokens: 13.0 / 15.7, 2000: 23.2 / 22.5.  Several units for a
+  // sequence and kv head, local against what else would run, 4 query heads each: 1 sequence of 16 rows, 777
+  // tokens 12.7 / 17.2; 4 of 8 rows 12.7 / 22.8; 8 of 16 rows, 1500 tokens 21.6 / 31.9; one prompt of 64
+  // 7.1 / 9.2; 400 units, heads of 64, a prompt of 200: 9.8 / 8.8.
+  const int64_t most = units < 64 ? 256 << 10 : units <= 256 ? 512 << 10 : 160 << 10;
+  return units <= (columns <= 16 ? 256 * 128 / c.head_dim : 256) && (kv_span(c, b, a) + 46) / 32 * 64 * c.head_dim <= most;
+}
 // Few rows a sequence (kv_decode.hip): split over the keys, joined by a second launch.
 size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
 hipError_t launch_kv_decode(const KvAttentionCall& a, hipStream_t s);
