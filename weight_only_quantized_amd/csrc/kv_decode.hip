@@ -3,10 +3,10 @@
 //
 // Mathematics.  For the queries c of one sequence and kv head and its visible tokens j,
 //     t_cj = log2(e) scale k_scale(j) <q_c, kc_j> + log2 v_scale(j),    w_cj = 2^(t_cj - m_c),
-//     out_c = sum_j w_cj vc_j / sum_j w_cj / v_scale(j),
+//     out_c = 2^r sum_j w_cj vc_j / sum_j w_cj 2^r / v_scale(j),
 // in one pass: the value scale rides in the exponent, so every weight that multiplies codes is
 // relative to the column's largest contribution, whatever the pages' scales are, and the sum of
-// probabilities takes the scale out again.  m_c only moves when a weight would pass 2^14 (then what
+// probabilities takes the scale out again (2^r is about as large and keeps it in float32).  m_c only moves when a weight would pass 2^14 (then what
 // was summed is scaled by 2^(m - m')), so the usual step has no cross-lane work.
 //
 // What bounds it: the cache's bytes.  MFMA operands are float16: codes are exact integers (the byte
@@ -98,13 +98,14 @@ __device__ __forceinline__ KvAttentionCall call_again() {
   return *(const KvAttentionCall*)p;
 }
 
-// o / sum, four values; zeros where nothing was seen.
+// 2^ref o / sum, four values; zeros where nothing was seen.
 template <int BF16>
-__device__ __forceinline__ void store_joined(uint16_t* to, f32x4 o, float sum) {
-  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+__device__ __forceinline__ void store_joined(uint16_t* to, f32x4 o, float sum, float ref) {
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f, back = __builtin_amdgcn_exp2f(ref);
+  o = o * inv * back;
   uint2 w;
-  w.x = (uint32_t)from_f32<BF16>(o[0] * inv) | (uint32_t)from_f32<BF16>(o[1] * inv) << 16;
-  w.y = (uint32_t)from_f32<BF16>(o[2] * inv) | (uint32_t)from_f32<BF16>(o[3] * inv) << 16;
+  w.x = (uint32_t)from_f32<BF16>(o[0]) | (uint32_t)from_f32<BF16>(o[1]) << 16;
+  w.y = (uint32_t)from_f32<BF16>(o[2]) | (uint32_t)from_f32<BF16>(o[3]) << 16;
   *(uint2*)to = w;
 }
 
@@ -218,11 +219,12 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   float q_scale[CT], top[CT], total[CT];
   f16x8 q[CT][2 * KL];
   u32x4 query[CT][2 * KL];
-  auto page_id = [&](int base) {                  // 16 tokens a lane
+  auto page_id = [&](int base, int end) {         // 16 tokens a lane
     const int my_pos = base + lane * 16;
-    return tile_page_id(a.c, a.b, seq, my_pos, my_pos < run1, page_shift);
+    return tile_page_id(a.c, a.b, seq, my_pos, my_pos < end, page_shift);
   };
-  int page = page_id(run0);                       // on its way with the query
+  int page = page_id(run0, run1);                 // on its way with the query
+  const int head_page = page_id(work.lo, work.hi);     // of the unit's first tokens, for one reference of all its parts
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     int c = first_col + ct * 16 + col16;
@@ -399,14 +401,16 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     load_values(odd, 1);
     __builtin_amdgcn_sched_barrier(0);
   };
+  const TilePage head_pages = tile_scales(a.c, head_page, kv_head);
   start_run();
+  const float ref = scale_reference(marked(head_pages).v_scale);
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) q_scale[ct] = query_f16<BF16, 2 * KL>(query[ct], q[ct], 16, 32) * (a.a.scale * kLog2e);
   for (;;) {
-    const TilePage there = settled(pages);
+    const TilePage there = marked(pages);
     pages = there;
-    my_log = scale_log(there.v_scale);
-    my_inv = scale_inv(my_log);
+    my_log = scale_log(there.v_scale, ref);
+    my_inv = scale_inv(my_log, ref);
     const int n = run1 - base < kMaxRun ? (run1 - base + kStep - 1) / kStep : kMaxRun / kStep;
     if constexpr (CT == 1) {               // pairs, so that every wait in the loop is for what it needs
       int i = 0;
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     }
     base += kMaxRun;
     if (base >= run1) break;
-    page = page_id(base);
+    page = page_id(base, run1);
     start_run();
   }
 
@@ -444,14 +448,14 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     const int c = first_col + ct * 16 + col16;
     if (c >= columns) continue;
     if (alone) {
-      const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = sum != 0.0f ? 1.0f / sum : 0.0f, back = __builtin_amdgcn_exp2f(ref);
       uint16_t* to = e_call.out + (int64_t)(s.row0 + c / group) * e_call.a.out_stride + (kv_head * group + c % group) * DIM;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         uint32_t o[VB / 2];
 #pragma unroll
         for (int t = 0; t < VB; t += 2)
-          o[t / 2] = (uint32_t)from_f32<BF16>(acc[ct][t][e] * inv) | (uint32_t)from_f32<BF16>(acc[ct][t + 1][e] * inv) << 16;
+          o[t / 2] = (uint32_t)from_f32<BF16>(acc[ct][t][e] * inv * back) | (uint32_t)from_f32<BF16>(acc[ct][t + 1][e] * inv * back) << 16;
         __builtin_memcpy(__builtin_assume_aligned(to + VB * (4 * quad + e), VB * 2), o, VB * 2);
       }
     } else {
@@ -467,6 +471,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
       if (quad == 0) {
         to[DIM] = top[ct];
         to[DIM + 1] = sum;
+        to[DIM + 2] = ref;
       }
     }
   }
@@ -491,7 +496,8 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
       all = __builtin_fmaf(from[DIM + 1], in, all);
       o += *(const f32x4*)(from + d) * in;
     }
-    store_joined<BF16>(a.out + (int64_t)(work.s.row0 + c / group) * a.a.out_stride + (kv_head * group + c % group) * DIM + d, o, all);
+    store_joined<BF16>(a.out + (int64_t)(work.s.row0 + c / group) * a.a.out_stride + (kv_head * group + c % group) * DIM + d, o, all,
+                       sums[0][c - first_col][DIM + 2]);
   }
 }
 
@@ -516,6 +522,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, De
   const float* part = (const float*)((const uint8_t*)a.ws + parts_offset(plan)) +
                       ((int64_t)parts.first * plan.width + c % width) * kPitch;
   const int thread = threadIdx.x % THREADS, in_part = thread % kLanes;
+  const float ref = part[DIM + 2];
   float most = kNoTop, all = 0.0f;
   f32x4 o{0, 0, 0, 0};
   auto join = [&](float top, float sum, f32x4 v) {
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, De
       for (int w = 1; w < kWaves; ++w) join(sums[w][DIM], sums[w][DIM + 1], *(const f32x4*)&sums[w][in_part * 4]);
   }
   if (thread >= kLanes) return;
-  store_joined<BF16>(a.out + row * a.a.out_stride + head * DIM + in_part * 4, o, all);
+  store_joined<BF16>(a.out + row * a.a.out_stride + head * DIM + in_part * 4, o, all, ref);
 }
 
 // Two waves a SIMD (256 CUs), or as many as there can be steps: measured with 1, 1.5, 3 and 4 as well (221

@@ -50,15 +50,13 @@ __device__ __forceinline__ KeyRange key_range(const SeqRows& s, int row, const g
   return KeyRange{begin, end};
 }
 
-// The page of a tile of 16 tokens, one a lane, and its scales for one kv head.  An absent tile has
-// page -1 and scales 0: its weights are 0.  Value scales below 2^-64 count as 2^-64 (an all-zero page
-// has scale 0).
+// The page of a tile of 16 tokens, one a lane, and its scales for one kv head, in parts for callers that
+// have other loads to send between them: the page (-1: absent), and its scales (page 0's for an absent tile;
+// `marked` makes them 0 and -1).  No branches.
 struct TilePage {
   int page;
   float k_scale, v_scale;
 };
-// The same in parts, for a caller that has other loads to send between them: the page, its scales as they
-// are (page 0's for an absent tile), and what tile_page gives.  No branches.
 __device__ __forceinline__ int tile_page_id(const gptq_kv_cache& c, const gptq_kv_batch& b, int seq, int pos, bool wanted,
                                             int page_shift) {
   const int j = pos >> page_shift;
@@ -70,27 +68,36 @@ __device__ __forceinline__ TilePage tile_scales(const gptq_kv_cache& c, int page
   const int64_t unit = (int64_t)(page < 0 ? 0 : page) * c.kv_heads + kv_head;
   return TilePage{page, c.k_scale[unit], c.v_scale[unit]};
 }
-__device__ __forceinline__ TilePage settled(const TilePage& t) {
-  return TilePage{t.page, t.page < 0 ? 0.0f : t.k_scale, t.page < 0 ? 0.0f : __builtin_fmaxf(t.v_scale, 0x1p-64f)};
-}
-__device__ __forceinline__ TilePage tile_page(const gptq_kv_cache& c, const gptq_kv_batch& b, int seq, int kv_head,
-                                              int pos, bool wanted, int page_shift) {
-  return settled(tile_scales(c, tile_page_id(c, b, seq, pos, wanted, page_shift), kv_head));
+__device__ __forceinline__ TilePage marked(const TilePage& t) {
+  return TilePage{t.page, t.page < 0 ? 0.0f : t.k_scale, t.page < 0 ? -1.0f : t.v_scale};
 }
 // Bytes before a tile's codes (page 0's for an absent tile, which is safe to read).
 __device__ __forceinline__ uint64_t tile_base(const gptq_kv_cache& c, int page, int kv_head, int pos, int page_shift) {
   const uint64_t unit = (uint64_t)(page < 0 ? 0 : page) * (uint32_t)c.kv_heads + (uint32_t)kv_head;
   return ((unit << page_shift) + (uint32_t)(pos & ((1 << page_shift) - 1))) * (uint32_t)c.head_dim;
 }
-// log2 of a value scale and the inverse of that power of two (so that both cancel); -inf and 0 when
-// the tile is absent.
-__device__ __forceinline__ float scale_log(float v_scale) { return __builtin_amdgcn_logf(v_scale); }
-__device__ __forceinline__ float scale_inv(float v_log) {
-  return v_log > -1e30f ? __builtin_amdgcn_exp2f(-v_log) : 0.0f;
-}
-
 __device__ __forceinline__ float lane_f32(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+// Sums of probabilities are kept times 2^ref: a weight 2^(t + log v) stands for the probability
+// 2^(t + log v) 2^(ref - log v).  float32 holds such sums for value scales of 2^(ref - 80) (2^80, weights
+// of 2^14 and 2^30 tokens make 2^124) up to 2^(ref + 118).  ref lies 19 below the first value scale that is
+// not zero (of marked tiles, one a lane), so that scales within 2^99 of that one keep their bits, and between
+// -79 and 41, so that those of 2^-39 .. 2^39 always do.
+__device__ __forceinline__ float scale_reference(float v_scale) {
+  const uint64_t some = __ballot(v_scale > 0.0f);
+  int e = some ? __builtin_amdgcn_frexp_expf(lane_f32(v_scale, __builtin_ctzll(some))) : 0;
+  e = e < -60 ? -60 : e > 60 ? 60 : e;
+  return (float)__builtin_amdgcn_readfirstlane(e - 19);
+}
+// log2 of a value scale (subnormal ones too; zero and what lies below the range count as its end), and 2^ref
+// over the scale by the same logarithm, so that both cancel; -inf and 0 when the tile is absent.
+__device__ __forceinline__ float scale_log(float v_scale, float ref) {
+  const float log = __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(v_scale)) + (float)__builtin_amdgcn_frexp_expf(v_scale);
+  return v_scale < 0.0f ? -__builtin_inff() : __builtin_fmaxf(log, ref - 80.0f);
+}
+__device__ __forceinline__ float scale_inv(float v_log, float ref) {
+  return v_log > -1e30f ? __builtin_amdgcn_exp2f(ref - v_log) : 0.0f;
 }
 // Codes to float16, exactly: byte b becomes 0x64'(b ^ 0x80) = 1024 + (code + 128), minus 1152.
 __device__ __forceinline__ uint32_t less_1152(uint32_t w) {

@@ -87,15 +87,20 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
   const int inner_lo = key_range(s, wave_last / group, a.a, room).begin;
   const int inner_hi = key_range(s, (wave_col < columns ? wave_col : columns - 1) / group, a.a, room).end;
 
-  // staging: a wave's tokens lie in the 16 from 16 * part on; lane u of `pages` holds tokens
-  // [16 u, 16 u + 16) of a run of 16 tiles
+  // staging: a wave's tokens lie in the 16 from 16 * part on; lane u of page, k_scale
+  // and v_log holds tokens [16 u, 16 u + 16) of a run of 16 tiles (log2 of the value scale once a run: its
+  // few instructions in every step cost 8192 tokens 558 us instead of 555)
   constexpr int kSplit = 16 / kShare;     // waves that share 16 tokens
   const int part = wave / kSplit, in_part = wave % kSplit;
   auto pages_of = [&](int run) {
     const int pos = lo + run * 1024 + lane * 16;
-    return tile_page(a.c, a.b, seq, kv_head, pos, pos < hi, page_shift);
+    return marked(tile_scales(a.c, tile_page_id(a.c, a.b, seq, pos, pos < hi, page_shift), kv_head));
   };
-  TilePage pages = pages_of(0), next_pages = pages_of(1);
+  TilePage next_pages = pages_of(0);
+  const float ref = scale_reference(next_pages.v_scale);
+  int page = next_pages.page;
+  float k_scale = next_pages.k_scale, v_log = scale_log(next_pages.v_scale, ref);
+  next_pages = pages_of(1);
   // keys: a row by neighbouring lanes (lanes that each read their own row cost the address unit a
   // cycle a lane); the piece of 16 codes in k_codes[p] is of row key_row + p * 1024 / DIM
   constexpr int kPieces = DIM / 16;
@@ -109,18 +114,20 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
   u32x4 k_codes[KL];
   uint32_t v_codes[4][VW];
   uint64_t k_base = 0;                    // of the tile in k_codes; its scales
-  float st_k = 0.0f, st_v = 0.0f;
+  float st_k = 0.0f, st_log = 0.0f;
   auto turn_pages = [&](int j) {          // before tile j's keys are loaded
     if (!(j & 15)) {
-      pages = next_pages;
+      page = next_pages.page;
+      k_scale = next_pages.k_scale;
+      v_log = scale_log(next_pages.v_scale, ref);
       next_pages = pages_of((j >> 4) + 1);
     }
   };
   auto load_keys = [&](int j) {
     const int u = (j & 15) * 4 + part;
-    k_base = tile_base(a.c, __builtin_amdgcn_readlane(pages.page, u), kv_head, lo + j * kTile + part * 16, page_shift);
-    st_k = lane_f32(pages.k_scale, u);
-    st_v = lane_f32(pages.v_scale, u);
+    k_base = tile_base(a.c, __builtin_amdgcn_readlane(page, u), kv_head, lo + j * kTile + part * 16, page_shift);
+    st_k = lane_f32(k_scale, u);
+    st_log = lane_f32(v_log, u);
     const int8_t* kb = a.c.k_codes + k_base;
 #pragma unroll
     for (int p = 0; p < KL; ++p) k_codes[p] = *(const u32x4*)(kb + k_off + p * 1024);
@@ -140,9 +147,9 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
     }
   };
   auto store_scales = [&](int j) {        // of the tile in k_codes
-    const float log = scale_log(st_v), inverse = scale_inv(log);
+    const float inverse = scale_inv(st_log, ref);
     float one = st_k;
-    one = lane == 1 ? log : one;
+    one = lane == 1 ? st_log : one;
     one = lane == 2 ? inverse : one;
     const int to = lane < 3 && in_part == 0 ? (j & 3) * 12 + lane * 4 + part : 48 + lane;
     scales[to] = one;
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
 
   const float sum = total + __shfl_xor(total, 32);
   if (wave_col + col32 >= columns) return;
-  const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
+  const float norm = sum != 0.0f ? 1.0f / sum : 0.0f, back = __builtin_amdgcn_exp2f(ref);
   uint16_t* to = a.out + (int64_t)(s.row0 + row) * a.a.out_stride + head * DIM;
   // element e of tile t is LDS row 32 t + 8 (e / 4) + 4 half + e % 4, which is value VB (row % kGroups) +
   // row / kGroups: of one e the tiles (and, with 16 groups, element e + 8) are values next to each other
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
 #pragma unroll
     for (int t = 0; t < VB / 2; ++t) {
       const float v0 = kBoth == 2 ? acc[t][e] : acc[2 * t % DT][e], v1 = kBoth == 2 ? acc[t % DT][(e + 8) % 16] : acc[(2 * t + 1) % DT][e];
-      o[t] = (uint32_t)from_f32<BF16>(v0 * norm) | (uint32_t)from_f32<BF16>(v1 * norm) << 16;
+      o[t] = (uint32_t)from_f32<BF16>(v0 * norm * back) | (uint32_t)from_f32<BF16>(v1 * norm * back) << 16;
     }
     __builtin_memcpy(__builtin_assume_aligned(to + VB * (8 * (e >> 2) + 4 * half + (e & 3)), VB * 2), o, VB * 2);
   }
