@@ -369,6 +369,7 @@ typedef struct {
  *   rint(x / unit) within [-127, 127] (0 when unit is 0).
  * A page filled in one call is therefore rounded once; one filled token by token is rounded again
  * only when a token exceeds everything before it.  Codes past the newest token are left alone.
+ * (quotients as products with float32's 1 / unit, each rounded once).
  * Infinities take no part in the maximum and become +-127; NaN becomes 0.
  * Two sequences must not append to the same page in one call.
  * Errors: GPTQ_E_INVALID_ARG (NULL, alignment, strides, dtype, reserved, overlap), GPTQ_E_SHAPE

@@ -90,3 +90,25 @@ def test_value_scales_far_from_one(pattern, form):
     err = np.abs(out - want)
     assert np.all(np.isfinite(out))
     assert np.all(err <= bound), (pattern, form, float((err / bound).max()), np.argwhere(err > bound)[:4].tolist())
+
+
+@pytest.mark.parametrize("n", [1, 40], ids=["token", "rows"])
+@pytest.mark.parametrize("had", [0.3, 2.0], ids=["grows", "stays"])
+@pytest.mark.parametrize("size", [1e-35, 1e-37, 1e-38, 3e-39])
+def test_append_of_values_near_the_smallest(size, had, n):
+    """Pages whose scale has no float32 inverse.  Bounds: a scale is within 4 float32 roundings and half of
+    the smallest subnormal step, 2^-150, of the ideal, and the codes follow it."""
+    import torch
+    starts, ns = [5, 0, 16], [n, n, n]
+    pool = Pool([s + n for s in starts], 16, 2, 64, seed=n)
+    pool.k_scale[:] = pool.v_scale[:] = np.float32(had * size / 127)
+    cache, cu, rng = pool.cache(), offsets(ns), np.random.default_rng(n)
+    say("append", size, had, n)
+    k, v = (dev(np.clip(rng.normal(0, 0.4, (3 * n, 2, 64)), -1, 1) * size, torch.bfloat16) for _ in "kv")
+    cache.append(k, v, dev(pool.table), dev(np.asarray(starts, np.int32)), dev(cu), max_new=n)
+    for name, x in (("k", k), ("v", v)):
+        ideal, scale = so.append(getattr(pool, name + "_codes"), getattr(pool, name + "_scale"), host(x), pool.table, starts, cu)
+        got, got_scale = host(getattr(cache, name + "_codes")), host(getattr(cache, name + "_scale"))
+        assert np.all(np.abs(got_scale - scale) <= scale * 4 * 2.0 ** -23 + 2.0 ** -150)
+        off = 0.5 + 127 * (16 * 2.0 ** -24 + 2.0 ** -150 / np.maximum(scale, 2.0 ** -149))[:, :, None, None]
+        assert np.all(np.abs(got - ideal) <= off), (name, float(np.abs(got - ideal).max()))

@@ -143,8 +143,17 @@ __device__ __forceinline__ void append_page(const KvAppendCall& a, int slot, int
   for (int i = 0; i < THREADS / 64; ++i) most = __builtin_fmaxf(most, most_of_wave[i]);
   const float had = base < start ? *scale : 0.0f;
   const float unit = __builtin_fmaxf(had, most * (1.0f / 127.0f));
-  const float inverse = unit > 0.0f ? 1.0f / unit : 0.0f;
-  const float ratio = had * inverse;
+  // below 2^-128 the inverse would be infinite: there the page's values, exactly, times 2^64
+  const bool tiny = unit < 0x1p-100f;
+  const float up = tiny ? 0x1p64f : 1.0f;
+  const float inverse = unit > 0.0f ? 1.0f / (unit * up) : 0.0f;
+  const float ratio = had * up * inverse;
+  if (tiny) {
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] *= up;
+  }
   __syncthreads();                                            // every thread has read the old scale
   if (threadIdx.x == 0) *scale = unit;
 #pragma unroll
