@@ -413,7 +413,8 @@ typedef struct {
  * q scaled by a power of two of its row, probabilities scaled so that they keep their bits), and
  * out is rounded once.  A call with the same arguments gives the same bits.
  * workspace: gptq_kv_attention_workspace_size() bytes (0 when the keys are not split), 256-byte
- * aligned.  Errors: as for gptq_kv_append, and GPTQ_E_WORKSPACE. */
+ * aligned.  max_rows == 0, like no rows: GPTQ_OK, nothing launched.
+ * Errors: as for gptq_kv_append, and GPTQ_E_WORKSPACE. */
 gptq_status gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const gptq_kv_batch* batch,
                                              const gptq_attention* call, size_t* bytes);
 gptq_status gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const gptq_attention* call,

@@ -87,6 +87,9 @@ gptq_status check_rope(const gptq_rope* r, int head_dim) {
   return GPTQ_OK;
 }
 
+// Whether a call has nothing to attend for.
+bool no_queries(const gptq_kv_batch& b) { return b.rows == 0 || b.batch == 0 || b.max_rows == 0; }
+
 gptq_status check_attention(const gptq_kv_cache* c, const gptq_kv_batch* b, const gptq_attention* a) {
   gptq_status st = check_cache(c);
   if (st == GPTQ_OK) st = check_batch(b);
@@ -200,7 +203,7 @@ gptq_status gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const g
   if (!bytes) return GPTQ_E_INVALID_ARG;
   const gptq_status st = check_attention(cache, batch, call);
   if (st != GPTQ_OK) return st;
-  *bytes = batch->rows == 0 || batch->batch == 0 ? 0 : kv_attention_ws_bytes(*cache, *batch, *call);
+  *bytes = no_queries(*batch) ? 0 : kv_attention_ws_bytes(*cache, *batch, *call);
   return GPTQ_OK;
 }
 
@@ -208,7 +211,7 @@ gptq_status gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* b
                               const void* q, void* out, void* workspace, size_t workspace_bytes, void* stream) {
   gptq_status st = check_attention(cache, batch, call);
   if (st != GPTQ_OK) return st;
-  if (batch->rows == 0 || batch->batch == 0) return GPTQ_OK;
+  if (no_queries(*batch)) return GPTQ_OK;
   const int64_t width = (int64_t)call->q_heads * cache->head_dim;
   if ((st = check_rows(q, width, call->q_stride)) != GPTQ_OK) return st;
   if ((st = check_rows(out, width, call->out_stride)) != GPTQ_OK) return st;
