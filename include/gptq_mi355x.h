@@ -310,7 +310,12 @@ gptq_status gptq_pack(const uint8_t* codes, const float* scales, const int32_t* 
  *
  * What lives in device memory (page tables, lengths, adapter ids) cannot be checked by the host
  * without a synchronisation, so the kernels check it where they use it: an entry outside its range
- * is treated as absent, as stated at each call, and never addresses memory. */
+ * is treated as absent, as stated at each call, and never addresses memory.
+ *
+ * GPTQ_E_SHAPE stands for sizes outside the ranges below, for calls whose launch would have 2^32 threads or
+ * more, and for attention that splits its keys over the card into 2^31 steps or more (a step: 32 tokens of 16
+ * or 32 (row, head) columns of one sequence and kv head; max_kv, the window and the table bound the tokens).
+ * The workspace queries refuse what the calls refuse. */
 
 /* A paged cache of one layer.  A page holds page_size consecutive tokens of one sequence; for each
  * page and head its codes are int8 in [-127, 127] with one float32 scale: value = code * scale. */

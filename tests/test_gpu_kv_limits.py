@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from test_gpu_kv_cache import Pool, dev, offsets, say
+from test_gpu_kv_cache import Pool, check_attention, dev, host, offsets, say
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +29,19 @@ def test_no_rows_of_any_sequence(length):
                                  out=out)
     torch.cuda.synchronize()
     assert got is out and bool((out == 7.0).all())
+
+
+def test_short_sequences_in_a_wide_table():
+    """2^12 units over a table of 2^24 tokens each: what a call can see is 64 tokens."""
+    import torch
+    batch, hkv = 512, 8
+    rng = np.random.default_rng(8)
+    lens = rng.integers(1, 65, batch).astype(np.int32)
+    say("wide table", batch)
+    pool = Pool(lens.tolist(), 256, hkv, 64, seed=4)
+    table = torch.full((batch, 1 << 16), -1, dtype=torch.int32, device="cuda")
+    table[:, :pool.table.shape[1]] = dev(pool.table)
+    cu = offsets([1] * batch)
+    q = dev(rng.normal(0, 1.5, (batch, hkv, 64)), torch.float16)
+    out = pool.cache().attention(q, table, dev(lens), dev(cu), max_q=1, max_kv=64)
+    check_attention(host(out), host(q), pool, lens, cu, "f16", 64 ** -0.5)

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import weight_only_quantized_amd as wq
-from test_serving_cpu import Attention, attention, batch, cache
+from test_serving_cpu import A, FREE, Attention, Bank, append, attention, batch, cache
 
 
 def workspace(c, b, **kw):
@@ -23,3 +23,32 @@ def test_no_rows_of_any_sequence(max_kv):
     b = batch(max_rows=0, table_width=4096)
     assert workspace(cache(), b, max_kv=max_kv) == ("OK", 0)
     assert attention(b=b, max_kv=max_kv) == "OK"
+
+
+def test_steps_count_by_what_a_call_can_see():
+    """A wide table is no reason to refuse short sequences; what cannot be counted is refused by both
+    entry points, as a size."""
+    c = cache(kv_heads=8, page_size=256, num_pages=4096)
+    b = batch(rows=1 << 20, max_rows=1, batch=1 << 20, table_width=1 << 16)
+    wide = dict(q_heads=8, q_stride=512, out_stride=512)
+    assert workspace(c, b, max_kv=64, **wide) == ("OK", 0)
+    assert workspace(c, b, max_kv=1 << 24, window=40, **wide) == ("OK", 0)
+    assert workspace(c, b, max_kv=1 << 24, **wide)[0] == "E_SHAPE"
+    assert attention(c=c, b=b, max_kv=1 << 24, **wide) == "E_SHAPE"
+    # any number of sequences, columns and tokens
+    b = batch(rows=1 << 24, max_rows=1 << 24, batch=1 << 20, table_width=1 << 22)
+    c.kv_heads = 1024
+    for q_heads in (1024, 65536):
+        huge = dict(q_heads=q_heads, q_stride=q_heads * 64, out_stride=q_heads * 64, max_kv=1 << 30)
+        assert workspace(c, b, **huge)[0] == "E_SHAPE" and attention(c=c, b=b, **huge) == "E_SHAPE"
+
+
+def test_launches_that_cannot_number_their_threads():
+    lib, n = wq.load_library(), ctypes.c_size_t()
+    c, b = cache(kv_heads=1024, num_pages=4096), batch(rows=1 << 24, max_rows=1 << 24, batch=1)
+    far = FREE + (1 << 45)
+    assert append(c=c, b=b, ks=65536, v=far, vs=65536) == "E_SHAPE"
+    assert wq.STATUS[lib.gptq_kv_read(ctypes.byref(c), ctypes.byref(b), FREE, far, 0, None)] == "E_SHAPE"
+    bank = Bank(A, A + (1 << 20), A + (2 << 20), 3, 16, 64, 1 << 20, 0, 0)
+    assert wq.STATUS[lib.gptq_lora_workspace_size(ctypes.byref(bank), 1 << 24, ctypes.byref(n))] == "E_SHAPE"
+    assert wq.STATUS[lib.gptq_lora_add(ctypes.byref(bank), FREE, far, FREE, 1 << 24, far, None, 0, None)] == "E_SHAPE"

@@ -261,21 +261,31 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(gptq_kv_cache c, gptq
   }
 }
 
+struct AppendGrid {
+  int64_t slots, page_blocks, blocks;
+  int chunks, threads, waves_per_row;
+};
+AppendGrid append_grid(const gptq_kv_cache& c, const gptq_kv_batch& b, int q_heads) {
+  AppendGrid g;
+  const int page_shift = __builtin_ctz(c.page_size);
+  // slots of every sequence: its rows / page, rounded down, and two
+  g.slots = b.max_rows == 1 ? b.batch : (b.rows >> page_shift) + 2 * (int64_t)b.batch;
+  g.page_blocks = g.slots * c.kv_heads * 2;
+  g.waves_per_row = (q_heads * (c.head_dim / 8) + 63) / 64;
+  g.chunks = (c.head_dim / 8) << page_shift;
+  g.threads = g.chunks > 1024 ? 1024 : 256;
+  g.blocks = g.page_blocks + (b.rows * g.waves_per_row + g.threads / 64 - 1) / (g.threads / 64);
+  return g;
+}
+
 template <int BF16, int DIM>
 hipError_t launch_append_dim(const KvAppendCall& a, int page_shift, hipStream_t s) {
-  // slots of every sequence: its rows / page, rounded down, and two
-  const int64_t slots = a.b.max_rows == 1 ? a.b.batch : (a.b.rows >> page_shift) + 2 * (int64_t)a.b.batch;
-  const int64_t page_blocks = slots * a.c.kv_heads * 2;
-  const int waves_per_row = (a.q_heads * (DIM / 8) + 63) / 64;
-  const int chunks = (DIM / 8) << page_shift;
-  const int threads = chunks > 1024 ? 1024 : 256;
-  const int64_t q_blocks = a.q ? (a.b.rows * waves_per_row + threads / 64 - 1) / (threads / 64) : 0;
-  const int64_t blocks = page_blocks + q_blocks;
-  if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-#define GQ_APPEND(C, T)                                                                                          \
-  kv_append_kernel<BF16, C, DIM, T><<<dim3((uint32_t)blocks), dim3(T), 0, s>>>(a, (int)page_blocks, (int)slots, \
-                                                                               page_shift, waves_per_row)
-  if (threads == 1024) {
+  const AppendGrid g = append_grid(a.c, a.b, a.q_heads);
+  const int chunks = g.chunks;
+#define GQ_APPEND(C, T)                                                                                            \
+  kv_append_kernel<BF16, C, DIM, T><<<dim3((uint32_t)g.blocks), dim3(T), 0, s>>>(a, (int)g.page_blocks, (int)g.slots, \
+                                                                                 page_shift, g.waves_per_row)
+  if (g.threads == 1024) {
     if (chunks <= 2048) GQ_APPEND(2, 1024);
     else GQ_APPEND(4, 1024);
   } else if (chunks <= 256) {
@@ -289,7 +299,19 @@ hipError_t launch_append_dim(const KvAppendCall& a, int page_shift, hipStream_t 
   return hipGetLastError();
 }
 
+int read_waves_per_row(const gptq_kv_cache& c) { return (c.kv_heads * (c.head_dim / 8) + 63) / 64; }
+int64_t read_blocks(const gptq_kv_cache& c, const gptq_kv_batch& b) {
+  return (b.rows * read_waves_per_row(c) + kThreads / 64 - 1) / (kThreads / 64);
+}
+
 }  // namespace
+
+bool kv_append_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, int q_heads) {
+  const AppendGrid g = append_grid(c, b, q_heads);
+  return grid_fits(g.blocks, g.threads);
+}
+
+bool kv_read_fits(const gptq_kv_cache& c, const gptq_kv_batch& b) { return grid_fits(read_blocks(c, b), kThreads); }
 
 hipError_t launch_kv_append(const KvAppendCall& a, hipStream_t s) {
   const int page_shift = __builtin_ctz(a.c.page_size);
@@ -301,10 +323,8 @@ hipError_t launch_kv_append(const KvAppendCall& a, hipStream_t s) {
 hipError_t launch_kv_read(const gptq_kv_cache& c, const gptq_kv_batch& b, void* k_out, void* v_out, int dtype,
                           hipStream_t s) {
   const int page_shift = __builtin_ctz(c.page_size);
-  const int waves_per_row = (c.kv_heads * (c.head_dim / 8) + 63) / 64;
-  const int64_t blocks = (b.rows * waves_per_row + kThreads / 64 - 1) / (kThreads / 64);
-  if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const dim3 grid((uint32_t)blocks), block(kThreads);
+  const int waves_per_row = read_waves_per_row(c);
+  const dim3 grid((uint32_t)read_blocks(c, b)), block(kThreads);
   if (dtype == GPTQ_F16) kv_read_kernel<GPTQ_F16><<<grid, block, 0, s>>>(c, b, k_out, v_out, page_shift, waves_per_row);
   else if (dtype == GPTQ_BF16) kv_read_kernel<GPTQ_BF16><<<grid, block, 0, s>>>(c, b, k_out, v_out, page_shift, waves_per_row);
   else kv_read_kernel<GPTQ_F32><<<grid, block, 0, s>>>(c, b, k_out, v_out, page_shift, waves_per_row);

@@ -49,7 +49,8 @@ struct DecodePlan {
   int col_tiles;    // 16-column tiles of a unit: 1 or 2
   int col_groups;   // units of a sequence and kv head, at most
   int waves, wave_bits;    // when split a power of two
-  int units;        // batch * kv_heads * col_groups
+  int units;        // batch * kv_heads * col_groups, at most 2^31 - 1 (kv_decode_fits refuses so many)
+  int64_t steps;    // of a unit, at most
   int width;        // columns of a part: those that a unit can have
   int local;        // a workgroup of kLocalWaves takes a unit and joins it
   int split;        // units may cross waves: they leave parts; else (nor local) a wave takes a unit
@@ -566,8 +567,8 @@ DecodePlan plan_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_at
   p.col_tiles = columns <= 16 || p.local ? 1 : 2;
   p.width = (int)(columns < 16 * p.col_tiles ? columns : 16 * p.col_tiles);
   p.col_groups = (int)((columns + 16 * p.col_tiles - 1) / (16 * p.col_tiles));
-  const int64_t steps = (kv_span(c, b, a) + 15 + kStep - 1) / kStep;      // a range starts at 16: up to 15 more
-  const int64_t units = (int64_t)b.batch * c.kv_heads * p.col_groups;
+  const int64_t steps = p.steps = (kv_span(c, b, a) + 15 + kStep - 1) / kStep;      // a range starts at 16: up to 15 more
+  const int64_t all = (int64_t)b.batch * c.kv_heads * p.col_groups, units = all < 0x7fffffff ? all : 0x7fffffff;
   const int64_t fit = 256 * kWaves * 2;
   // Many short units: a wave takes a whole one, so that nothing is joined and no wave looks for its share.
   // Us, a wave a unit / split, 8 kv heads of 128, sequences of very different lengths up to: 64 of 128 8.7 /
@@ -575,7 +576,7 @@ DecodePlan plan_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_at
   // 2000: 95 / 83; 16 heads of 64: 64 of 500 14.7 / 16.2, 1000: 24.3 / 20.9.
   const bool whole = steps <= 48 && steps * 32 * 128 <= units * c.head_dim;
   p.split = !p.local && steps > 1 && !whole;
-  p.units = units > 0x7fffffff ? 0x7fffffff : (int)units;
+  p.units = (int)units;
   p.many_parts = steps > 1024 || units < fit / 32;
   p.wave_bits = 0;
   while (1 << p.wave_bits < fit && 1 << p.wave_bits < units * steps) ++p.wave_bits;
@@ -583,7 +584,19 @@ DecodePlan plan_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_at
   return p;
 }
 
+int64_t kernel_blocks(const DecodePlan& p) { return p.local ? p.units : ((int64_t)p.waves + kWaves - 1) / kWaves; }
+int64_t join_blocks(const DecodePlan& p, const gptq_kv_batch& b, const gptq_attention& a) {
+  return p.many_parts ? b.rows * a.q_heads : (b.rows * a.q_heads + kWaves - 1) / kWaves;
+}
+
 }  // namespace
+
+bool kv_decode_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  const DecodePlan p = plan_of(c, b, a);
+  if (p.units == 0x7fffffff || !grid_fits(kernel_blocks(p), p.local ? 64 * kLocalWaves : kThreads)) return false;
+  // a split call's waves count the steps of all units in 32 bits
+  return !p.split || (p.steps * p.units <= 0x7fffffff && grid_fits(join_blocks(p, b, a), kThreads));
+}
 
 size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   const DecodePlan p = plan_of(c, b, a);
@@ -592,19 +605,12 @@ size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const 
 
 template <int BF16, int DIM>
 static hipError_t launch_dim(const KvAttentionCall& a, const DecodePlan& p, int page_shift, hipStream_t s) {
-  const int64_t joins = p.many_parts ? a.b.rows * a.a.q_heads : (a.b.rows * a.a.q_heads + kWaves - 1) / kWaves;
-  // all steps count in 32 bits
-  const int64_t steps = ((int64_t)a.b.table_width * a.c.page_size + kStep - 1) / kStep;
-  if (joins > 0x7fffffff || p.units == 0x7fffffff || (steps + 1) * p.units > 0x7fffffff)
-    return hipErrorInvalidConfiguration;
-  const dim3 grid((uint32_t)((p.waves + kWaves - 1) / kWaves)), block(kThreads);
-  if (p.local) {
-    const dim3 units((uint32_t)p.units), threads(64 * kLocalWaves);
-    kv_decode_kernel<BF16, DIM, 1, true><<<units, threads, 0, s>>>(a, p, page_shift);
-  } else if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1, false><<<grid, block, 0, s>>>(a, p, page_shift);
+  const dim3 grid((uint32_t)kernel_blocks(p)), block(kThreads), joins((uint32_t)join_blocks(p, a.b, a.a));
+  if (p.local) kv_decode_kernel<BF16, DIM, 1, true><<<grid, dim3(64 * kLocalWaves), 0, s>>>(a, p, page_shift);
+  else if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1, false><<<grid, block, 0, s>>>(a, p, page_shift);
   else kv_decode_kernel<BF16, DIM, 2, false><<<grid, block, 0, s>>>(a, p, page_shift);
-  if (p.split && p.many_parts) kv_join_kernel<BF16, DIM, kThreads><<<dim3((uint32_t)joins), block, 0, s>>>(a, p);
-  else if (p.split) kv_join_kernel<BF16, DIM, 64><<<dim3((uint32_t)joins), block, 0, s>>>(a, p);
+  if (p.split && p.many_parts) kv_join_kernel<BF16, DIM, kThreads><<<joins, block, 0, s>>>(a, p);
+  else if (p.split) kv_join_kernel<BF16, DIM, 64><<<joins, block, 0, s>>>(a, p);
   return hipGetLastError();
 }
 

@@ -348,25 +348,36 @@ __global__ void __launch_bounds__(64 * WAVES, 2) kv_prefill_kernel(KvAttentionCa
   }
 }
 
+int64_t column_slots(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a, int waves) {
+  return b.rows * (a.q_heads / c.kv_heads) / (32 * waves) + b.batch;
+}
+
 template <int BF16, int DIM, int WAVES>
 hipError_t launch_waves(const KvAttentionCall& a, int page_shift, hipStream_t s) {
-  const int group = a.a.q_heads / a.c.kv_heads;
-  const int64_t slots = a.b.rows * group / (32 * WAVES) + a.b.batch, blocks = slots * a.c.kv_heads;
-  if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const int64_t slots = column_slots(a.c, a.b, a.a, WAVES), blocks = slots * a.c.kv_heads;
   kv_prefill_kernel<BF16, DIM, WAVES><<<dim3((uint32_t)blocks), dim3(64 * WAVES), 0, s>>>(a, (int)slots, page_shift);
   return hipGetLastError();
 }
 
+// Waves of a workgroup (heads of 128).  Eight share the conversion of a tile: with two workgroups for every CU
+// or more (us, 8 waves / 4, 32 heads: 8192 tokens 561 / 609, 4096: 152 / 167); the smaller workgroups fill the
+// card better before (3000 tokens 96 / 95, 2048: 64 / 60).
+int waves_of(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  return c.head_dim == 128 && b.rows * a.q_heads >= 256 * 512 ? 8 : 4;
+}
+
 }  // namespace
+
+bool kv_prefill_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  const int waves = waves_of(c, b, a);
+  return grid_fits(column_slots(c, b, a, waves) * c.kv_heads, 64 * waves);
+}
 
 hipError_t launch_kv_prefill(const KvAttentionCall& a, hipStream_t s) {
   const int page_shift = __builtin_ctz(a.c.page_size);
   const bool bf16 = a.a.dtype == GPTQ_BF16;
   if (a.c.head_dim == 64) return bf16 ? launch_waves<1, 64, 4>(a, page_shift, s) : launch_waves<0, 64, 4>(a, page_shift, s);
-  // eight waves share the conversion of a tile: with two workgroups for every CU or more (us, 8 waves / 4, 32
-  // heads: 8192 tokens 561 / 609, 4096: 152 / 167); the smaller workgroups fill the card better before (3000
-  // tokens 96 / 95, 2048: 64 / 60)
-  if (a.b.rows * a.a.q_heads >= 256 * 512)
+  if (waves_of(a.c, a.b, a.a) == 8)
     return bf16 ? launch_waves<1, 128, 8>(a, page_shift, s) : launch_waves<0, 128, 8>(a, page_shift, s);
   return bf16 ? launch_waves<1, 128, 4>(a, page_shift, s) : launch_waves<0, 128, 4>(a, page_shift, s);
 }

@@ -642,8 +642,6 @@ void launch_up(const LoraCall& c, const LoraPlan& p, hipStream_t s) {
 template <int BF16>
 hipError_t launch_type(const LoraCall& c, hipStream_t s) {
   const LoraPlan p = plan_of(c.bank, c.M);
-  if ((int64_t)p.low_tiles * p.slices > 0x7fffffff || (int64_t)p.up_tiles * p.blocks_n > 0x7fffffff)
-    return hipErrorInvalidConfiguration;
   const int rank = c.bank.rank;
   if (p.here) ;
   else if (rank <= 16) launch_low<BF16, 1>(c, p, s);
@@ -657,6 +655,11 @@ hipError_t launch_type(const LoraCall& c, hipStream_t s) {
 }
 
 }  // namespace
+
+bool lora_fits(const gptq_lora_bank& bank, int64_t M) {
+  const LoraPlan p = plan_of(bank, M);
+  return grid_fits((int64_t)p.low_tiles * p.slices, kThreads) && grid_fits((int64_t)p.up_tiles * p.blocks_n, kThreads);
+}
 
 size_t lora_ws_bytes(const gptq_lora_bank& bank, int64_t M) {
   const LoraPlan p = plan_of(bank, M);

@@ -113,6 +113,10 @@ bool few_rows(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attenti
   return units <= 24 || (units <= 700 && units * span <= 700 * (span - 1000));
 }
 
+bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
+  return few_rows(c, b, a) ? kv_decode_fits(c, b, a) : kv_prefill_fits(c, b, a);
+}
+
 size_t kv_attention_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   return few_rows(c, b, a) ? kv_decode_ws_bytes(c, b, a) : 0;
 }
@@ -146,6 +150,7 @@ gptq_status gptq_kv_append(const gptq_kv_cache* cache, const gptq_kv_batch* batc
   if (q && (q_heads < 1 || q_heads > 65536)) return GPTQ_E_SHAPE;
   if (batch->rows == 0 || batch->batch == 0) return GPTQ_OK;
   const int64_t kv_width = (int64_t)cache->kv_heads * cache->head_dim, q_width = (int64_t)q_heads * cache->head_dim;
+  if (!kv_append_fits(*cache, *batch, q ? q_heads : 0)) return GPTQ_E_SHAPE;
   if ((st = check_rows(k, kv_width, k_stride)) != GPTQ_OK) return st;
   if ((st = check_rows(v, kv_width, v_stride)) != GPTQ_OK) return st;
   const size_t kb = row_bytes(batch->rows, kv_width, k_stride), vb = row_bytes(batch->rows, kv_width, v_stride);
@@ -188,6 +193,7 @@ gptq_status gptq_kv_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch,
   if (st != GPTQ_OK) return st;
   if (!is_16bit(dtype) && dtype != GPTQ_F32) return GPTQ_E_INVALID_ARG;
   if (batch->rows == 0 || batch->batch == 0) return GPTQ_OK;
+  if (!kv_read_fits(*cache, *batch)) return GPTQ_E_SHAPE;
   if (!k_out && !v_out) return GPTQ_E_INVALID_ARG;
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return GPTQ_E_INVALID_ARG;
   const size_t n = (size_t)batch->rows * cache->kv_heads * cache->head_dim * (dtype == GPTQ_F32 ? 4 : 2);
@@ -203,6 +209,7 @@ gptq_status gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const g
   if (!bytes) return GPTQ_E_INVALID_ARG;
   const gptq_status st = check_attention(cache, batch, call);
   if (st != GPTQ_OK) return st;
+  if (!no_queries(*batch) && !kv_attention_fits(*cache, *batch, *call)) return GPTQ_E_SHAPE;
   *bytes = no_queries(*batch) ? 0 : kv_attention_ws_bytes(*cache, *batch, *call);
   return GPTQ_OK;
 }
@@ -212,6 +219,7 @@ gptq_status gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* b
   gptq_status st = check_attention(cache, batch, call);
   if (st != GPTQ_OK) return st;
   if (no_queries(*batch)) return GPTQ_OK;
+  if (!kv_attention_fits(*cache, *batch, *call)) return GPTQ_E_SHAPE;
   const int64_t width = (int64_t)call->q_heads * cache->head_dim;
   if ((st = check_rows(q, width, call->q_stride)) != GPTQ_OK) return st;
   if ((st = check_rows(out, width, call->out_stride)) != GPTQ_OK) return st;
@@ -236,6 +244,7 @@ gptq_status gptq_lora_workspace_size(const gptq_lora_bank* bank, int64_t M, size
   if (!bytes) return GPTQ_E_INVALID_ARG;
   const gptq_status st = check_bank(bank, M);
   if (st != GPTQ_OK) return st;
+  if (M > 0 && !lora_fits(*bank, M)) return GPTQ_E_SHAPE;
   *bytes = M == 0 ? 0 : lora_ws_bytes(*bank, M);
   return GPTQ_OK;
 }
@@ -247,6 +256,7 @@ gptq_status gptq_lora_add(const gptq_lora_bank* bank, const void* x, const void*
   if (!bank->a || !bank->b || !bank->scale || !aligned(bank->a, 16) || !aligned(bank->b, 16) || !aligned(bank->scale, 4))
     return GPTQ_E_INVALID_ARG;
   if (M == 0) return GPTQ_OK;
+  if (!lora_fits(*bank, M)) return GPTQ_E_SHAPE;
   if (!x || !y || !out || !ids || !aligned(x, 16) || !aligned(y, 16) || !aligned(out, 16) || !aligned(ids, 4))
     return GPTQ_E_INVALID_ARG;
   const size_t xb = (size_t)M * bank->in_features * 2, yb = (size_t)M * bank->out_features * 2;

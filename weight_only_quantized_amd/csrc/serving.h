@@ -12,6 +12,9 @@ namespace gq {
 // True when device `dev` is a gfx950 (api.cpp; looked up once per device).
 bool is_gfx950_device(int dev);
 
+// Whether a launch can number its threads.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= 0x7fffffff && blocks * threads <= 0xffffffffLL; }
+
 struct KvAppendCall {
   gptq_kv_cache c;
   gptq_kv_batch b;
@@ -21,7 +24,9 @@ struct KvAppendCall {
   int32_t q_heads, bf16;
   gptq_rope rope;                // dim 0: no rotation
 };
+bool kv_append_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, int q_heads);
 hipError_t launch_kv_append(const KvAppendCall& a, hipStream_t s);
+bool kv_read_fits(const gptq_kv_cache& c, const gptq_kv_batch& b);
 hipError_t launch_kv_read(const gptq_kv_cache& c, const gptq_kv_batch& b, void* k_out, void* v_out, int dtype,
                           hipStream_t s);
 
@@ -56,9 +61,11 @@ inline bool kv_local(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_
   return units <= (columns <= 16 ? 256 * 128 / c.head_dim : 256) && (kv_span(c, b, a) + 46) / 32 * 64 * c.head_dim <= most;
 }
 // Few rows a sequence (kv_decode.hip): split over the keys, joined by a second launch.
+bool kv_decode_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
 size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
 hipError_t launch_kv_decode(const KvAttentionCall& a, hipStream_t s);
 // Many rows a sequence (kv_prefill.hip).
+bool kv_prefill_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a);
 hipError_t launch_kv_prefill(const KvAttentionCall& a, hipStream_t s);
 
 struct LoraCall {
@@ -69,6 +76,7 @@ struct LoraCall {
   uint16_t* out;
   void* ws;
 };
+bool lora_fits(const gptq_lora_bank& bank, int64_t M);
 size_t lora_ws_bytes(const gptq_lora_bank& bank, int64_t M);
 hipError_t launch_lora(const LoraCall& a, hipStream_t s);
 
