@@ -45,3 +45,19 @@ def test_short_sequences_in_a_wide_table():
     q = dev(rng.normal(0, 1.5, (batch, hkv, 64)), torch.float16)
     out = pool.cache().attention(q, table, dev(lens), dev(cu), max_q=1, max_kv=64)
     check_attention(host(out), host(q), pool, lens, cu, "f16", 64 ** -0.5)
+
+
+def test_a_workspace_on_the_host_is_refused():
+    import torch
+    import weight_only_quantized_amd as wq
+    say("host workspace")
+    pool = Pool([6000], 16, 2, 64, seed=5)
+    q, host_ws = dev(np.ones((1, 4, 64)), torch.float16), torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace"):
+        pool.cache().attention(q, dev(pool.table), dev(np.asarray([6000], np.int32)), dev(offsets([1])), max_q=1,
+                               workspace=host_ws)
+    a, b = (torch.zeros(s, dtype=torch.float16, device="cuda") for s in ((2, 64, 64), (2, 32, 64)))
+    bank = wq.LoraBank(a, b, torch.ones(2, device="cuda"))
+    x, y = (torch.zeros(s, dtype=torch.float16, device="cuda") for s in ((40, 64), (40, 32)))
+    with pytest.raises(ValueError, match="workspace"):
+        bank.add(y, x, torch.zeros(40, dtype=torch.int32, device="cuda"), workspace=host_ws)

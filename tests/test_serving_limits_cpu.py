@@ -52,3 +52,28 @@ def test_launches_that_cannot_number_their_threads():
     bank = Bank(A, A + (1 << 20), A + (2 << 20), 3, 16, 64, 1 << 20, 0, 0)
     assert wq.STATUS[lib.gptq_lora_workspace_size(ctypes.byref(bank), 1 << 24, ctypes.byref(n))] == "E_SHAPE"
     assert wq.STATUS[lib.gptq_lora_add(ctypes.byref(bank), FREE, far, FREE, 1 << 24, far, None, 0, None)] == "E_SHAPE"
+
+
+def test_tensors_on_the_host_are_refused():
+    """The kernels would be given host addresses."""
+    import torch
+    c = wq.KVCache.allocate(4, 16, 2, 64, device="cpu")
+    at, table, cu = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32), torch.tensor([0, 1], dtype=torch.int32)
+    k, q = torch.zeros(1, 2, 64, dtype=torch.float16), torch.zeros(1, 4, 64, dtype=torch.float16)
+    bank = wq.LoraBank(torch.zeros(2, 8, 64).half(), torch.zeros(2, 32, 8).half(), torch.zeros(2))
+    for call in (lambda: c.append(k, k, table, at, cu, max_new=1), lambda: c.attention(q, table, at, cu, max_q=1),
+                 lambda: c.read(table, at, cu, rows=1, max_rows=1),
+                 lambda: bank.add(torch.zeros(3, 32).half(), torch.zeros(3, 64).half(), torch.zeros(3, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+def test_a_workspace_is_a_whole_tensor_of_the_device():
+    """(Pointer, bytes) that the library may write to: not host memory, not a view that repeats itself."""
+    import torch
+    from weight_only_quantized_amd import serving
+    t = torch.zeros(16, dtype=torch.float32)                    # get_device() of the host is -1
+    assert serving._scratch(t, -1) == (t.data_ptr(), 64)
+    for bad, device in ((t, 0), (t[:1].expand(1 << 20), -1), (t[::2], -1)):
+        with pytest.raises(ValueError, match="workspace"):
+            serving._scratch(bad, device)

@@ -38,6 +38,8 @@ _BANK = struct.Struct("PPPiiiiii")         # gptq_lora_bank
 def _here(stream, index):
     """The hipStream_t to queue on when nothing has to wait or be recorded: no stream given, and the
     tensors' device is the current one.  Else None."""
+    if index < 0:
+        raise ValueError("the call runs on a GPU: its tensors must be there")
     return torch._C._cuda_getCurrentRawStream(index) if stream is None and torch._C._cuda_getDevice() == index else None
 
 
@@ -106,6 +108,13 @@ def _like(t):
 def _dense(t):
     """A contiguous 16-byte aligned tensor (copied if it is not)."""
     return t if t.is_contiguous() and not t.data_ptr() & 15 else t.clone(memory_format=torch.contiguous_format)
+
+
+def _scratch(t, device):
+    """(pointer, bytes) of a caller's workspace."""
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 class KVCache:
@@ -268,7 +277,7 @@ class KVCache:
         if need is None:
             need = self._workspace_size(batch, call, key)
         if workspace is not None:
-            ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            ws, need = _scratch(workspace, device)
         elif need:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
             ws = workspace.data_ptr()
@@ -343,16 +352,16 @@ class LoraBank:
         x, y = _dense(x), _dense(y)
         if out is None:
             out = torch.empty_like(y)          # y is dense here
-        if workspace is None:
-            size = self._sizes.get(M)
+        if workspace is not None:
+            ws, size = _scratch(workspace, self._index)
+        else:
+            size, ws = self._sizes.get(M), None
             if size is None:
                 size = self.workspace_size(M)
             if size:
                 workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
-        else:
-            size = workspace.numel() * workspace.element_size()
-        st = self._lib.gptq_lora_add(self._c, x.data_ptr(), y.data_ptr(), id_ptr, M, out.data_ptr(),
-                                     workspace.data_ptr() if workspace is not None else None, size, ptr)
+                ws = workspace.data_ptr()
+        st = self._lib.gptq_lora_add(self._c, x.data_ptr(), y.data_ptr(), id_ptr, M, out.data_ptr(), ws, size, ptr)
         if st:
             raise GPTQError(st, "gptq_lora_add", self._lib)
         return out
