@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import weight_only_quantized_amd as wq
-from test_serving_cpu import A, FREE, Attention, Bank, append, attention, batch, cache
+from test_serving_cpu import A, FREE, Attention, Bank, append, attention, batch, cache, rope
 
 
 def workspace(c, b, **kw):
@@ -77,3 +77,28 @@ def test_a_workspace_is_a_whole_tensor_of_the_device():
     for bad, device in ((t, 0), (t[:1].expand(1 << 20), -1), (t[::2], -1)):
         with pytest.raises(ValueError, match="workspace"):
             serving._scratch(bad, device)
+
+
+def test_outputs_do_not_overlap_tables():
+    """Page tables, lengths, rotation tables, ids and adapters' scales are read while outputs and
+    workspaces are written."""
+    lib, n = wq.load_library(), ctypes.c_size_t()
+    here = FREE + (8 << 20)
+    for table in ("page_table", "at", "cu"):
+        b = batch(**{table: here})
+        assert attention(b=b, out=here) == "E_INVALID_ARG", table
+        assert append(b=b, q=FREE + (2 << 20), qs=128, heads=2, out=here, os_=128, rope=rope()) == "E_INVALID_ARG", table
+        for k, v in ((here, None), (None, here)):
+            assert wq.STATUS[lib.gptq_kv_read(ctypes.byref(cache()), ctypes.byref(b), k, v, 0, None)] == "E_INVALID_ARG", table
+        long = batch(rows=1, max_rows=1, batch=1, table_width=4096, **{table: here})
+        assert workspace(cache(), long, max_kv=65536)[1] > 0
+        assert attention(b=long, max_kv=65536, ws=here, ws_bytes=1 << 30) == "E_INVALID_ARG", table
+    for table in ("cos", "sin"):
+        assert append(q=FREE + (2 << 20), qs=128, heads=2, out=here, os_=128, rope=rope(**{table: here})) == "E_INVALID_ARG", table
+
+    def lora(scale=A + (2 << 20), ids=FREE + (2 << 20), out=FREE + (3 << 20), ws=FREE + (4 << 20)):
+        bank = Bank(A, A + (1 << 20), scale, 3, 64, 64, 96, 0, 0)
+        return wq.STATUS[lib.gptq_lora_add(ctypes.byref(bank), FREE, FREE + (1 << 20), ids, 5, out, ws, 1 << 20, None)]
+    assert lora() in ("E_HIP", "E_DEVICE")
+    for kw in (dict(scale=here, out=here), dict(scale=here, ws=here), dict(ids=here, ws=here), dict(ids=here, out=here)):
+        assert lora(**kw) == "E_INVALID_ARG", kw

@@ -79,6 +79,12 @@ bool overlaps_cache(const gptq_kv_cache* c, const void* p, size_t n) {
          overlaps(p, n, c->k_scale, scales) || overlaps(p, n, c->v_scale, scales);
 }
 
+// Whether [p, p + n) overlaps the batch's tables.
+bool overlaps_tables(const gptq_kv_batch* b, const void* p, size_t n) {
+  return overlaps(p, n, b->page_table, (size_t)b->batch * b->table_width * 4) || overlaps(p, n, b->at, (size_t)b->batch * 4) ||
+         overlaps(p, n, b->cu, ((size_t)b->batch + 1) * 4);
+}
+
 gptq_status check_rope(const gptq_rope* r, int head_dim) {
   if (r->reserved != 0 || !r->cos || !r->sin || !aligned(r->cos, 16) || !aligned(r->sin, 16)) return GPTQ_E_INVALID_ARG;
   if (r->interleaved != 0 && r->interleaved != 1) return GPTQ_E_INVALID_ARG;
@@ -165,7 +171,10 @@ gptq_status gptq_kv_append(const gptq_kv_cache* cache, const gptq_kv_batch* batc
         rows_overlap(k, kv_width, k_stride, q_out, q_width, q_out_stride, rows) ||
         rows_overlap(v, kv_width, v_stride, q_out, q_width, q_out_stride, rows))
       return GPTQ_E_INVALID_ARG;
-    if (overlaps_cache(cache, q_out, ob)) return GPTQ_E_INVALID_ARG;
+    const size_t turns = (size_t)rope->rows * (rope->dim / 2) * 4;
+    if (overlaps_cache(cache, q_out, ob) || overlaps_tables(batch, q_out, ob) || overlaps(q_out, ob, rope->cos, turns) ||
+        overlaps(q_out, ob, rope->sin, turns))
+      return GPTQ_E_INVALID_ARG;
   }
   if ((st = check_device()) != GPTQ_OK) return st;
   KvAppendCall a{};
@@ -197,7 +206,8 @@ gptq_status gptq_kv_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch,
   if (!k_out && !v_out) return GPTQ_E_INVALID_ARG;
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return GPTQ_E_INVALID_ARG;
   const size_t n = (size_t)batch->rows * cache->kv_heads * cache->head_dim * (dtype == GPTQ_F32 ? 4 : 2);
-  if (overlaps(k_out, n, v_out, n) || overlaps_cache(cache, k_out, n) || overlaps_cache(cache, v_out, n))
+  if (overlaps(k_out, n, v_out, n) || overlaps_cache(cache, k_out, n) || overlaps_cache(cache, v_out, n) ||
+      overlaps_tables(batch, k_out, n) || overlaps_tables(batch, v_out, n))
     return GPTQ_E_INVALID_ARG;
   if ((st = check_device()) != GPTQ_OK) return st;
   const hipError_t e = launch_kv_read(*cache, *batch, k_out, v_out, dtype, (hipStream_t)stream);
@@ -225,12 +235,13 @@ gptq_status gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* b
   if ((st = check_rows(out, width, call->out_stride)) != GPTQ_OK) return st;
   const size_t qb = row_bytes(batch->rows, width, call->q_stride), ob = row_bytes(batch->rows, width, call->out_stride);
   if (rows_overlap(q, width, call->q_stride, out, width, call->out_stride, batch->rows) ||
-      overlaps_cache(cache, out, ob))
+      overlaps_cache(cache, out, ob) || overlaps_tables(batch, out, ob))
     return GPTQ_E_INVALID_ARG;
   const size_t need = kv_attention_ws_bytes(*cache, *batch, *call);
   if (need > 0) {
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return GPTQ_E_WORKSPACE;
-    if (overlaps(workspace, need, q, qb) || overlaps(workspace, need, out, ob) || overlaps_cache(cache, workspace, need))
+    if (overlaps(workspace, need, q, qb) || overlaps(workspace, need, out, ob) || overlaps_cache(cache, workspace, need) ||
+        overlaps_tables(batch, workspace, need))
       return GPTQ_E_INVALID_ARG;
   }
   if ((st = check_device()) != GPTQ_OK) return st;
@@ -263,12 +274,14 @@ gptq_status gptq_lora_add(const gptq_lora_bank* bank, const void* x, const void*
   const size_t ab = (size_t)bank->adapters * bank->rank * bank->in_features * 2;
   const size_t bb = (size_t)bank->adapters * bank->rank * bank->out_features * 2;
   if (overlaps(out, yb, x, xb) || (out != y && overlaps(out, yb, y, yb)) || overlaps(out, yb, bank->a, ab) ||
-      overlaps(out, yb, bank->b, bb) || overlaps(out, yb, ids, (size_t)M * 4))
+      overlaps(out, yb, bank->b, bb) || overlaps(out, yb, ids, (size_t)M * 4) ||
+      overlaps(out, yb, bank->scale, (size_t)bank->adapters * 4))
     return GPTQ_E_INVALID_ARG;
   const size_t need = lora_ws_bytes(*bank, M);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return GPTQ_E_WORKSPACE;
   if (overlaps(workspace, need, x, xb) || overlaps(workspace, need, y, yb) || overlaps(workspace, need, out, yb) ||
-      overlaps(workspace, need, bank->a, ab) || overlaps(workspace, need, bank->b, bb))
+      overlaps(workspace, need, bank->a, ab) || overlaps(workspace, need, bank->b, bb) ||
+      overlaps(workspace, need, ids, (size_t)M * 4) || overlaps(workspace, need, bank->scale, (size_t)bank->adapters * 4))
     return GPTQ_E_INVALID_ARG;
   if ((st = check_device()) != GPTQ_OK) return st;
   const LoraCall c{*bank, (const uint16_t*)x, (const uint16_t*)y, ids, M, (uint16_t*)out, workspace};
