@@ -61,3 +61,70 @@ def test_a_workspace_on_the_host_is_refused():
     x, y = (torch.zeros(s, dtype=torch.float16, device="cuda") for s in ((40, 64), (40, 32)))
     with pytest.raises(ValueError, match="workspace"):
         bank.add(y, x, torch.zeros(40, dtype=torch.int32, device="cuda"), workspace=host_ws)
+
+
+# (lengths, cu, max_q) of four rows over two sequences of 64 cached tokens -> what each row gives: None where it
+# stays as it was, 0 where it sees nothing, else (sequence, tokens that it sees)
+BOUNDS = {
+    "all_rows": ([64, 64], [0, 2, 4], 4, [(0, 63), (0, 64), (1, 63), (1, 64)]),
+    "first_rows": ([64, 64], [0, 2, 4], 1, [(0, 63), None, (1, 63), None]),
+    "past_the_table": ([1 << 30, 64], [0, 2, 4], 4, [(0, 64), (0, 64), (1, 63), (1, 64)]),
+    "no_tokens": ([-4, 0], [0, 2, 4], 4, [0, 0, 0, 0]),
+    "more_rows_than_tokens": ([1, 2], [0, 2, 4], 4, [0, (0, 1), (1, 1), (1, 2)]),
+    "rows_that_descend": ([64, 64], [0, -9, 4], 4, [None, None, None, None]),
+    "rows_past_the_last": ([64, 64], [9, 12, 15], 4, [None, None, None, None]),
+    "second_past_the_last": ([64, 64], [0, 2, 9], 4, [(0, 63), (0, 64), None, None]),
+}
+
+
+@pytest.mark.parametrize("hkv,heads", [(1, 2), (1, 40), (16, 1024)], ids=["few_heads", "heads", "many_heads"])
+@pytest.mark.parametrize("case", BOUNDS)
+def test_each_row_within_the_stated_bounds(case, hkv, heads):
+    """Rows that are absent stay as they were, rows that see nothing are zero, all others are right."""
+    import torch
+    lens, cu, max_q, rows = BOUNDS[case]
+    say("bounds", case, heads)
+    pool = Pool([64, 64], 16, hkv, 64, seed=71)
+    q = dev(np.random.default_rng(3).normal(0, 1.5, (4, heads, 64)), torch.float16)
+    out = torch.full_like(q, 77.0)
+    pool.cache().attention(q, dev(pool.table), dev(np.asarray(lens, np.int32)), dev(np.asarray(cu, np.int32)), max_q=max_q,
+                           out=out)
+    got = host(out)
+    for i, row in enumerate(rows):
+        if row is None:
+            assert np.all(got[i] == 77.0), (case, i)
+        elif row == 0:
+            assert np.all(got[i] == 0.0), (case, i)
+        else:
+            one = Pool([64], 16, hkv, 64, seed=71)
+            for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
+                setattr(one, name, getattr(pool, name))
+            one.table = pool.table[row[0]:row[0] + 1]
+            check_attention(got[i:i + 1], host(q)[i:i + 1], one, [row[1]], offsets([1]), "f16", 64 ** -0.5, label=(case, i))
+
+
+def test_a_page_that_fills_token_by_token():
+    """Each growth of a page's scale rounds its older codes once more, by half a code of the new scale, and
+    what they were off before shrinks with the ratio: a value is off by half a code for its own rounding and
+    half for each growth after it, and a few float32 roundings of 127 codes."""
+    import torch
+    rng = np.random.default_rng(9)
+    steps, page = 96, 32
+    pool = Pool([steps], page, 2, 64, seed=51)
+    cache, table, cu = pool.cache(), dev(pool.table), dev(offsets([1]))
+    grow = np.exp(np.arange(steps) / 40.0)[:, None, None]                    # values that grow all along
+    x = dev(rng.normal(0, 0.3, (steps, 2, 64)) * grow, torch.float16)
+    growths = np.zeros((steps, 2))
+    before = None
+    for t in range(steps):
+        cache.append(x[t:t + 1], x[t:t + 1], table, dev(np.asarray([t], np.int32)), cu, max_new=1)
+        now = host(cache.k_scale)[pool.table[0, t // page]]
+        if t % page:
+            growths[t - t % page:t] += now > before
+        before = now
+    k, v = cache.read(table, dev(np.zeros(1, np.int32)), dev(offsets([steps])), rows=steps, max_rows=steps, dtype=torch.float32)
+    unit = host(cache.k_scale)[pool.table[0, np.arange(steps) // page]]
+    bound = unit[..., None] * (0.5 * (1 + growths) + (1 + growths) * 127 * 4 * 2.0 ** -23)[..., None]
+    assert growths.max() > 3
+    for got in (k, v):
+        assert np.all(np.abs(host(got) - host(x)) <= bound), float((np.abs(host(got) - host(x)) / bound).max())

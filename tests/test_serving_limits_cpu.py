@@ -102,3 +102,19 @@ def test_outputs_do_not_overlap_tables():
     assert lora() in ("E_HIP", "E_DEVICE")
     for kw in (dict(scale=here, out=here), dict(scale=here, ws=here), dict(ids=here, ws=here), dict(ids=here, out=here)):
         assert lora(**kw) == "E_INVALID_ARG", kw
+
+
+@pytest.mark.parametrize("batch_size,max_rows,tokens", [(1, 1, 65536), (64, 1, 4096), (4, 64, 16000)])
+def test_a_split_call_needs_its_workspace(batch_size, max_rows, tokens):
+    """Calls whose keys are split: a missing, short, misaligned or overlapping workspace is refused."""
+    rows = batch_size * max_rows
+    c = cache(kv_heads=8, num_pages=512)
+    b = batch(rows=rows, max_rows=max_rows, batch=batch_size, table_width=4096)
+    far = FREE + (1 << 30)
+    kw = dict(max_kv=tokens, q_heads=32, q_stride=2048, out_stride=2048)
+    status, need = workspace(c, b, **kw)
+    assert status == "OK" and need > 0
+    for ws in (dict(), dict(ws=far, ws_bytes=need - 1), dict(ws=far + 128, ws_bytes=need)):
+        assert attention(c=c, b=b, out=FREE + (64 << 20), **ws, **kw) == "E_WORKSPACE", ws
+    assert attention(c=c, b=b, out=FREE + (64 << 20), ws=FREE, ws_bytes=need, **kw) == "E_INVALID_ARG"
+    assert attention(c=c, b=b, out=FREE + (64 << 20), ws=far, ws_bytes=need, **kw) in ("E_HIP", "E_DEVICE")
