@@ -220,12 +220,11 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   float q_scale[CT], top[CT], total[CT];
   f16x8 q[CT][2 * KL];
   u32x4 query[CT][2 * KL];
-  auto page_id = [&](int base, int end) {         // 16 tokens a lane
+  auto page_id = [&](int base) {                  // 16 tokens a lane
     const int my_pos = base + lane * 16;
-    return tile_page_id(a.c, a.b, seq, my_pos, my_pos < end, page_shift);
+    return tile_page_id(a.c, a.b, seq, my_pos, my_pos < run1, page_shift);
   };
-  int page = page_id(run0, run1);                 // on its way with the query
-  const int head_page = page_id(work.lo, work.hi);     // of the unit's first tokens, for one reference of all its parts
+  int page = page_id(run0);                       // on its way with the query
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     int c = first_col + ct * 16 + col16;
@@ -402,9 +401,8 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     load_values(odd, 1);
     __builtin_amdgcn_sched_barrier(0);
   };
-  const TilePage head_pages = tile_scales(a.c, head_page, kv_head);
   start_run();
-  const float ref = scale_reference(marked(head_pages).v_scale);
+  const float ref = scale_reference(marked(pages).v_scale);        // of this part
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) q_scale[ct] = query_f16<BF16, 2 * KL>(query[ct], q[ct], 16, 32) * (a.a.scale * kLog2e);
   for (;;) {
@@ -435,7 +433,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     }
     base += kMaxRun;
     if (base >= run1) break;
-    page = page_id(base, run1);
+    page = page_id(base);
     start_run();
   }
 
@@ -491,14 +489,14 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     float most = kNoTop, all = 0.0f;
     f32x4 o{0, 0, 0, 0};
     for (int w = 0; w < count; ++w) most = __builtin_fmaxf(most, sums[w][c - first_col][DIM]);
+    const float ref = sums[0][c - first_col][DIM + 2];
     for (int w = 0; w < count; ++w) {
       const float* from = sums[w][c - first_col];
-      const float in = __builtin_amdgcn_exp2f(from[DIM] - most);
-      all = __builtin_fmaf(from[DIM + 1], in, all);
-      o += *(const f32x4*)(from + d) * in;
+      const float in = from[DIM] - most;
+      all = __builtin_fmaf(from[DIM + 1], __builtin_amdgcn_exp2f(in + (ref - from[DIM + 2])), all);
+      o += *(const f32x4*)(from + d) * __builtin_amdgcn_exp2f(in);
     }
-    store_joined<BF16>(a.out + (int64_t)(work.s.row0 + c / group) * a.a.out_stride + (kv_head * group + c % group) * DIM + d, o, all,
-                       sums[0][c - first_col][DIM + 2]);
+    store_joined<BF16>(a.out + (int64_t)(work.s.row0 + c / group) * a.a.out_stride + (kv_head * group + c % group) * DIM + d, o, all, ref);
   }
 }
 
@@ -523,24 +521,24 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, De
   const float* part = (const float*)((const uint8_t*)a.ws + parts_offset(plan)) +
                       ((int64_t)parts.first * plan.width + c % width) * kPitch;
   const int thread = threadIdx.x % THREADS, in_part = thread % kLanes;
-  const float ref = part[DIM + 2];
+  const float ref = part[DIM + 2];               // sums are joined relative to the first part's
   float most = kNoTop, all = 0.0f;
   f32x4 o{0, 0, 0, 0};
-  auto join = [&](float top, float sum, f32x4 v) {
+  auto join = [&](float top, float sum, float more, f32x4 v) {          // sum: times 2^more
     const float now = __builtin_fmaxf(most, top);
     const float keep = __builtin_amdgcn_exp2f(most - now), in = __builtin_amdgcn_exp2f(top - now);
-    all = all * keep + sum * in;
+    all = all * keep + sum * __builtin_amdgcn_exp2f(top - now + more);
     o = o * keep + v * in;
     most = now;
   };
 #pragma unroll 4
   for (int i = thread / kLanes; i < count; i += kGroups) {
     const float* from = part + (int64_t)i * plan.width * kPitch;
-    join(from[DIM], from[DIM + 1], *(const f32x4*)(from + in_part * 4));
+    join(from[DIM], from[DIM + 1], ref - from[DIM + 2], *(const f32x4*)(from + in_part * 4));
   }
 #pragma unroll
   for (int d = kLanes; d < 64; d <<= 1)
-    join(__shfl_xor(most, d), __shfl_xor(all, d),
+    join(__shfl_xor(most, d), __shfl_xor(all, d), 0.0f,
          f32x4{__shfl_xor(o[0], d), __shfl_xor(o[1], d), __shfl_xor(o[2], d), __shfl_xor(o[3], d)});
   if constexpr (THREADS == kThreads) {
     const int wave = threadIdx.x >> 6;
@@ -552,7 +550,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttentionCall a, De
     __syncthreads();
     if (threadIdx.x < kLanes)
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) join(sums[w][DIM], sums[w][DIM + 1], *(const f32x4*)&sums[w][in_part * 4]);
+      for (int w = 1; w < kWaves; ++w) join(sums[w][DIM], sums[w][DIM + 1], 0.0f, *(const f32x4*)&sums[w][in_part * 4]);
   }
   if (thread >= kLanes) return;
   store_joined<BF16>(a.out + row * a.a.out_stride + head * DIM + in_part * 4, o, all, ref);

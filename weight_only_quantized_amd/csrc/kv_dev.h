@@ -86,9 +86,10 @@ __device__ __forceinline__ float lane_f32(float v, int lane) {
 // -79 and 41, so that those of 2^-39 .. 2^39 always do.
 __device__ __forceinline__ float scale_reference(float v_scale) {
   const uint64_t some = __ballot(v_scale > 0.0f);
-  int e = some ? __builtin_amdgcn_frexp_expf(lane_f32(v_scale, __builtin_ctzll(some))) : 0;
+  const int bits = __builtin_amdgcn_readlane(__builtin_bit_cast(int, v_scale), some ? __builtin_ctzll(some) : 0);
+  int e = some ? (bits >> 23) - 126 : 0;
   e = e < -60 ? -60 : e > 60 ? 60 : e;
-  return (float)__builtin_amdgcn_readfirstlane(e - 19);
+  return (float)(e - 19);
 }
 // log2 of a value scale (subnormal ones too; zero and what lies below the range count as its end), and 2^ref
 // over the scale by the same logarithm, so that both cancel; -inf and 0 when the tile is absent.
