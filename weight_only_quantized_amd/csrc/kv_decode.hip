@@ -6,13 +6,19 @@
 //     out_c = 2^r sum_j w_cj vc_j / sum_j w_cj 2^r / v_scale(j),
 // in one pass: the value scale rides in the exponent, so every weight that multiplies codes is
 // relative to the column's largest contribution, whatever the pages' scales are, and the sum of
-// probabilities takes the scale out again (2^r is about as large and keeps it in float32).  m_c only moves when a weight would pass 2^14 (then what
-// was summed is scaled by 2^(m - m')), so the usual step has no cross-lane work.
+// probabilities takes the scale out again (2^r is about as large and keeps it in float32).  m_c only
+// moves when a weight would pass 2^14 (then what was summed is scaled by 2^(m - m')), so the usual step
+// has no cross-lane work.
 //
 // What bounds it: the cache's bytes.  MFMA operands are float16: codes are exact integers (the byte
 // is spliced under an exponent that makes one unit 1, then the offset is subtracted), q is exact
-// after a power-of-two scaling of its row, and a weight keeps 11 bits down to 2^-20 of the largest
-// one: the one rounding below 32 bits, of the size of the output's own.
+// after a power-of-two scaling of its row.  A weight is the one rounding below 32 bits.  Units of up to
+// eight columns use half of a matrix instruction's sixteen: there each column stands twice, once with its
+// weights' first 11 bits and once with the rest of them, and the two sums are joined at the end: 21 bits,
+// down to 2^-31 of the largest weight, for one fused multiply-add a weight (us, 11 bits / 21: one token 11.25 /
+// 11.5, 64 sequences 48.4 / 48.8).  Wider units keep 11 bits down to 2^-20 of the largest weight, an error of
+// the size of a float16 output's own rounding; there the rest would take matrix instructions of its own (500
+// rows over 9000 tokens: 147 -> 170 us).
 //
 // Split.  The work is cut into steps of 32 tokens of a unit: up to 32 (row, head) columns of one
 // sequence and kv head.  All units' steps in order are dealt to as many waves as the card holds at
@@ -128,6 +134,10 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   const int col16 = lane & 15, quad = lane >> 4;
   const int room = key_room(call.b, call.a, page_shift);
   const int group = call.a.q_heads / call.c.kv_heads;
+  // up to eight columns: each stands twice, with its weights' first 11 bits and with the rest of them
+  const bool paired = CT == 1 && plan.width <= 8;
+  const uint32_t first_bits = paired ? 0xffffe000u : 0xffffffffu;
+  const float less = paired && col16 >= 8 ? -1.0f : 0.0f;
 
   // this wave's share of all steps (LOCAL: of its unit's), and the sequence where they
   // start: a scan over 64 sequences at a time, one a lane
@@ -227,7 +237,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   int page = page_id(run0);                       // on its way with the query
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
-    int c = first_col + ct * 16 + col16;
+    int c = first_col + ct * 16 + (paired ? col16 & 7 : col16);
     c = c < columns ? c : columns - 1;
     const int row = c / group, head = kv_head * group + c % group;
     const KeyRange r = key_range(s, row, a.a, room);
@@ -372,7 +382,12 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
         for (int e = 0; e < 4; ++e) {
           const float p = __builtin_amdgcn_exp2f(x[ct][t][e]);
           total[ct] = __builtin_fmaf(p, rv, total[ct]);
-          w[ct][t * 4 + e] = (_Float16)p;
+          if constexpr (CT == 1) {                // the first bits, or what is left of them, negative
+            const float first = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, p) & first_bits);
+            w[ct][t * 4 + e] = (_Float16)__builtin_fmaf(p, less, first);
+          } else {
+            w[ct][t * 4 + e] = (_Float16)p;
+          }
         }
       }
     }
@@ -444,6 +459,17 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     float sum = total[ct];
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
+    if (paired) {                                 // less the sums of what was left, in the lane eight on
+#pragma unroll
+      for (int t = 0; t < VB; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mine = acc[ct][t][e];
+          acc[ct][t][e] = mine - __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, mine), 0x128, 15, 15,
+                                                                                    true));      // row_ror:8
+        }
+      if (col16 >= 8) continue;
+    }
     const int c = first_col + ct * 16 + col16;
     if (c >= columns) continue;
     if (alone) {

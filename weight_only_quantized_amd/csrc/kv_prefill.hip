@@ -2,7 +2,9 @@
 //
 // Mathematics as in kv_decode.hip: weights are powers of two relative to a column's top that moves
 // only when a weight would pass 2^14, the value scale rides in the exponent, operands are float16
-// (codes and queries exact, weights rounded once to 11 bits), sums float32.
+// (codes and queries exact, weights rounded once to 11 bits, of the size of a float16 output's own rounding;
+// the rest of them in products of its own would cost 8192 tokens 788 us instead of 565, chunks of five
+// prompts 202 instead of 155), sums float32.
 //
 // What bounds it: instruction issue, the matrix cores' and the vector units' together (a weight costs
 // a fused multiply-add, a maximum, an exponential, a sum and a conversion; a code four operations to
