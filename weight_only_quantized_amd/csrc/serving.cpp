@@ -107,16 +107,20 @@ gptq_status check_attention(const gptq_kv_cache* c, const gptq_kv_batch* b, cons
 }
 
 // Whether the keys are split over the card (kv_decode.hip) or each workgroup goes through all that its
-// columns see (kv_prefill.hip).  Splitting takes about 27 + 0.029 U n us for U units of 32 (row, head) columns
-// over n thousand tokens (less for a few units), going through 6 + 21 n while every workgroup has a CU.
-// Us, split / not, 8 kv heads of 128, 32 query heads: 1 sequence of 64 rows (U = 64), 2500 tokens 37 / 61,
-// 16000: 51 / 345; 4 of 64 rows (256), 16000: 145 / 349; 16 of 32 rows (512), 2500: 72 / 70; 32 of 32 rows
-// (1024), 4000: 155 / 144.  Few short units (kv_local) come before both.
+// columns see (kv_prefill.hip).  For U units of 32 (row, head) columns over n thousand tokens splitting takes
+// about 25 + U n / 30 us (U n / 20 when the codes of several sequences do not fit the caches), going through
+// 6 + 20 n while every workgroup has a CU: the first for less than 590 units, fewer for short ones.
+// Us, split / not, 8 kv heads of 128, 32 query heads: 1 sequence of 64 rows (U = 64), 2500 tokens 35 / 56,
+// 16000: 52 / 315; 300 rows (304), 2000: 46 / 47, 3000: 57 / 66; 350 rows (352), 60000: 578 / 1169; 540 rows
+// (544), 60000: 884 / 1173; 560 rows (560), 16000: 283 / 318; 600 rows (600), 30000: 655 / 592, 60000: 1363 /
+// 1173; 2 of 270 rows (544), 9000: 160 / 183; 4 of 64 rows (256), 16000: 139 / 320; 4 of 130 rows (544), 20000:
+// 445 / 402 (taken wrongly); 16 of 32 rows (512), 2500: 71 / 60, 8000: 180 / 173, 16000: 336 / 334; 20 of 32
+// rows (640), 30000: 929 / 824.  Few short units (kv_local) come before both.
 bool few_rows(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
   const int64_t columns = (int64_t)b.max_rows * (a.q_heads / c.kv_heads);
   if (columns <= 16 || kv_local(c, b, a)) return true;
   const int64_t units = (int64_t)b.batch * c.kv_heads * ((columns + 31) / 32), span = kv_span(c, b, a);
-  return units <= 24 || (units <= 700 && units * span <= 700 * (span - 1000));
+  return units <= 24 || (units <= 590 && units * span <= 590 * (span - 500));
 }
 
 bool kv_attention_fits(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_attention& a) {
