@@ -89,8 +89,10 @@ __device__ __forceinline__ SeqWork sequence_work(const KvAttentionCall& a, const
   return w;
 }
 
-// Codes that one unit reads are not kept in the caches (measured on 64 sequences: 50.5 -> 45.0 us);
-// with more than 16 columns other units may read them again.
+// Codes that few units read are not kept in the caches (64 sequences: 50.5 -> 45.0 us; one of 777 tokens 12.9 ->
+// 11.9).  Where a sequence and kv head have more columns, other units read them again (a workgroup a unit, not
+// kept / kept: 2 units of 16 columns, 4 sequences of 777 tokens 13.6 / 13.9 us; 4 units, 1 of 777 13.8 / 12.9; 16
+// units, 1 of 800 15.2 / 13.5).
 template <bool ONCE, typename T>
 __device__ __forceinline__ T load_once(const T* p) {
   if constexpr (ONCE) return __builtin_nontemporal_load(p);
@@ -116,7 +118,7 @@ __device__ __forceinline__ void store_joined(uint16_t* to, f32x4 o, float sum, f
   *(uint2*)to = w;
 }
 
-template <int BF16, int DIM, int CT, bool LOCAL>
+template <int BF16, int DIM, int CT, bool LOCAL, bool ONCE>
 __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     kv_decode_kernel(KvAttentionCall call, DecodePlan plan, int page_shift) {
   constexpr int kWaves = LOCAL ? kLocalWaves : gq::kWaves;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     for (int t = 0; t < 2; ++t) {
       const int8_t* kb = a.c.k_codes + step_base(i, t);
 #pragma unroll
-      for (int j = 0; j < KL; ++j) d.k[t][j] = load_once<CT == 1>((const u32x4*)(kb + k_off + j * 1024));
+      for (int j = 0; j < KL; ++j) d.k[t][j] = load_once<ONCE>((const u32x4*)(kb + k_off + j * 1024));
     }
   };
   constexpr int kPieces = DIM / 16;               // of a key row
@@ -293,11 +295,11 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if constexpr (VW == 2) {
-          const u32x2 w = load_once<CT == 1>((const u32x2*)(vb + v_off + e * DIM));
+          const u32x2 w = load_once<ONCE>((const u32x2*)(vb + v_off + e * DIM));
           d.v[t][e][0] = w[0];
           d.v[t][e][VW - 1] = w[1];
         } else {
-          d.v[t][e][0] = load_once<CT == 1>((const uint32_t*)(vb + v_off + e * DIM));
+          d.v[t][e][0] = load_once<ONCE>((const uint32_t*)(vb + v_off + e * DIM));
         }
       }
     }
@@ -630,9 +632,11 @@ size_t kv_decode_ws_bytes(const gptq_kv_cache& c, const gptq_kv_batch& b, const 
 template <int BF16, int DIM>
 static hipError_t launch_dim(const KvAttentionCall& a, const DecodePlan& p, int page_shift, hipStream_t s) {
   const dim3 grid((uint32_t)kernel_blocks(p)), block(kThreads), joins((uint32_t)join_blocks(p, a.b, a.a));
-  if (p.local) kv_decode_kernel<BF16, DIM, 1, true><<<grid, dim3(64 * kLocalWaves), 0, s>>>(a, p, page_shift);
-  else if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1, false><<<grid, block, 0, s>>>(a, p, page_shift);
-  else kv_decode_kernel<BF16, DIM, 2, false><<<grid, block, 0, s>>>(a, p, page_shift);
+  const dim3 local(64 * kLocalWaves);
+  if (p.local && p.col_groups <= 2) kv_decode_kernel<BF16, DIM, 1, true, true><<<grid, local, 0, s>>>(a, p, page_shift);
+  else if (p.local) kv_decode_kernel<BF16, DIM, 1, true, false><<<grid, local, 0, s>>>(a, p, page_shift);
+  else if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1, false, true><<<grid, block, 0, s>>>(a, p, page_shift);
+  else kv_decode_kernel<BF16, DIM, 2, false, false><<<grid, block, 0, s>>>(a, p, page_shift);
   if (p.split && p.many_parts) kv_join_kernel<BF16, DIM, kThreads><<<joins, block, 0, s>>>(a, p);
   else if (p.split) kv_join_kernel<BF16, DIM, 64><<<joins, block, 0, s>>>(a, p);
   return hipGetLastError();
