@@ -50,13 +50,16 @@ inline bool kv_local(const gptq_kv_cache& c, const gptq_kv_batch& b, const gptq_
   const int64_t units = (int64_t)b.batch * c.kv_heads * ((columns + 15) / 16);
   // A CU alone takes in some 50 GB/s, so short units only; fewer than 64 leave most of the card idle in
   // exchange for the second launch (4.6 us of the device, 2.7 of the host).  Us on the device, local
-  // against split, 8 kv heads of 128: 1 sequence of 256 tokens 7.2 / 9.4, 512: 8.7 / 9.7, 1024: 9.6 / 9.7,
-  // 2048: 16.9 / 10.5; 16 sequences of 1024: 13.3 / 17.6, 2048: 20.3 / 21.9, 4096: 32.7 / 31.1; 64
-  // sequences of 512: 22.5 / 20.2 (two workgroups for each CU take turns).  Heads of 64 leave room for two
-  // workgroups on a CU; 384 of them, 1000 tokens: 13.0 / 15.7, 2000: 23.2 / 22.5.  Several units for a
-  // sequence and kv head, local against what else would run, 4 query heads each: 1 sequence of 16 rows, 777
-  // tokens 12.7 / 17.2; 4 of 8 rows 12.7 / 22.8; 8 of 16 rows, 1500 tokens 21.6 / 31.9; one prompt of 64
-  // 7.1 / 9.2; 400 units, heads of 64, a prompt of 200: 9.8 / 8.8.
+  // against split, 8 kv heads of 128, codes not in the caches: 1 sequence of 128 tokens 6.4 / 9.3, 256: 7.8 /
+  // 9.4, 512: 10.1 / 10.2, 777: 11.9 / 11.8, 1024: 12.3 / 10.8, 2048: 17.2 / 11.4 (in the caches 512: 8.8 / 9.3,
+  // 777: 11.2 / 10.2, 1024: 11.0 / 9.1; a call among others, the host's launches counted, 777: 11.6 to 12.0 /
+  // 11.9, 1000: 11.5 to 12.5 / 11.7); 16 sequences of 512: 11.1 / 15.8, 1024: 13.8 / 19.3, 2048: 21.5 / 23.9,
+  // 4096: 35.2 / 33.2; 64 sequences of 512: 23.3 / 21.2 (two workgroups for each CU take turns).  Heads of 64
+  // leave room for two workgroups on a CU; 384 of them, 700 tokens: 14.7 / 17.3, 1000: 17.5 / 19.8, 2000: 26.5 /
+  // 26.8.  Several units for a sequence and kv head, local against what else would run, 4 query heads each: 1
+  // sequence of 16 rows, 777 tokens 12.7 / 17.2; 4 of 8 rows 12.7 / 22.8; 8 of 16 rows, 1500 tokens 21.6 / 31.9;
+  // one of 64 rows, 1500 tokens 17.2 / 34.0; one prompt of 64 7.1 / 9.2; 400 units, heads of 64, a prompt of 200:
+  // 9.8 / 8.8.
   const int64_t most = units < 64 ? 256 << 10 : units <= 256 ? 512 << 10 : 160 << 10;
   return units <= (columns <= 16 ? 256 * 128 / c.head_dim : 256) && (kv_span(c, b, a) + 46) / 32 * 64 * c.head_dim <= most;
 }
