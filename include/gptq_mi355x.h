@@ -445,8 +445,9 @@ typedef struct {
  * rows' adapters may come in any order (calls of more than 1024 rows are quick when they come in runs).
  *   x [M, K], y and out [M, N], row-major, 16-byte aligned; out may be y, and must not otherwise
  *   overlap anything.  ids int32 [M].
- * Both products accumulate in float32; A_i x[m] is kept to 16 bits or more for the second, and out
- * is rounded once.  A call with the same arguments gives the same bits.
+ * Both products accumulate in float32; scale A_i x[m] is kept for the second as two 16-bit numbers, to
+ * 16 bits of each value (F16: or 2^-49 of its row's largest, if that is more), and out is rounded
+ * once.  A call with the same arguments gives the same bits.
  * workspace: gptq_lora_workspace_size() bytes (0 when one launch does all), 256-byte aligned.
  * M == 0: GPTQ_OK, nothing launched.
  * Errors: GPTQ_E_INVALID_ARG, GPTQ_E_SHAPE (K or N, adapters, M > 2^24), GPTQ_E_UNSUPPORTED (rank),

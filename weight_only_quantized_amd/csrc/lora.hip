@@ -17,7 +17,8 @@
 // parts the second launch adds in order; with many rows over workgroups only, whose waves take
 // different rows and meet in the first-level cache over A_i, and a small launch in between adds the
 // parts once.  low goes into the second product as two 16-bit numbers (value and remainder, float16
-// after a power-of-two scaling of the row): 16 bits or more for one more product.
+// after a power-of-two scaling of the row, its remainder times 2^11): 16 bits or more of each value that is
+// 2^-33 of its row's largest or more, for one more product.
 //
 // Measured (the device's time): 1 row, rank 16, 4096 x 14336, one launch: 7.8 us, most of it two trips to
 // memory and the pass over A_i.  61 rows of 48 adapters, rank 32, 8192 x 28672 (86 MB): 7.0 + 15.9 us, 4.3
@@ -332,7 +333,10 @@ __device__ __forceinline__ int row_exponent(float most) {
   const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127 - 13;
   return e < -120 ? -120 : e > 114 ? 114 : e;
 }
-// low * down as value and remainder (0 beside an infinity)
+// low * down as value and remainder (0 beside an infinity).  float16's remainder is held times 2^11: a value
+// far below its row's largest is subnormal there, and what it lacks would be too small to hold.
+template <int BF16>
+constexpr float kRestUp = BF16 ? 1.0f : 0x1p11f;
 template <int BF16>
 __device__ __forceinline__ void split8(const float* low, float down, u32x4* high, u32x4* rest) {
 #pragma unroll
@@ -340,7 +344,7 @@ __device__ __forceinline__ void split8(const float* low, float down, u32x4* high
     const float v0 = low[2 * e] * down, v1 = low[2 * e + 1] * down;
     const uint16_t h0 = from_f32<BF16>(v0), h1 = from_f32<BF16>(v1);
     (*high)[e] = (uint32_t)h0 | (uint32_t)h1 << 16;
-    const float r0 = v0 - to_f32<BF16>(h0), r1 = v1 - to_f32<BF16>(h1);
+    const float r0 = (v0 - to_f32<BF16>(h0)) * kRestUp<BF16>, r1 = (v1 - to_f32<BF16>(h1)) * kRestUp<BF16>;
     constexpr uint32_t kInf = BF16 ? 0x7f80 : 0x7c00;
     (*rest)[e] = ((h0 & 0x7fffu) == kInf ? 0u : (uint32_t)from_f32<BF16>(r0)) |
                  ((h1 & 0x7fffu) == kInf ? 0u : (uint32_t)from_f32<BF16>(r1)) << 16;
@@ -524,13 +528,17 @@ __global__ void __launch_bounds__(kThreads, KS == 4 ? 1 : 2) lora_up_kernel(Lora
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 1; part >= 0; --part) {            // the remainders first
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             const u32x4 low = lows[part][(m * 16 + col) * kPitch + k * 4 + quad];
 #pragma unroll
             for (int t = 0; t < 4; ++t) acc[t] = mfma16<BF16>(w[t][k], low, acc[t]);
           }
+          if (!BF16 && part == 1)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t] *= 1.0f / kRestUp<BF16>;
+        }
         const float back = BF16 ? 1.0f : scaled[m * 16 + col];
 #pragma unroll
         for (int t = 0; t < 4; ++t) *(f32x4*)(tile + col * kTilePitch + t * 16 + quad * 4) = BF16 ? acc[t] : acc[t] * back;
