@@ -128,3 +128,15 @@ def test_a_page_that_fills_token_by_token():
     assert growths.max() > 3
     for got in (k, v):
         assert np.all(np.abs(host(got) - host(x)) <= bound), float((np.abs(host(got) - host(x)) / bound).max())
+
+
+def test_bounds_past_32_bits():
+    """max_kv and window are upper bounds: any that is large enough is as good as none."""
+    import torch
+    say("large bounds")
+    pool = Pool([300, 40], 16, 2, 64, seed=6)
+    q, cu = dev(np.random.default_rng(4).normal(0, 1, (6, 4, 64)), torch.float16), dev(offsets([5, 1]))
+    lens = dev(np.asarray([300, 40], np.int32))
+    want = pool.cache().attention(q, dev(pool.table), lens, cu, max_q=5)
+    for kw in (dict(max_kv=1 << 31), dict(max_kv=1 << 40), dict(window=1 << 31), dict(window=1 << 40, max_kv=1 << 33)):
+        assert torch.equal(pool.cache().attention(q, dev(pool.table), lens, cu, max_q=5, **kw), want), kw

@@ -268,8 +268,11 @@ class KVCache:
             if not out_stride:
                 raise ValueError("out must have dense heads and aligned rows")
         batch = self._batch(page_table, kv_len, cu, rows, max_q)
-        if max_kv is None:
-            max_kv = page_table.shape[1] * self.page_size
+        room = page_table.shape[1] * self.page_size
+        if max_kv is None or max_kv > room:
+            max_kv = room
+        if window > 0x7fffffff:                 # past every position: hides nothing
+            window = 0
         call = _ATTENTION.pack(heads, code, dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, max_kv,
                                q_stride, out_stride)
         key = (rows, page_table.shape, max_q, heads, max_kv, causal, window)
