@@ -415,10 +415,11 @@ typedef struct {
  * 2^-99 (2^-39) of a larger one's.
  * A query that sees no token (a negative position, absent pages) gives zeros.  Scores, the running
  * maximum and sum and the output are held in float32.  Matrix operands are float16: codes exactly, q
- * scaled by a power of two of its row, and probabilities relative to the row's largest contribution,
- * kept to 21 bits where max_rows * q_heads / kv_heads is at most 8 and rounded to 11 bits beyond
- * (2^-12 of a token's contribution, of the size of float16's own rounding).  out is rounded once.  A
- * call with the same arguments gives the same bits.
+ * exactly (BF16: scaled by a power of two of its row, values below 2^-28 of its largest lose bits),
+ * and probabilities relative to the row's largest contribution, kept to 21 bits where max_rows *
+ * q_heads / kv_heads is at most 8 and rounded to 11 bits beyond (2^-12 of a token's contribution, of
+ * the size of float16's own rounding).  out is rounded once.  A call with the same arguments gives
+ * the same bits.
  * workspace: gptq_kv_attention_workspace_size() bytes (0 when the keys are not split), 256-byte
  * aligned.  max_rows == 0, like no rows: GPTQ_OK, nothing launched.
  * Errors: as for gptq_kv_append, and GPTQ_E_WORKSPACE. */

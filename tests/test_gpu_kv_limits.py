@@ -73,7 +73,6 @@ BOUNDS = {
     "more_rows_than_tokens": ([1, 2], [0, 2, 4], 4, [0, (0, 1), (1, 1), (1, 2)]),
     "rows_that_descend": ([64, 64], [0, -9, 4], 4, [None, None, None, None]),
     "rows_past_the_last": ([64, 64], [9, 12, 15], 4, [None, None, None, None]),
-    "second_past_the_last": ([64, 64], [0, 2, 9], 4, [(0, 63), (0, 64), None, None]),
 }
 
 
