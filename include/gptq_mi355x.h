@@ -417,7 +417,7 @@ typedef struct {
  * maximum and sum and the output are held in float32.  Matrix operands are float16: codes exactly, q
  * exactly (BF16: scaled by a power of two of its row, values below 2^-28 of its largest lose bits),
  * and probabilities relative to the row's largest contribution, kept to 21 bits where max_rows *
- * q_heads / kv_heads is at most 8 and rounded to 11 bits beyond (2^-12 of a token's contribution, of
+ * q_heads / kv_heads is at most 16 and rounded to 11 bits beyond (2^-12 of a token's contribution, of
  * the size of float16's own rounding).  out is rounded once.  A call with the same arguments gives
  * the same bits.
  * workspace: gptq_kv_attention_workspace_size() bytes (0 when the keys are not split), 256-byte

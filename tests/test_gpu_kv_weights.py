@@ -1,4 +1,4 @@
-"""Attention's probabilities in the second product: calls of up to eight (row, head) columns a sequence and kv
+"""Attention's probabilities in the second product: calls of up to sixteen (row, head) columns a sequence and kv
 head keep them to 21 bits and more.
 
 Bound, beside out's own rounding (half a unit of its type, half of float16's smallest step): the first 11 bits
@@ -37,6 +37,12 @@ FORMS = {
     "batch": ([40 + i for i in range(70)], [1] * 70, 4, 4, 128, 0),
     "batch_split": ([90 * i + 1 for i in range(40)], [1] * 40, 3, 15, 64, 0),
     "eight_heads": ([333, 2000], [1, 1], 2, 16, 128, 0),
+    "sixteen_heads": ([777, 40], [1, 1], 2, 32, 128, 0),
+    "nine": ([600, 130], [3, 2], 2, 6, 64, 0),
+    "drafts_of_four": ([5000, 4100], [3, 4], 1, 4, 64, 0),
+    "long_sixteen": ([7000, 300], [1, 1], 1, 16, 128, 0),
+    "batch_of_twelve": ([40 + i for i in range(70)], [1] * 70, 2, 24, 64, 0),
+    "batch_of_sixteen": ([900 - 9 * i for i in range(70)], [4] * 70, 1, 4, 128, 200),
 }
 
 

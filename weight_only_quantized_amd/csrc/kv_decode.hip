@@ -16,9 +16,10 @@
 // eight columns use half of a matrix instruction's sixteen: there each column stands twice, once with its
 // weights' first 11 bits and once with the rest of them, and the two sums are joined at the end: 21 bits,
 // down to 2^-31 of the largest weight, for one fused multiply-add a weight (us, 11 bits / 21: one token 11.25 /
-// 11.5, 64 sequences 48.4 / 48.8).  Wider units keep 11 bits down to 2^-20 of the largest weight, an error of
-// the size of a float16 output's own rounding; there the rest would take matrix instructions of its own (500
-// rows over 9000 tokens: 147 -> 170 us).
+// 11.5, 64 sequences 48.4 / 48.8).  Units of up to sixteen take a second instruction for the rest (one token
+// with 16 heads a kv head 12.05 / 12.25, 64 sequences of 3 drafts 95.0 / 95.2).  Wider units keep 11 bits down
+// to 2^-20 of the largest weight, an error of the size of a float16 output's own rounding: they are bound by
+// instructions (500 rows over 9000 tokens would take 170 us instead of 147).
 //
 // Split.  The work is cut into steps of 32 tokens of a unit: up to 32 (row, head) columns of one
 // sequence and kv head.  All units' steps in order are dealt to as many waves as the card holds at
@@ -118,8 +119,11 @@ __device__ __forceinline__ void store_joined(uint16_t* to, f32x4 o, float sum, f
   *(uint2*)to = w;
 }
 
-template <int BF16, int DIM, int CT, bool LOCAL, bool ONCE>
-__global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
+// A weight's bits in the second product: the first 11, rounded; those and the rest of them in the other eight
+// columns of one matrix instruction; or in a second one.
+enum { kFirstBits, kInPairs, kTwice };
+template <int BF16, int DIM, int CT, bool LOCAL, bool ONCE, int BITS>
+__global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, LOCAL && DIM == 64 ? 4 : 2)
     kv_decode_kernel(KvAttentionCall call, DecodePlan plan, int page_shift) {
   constexpr int kWaves = LOCAL ? kLocalWaves : gq::kWaves;
   constexpr int KL = DIM / 64;      // 16-byte loads of a lane for a tile's keys
@@ -136,10 +140,9 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   const int col16 = lane & 15, quad = lane >> 4;
   const int room = key_room(call.b, call.a, page_shift);
   const int group = call.a.q_heads / call.c.kv_heads;
-  // up to eight columns: each stands twice, with its weights' first 11 bits and with the rest of them
-  const bool paired = CT == 1 && plan.width <= 8;
-  const uint32_t first_bits = paired ? 0xffffe000u : 0xffffffffu;
-  const float less = paired && col16 >= 8 ? -1.0f : 0.0f;
+  constexpr bool kPaired = BITS == kInPairs;
+  static_assert(BITS == kFirstBits || CT == 1, "");
+  const float less = col16 >= 8 ? -1.0f : 0.0f;    // columns from 8 on: what is left of a weight, negative
 
   // this wave's share of all steps (LOCAL: of its unit's), and the sequence where they
   // start: a scan over 64 sequences at a time, one a lane
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
   int page = page_id(run0);                       // on its way with the query
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
-    int c = first_col + ct * 16 + (paired ? col16 & 7 : col16);
+    int c = first_col + ct * 16 + (kPaired ? col16 & 7 : col16);
     c = c < columns ? c : columns - 1;
     const int row = c / group, head = kv_head * group + c % group;
     const KeyRange r = key_range(s, row, a.a, room);
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
           for (int e = 0; e < 4; ++e) x[ct][t][e] -= to;
       }
     }
-    f16x8 w[CT];
+    f16x8 w[CT], rest;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
 #pragma unroll
@@ -384,12 +387,9 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
         for (int e = 0; e < 4; ++e) {
           const float p = __builtin_amdgcn_exp2f(x[ct][t][e]);
           total[ct] = __builtin_fmaf(p, rv, total[ct]);
-          if constexpr (CT == 1) {                // the first bits, or what is left of them, negative
-            const float first = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, p) & first_bits);
-            w[ct][t * 4 + e] = (_Float16)__builtin_fmaf(p, less, first);
-          } else {
-            w[ct][t * 4 + e] = (_Float16)p;
-          }
+          const float first = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, p) & 0xffffe000u);
+          w[ct][t * 4 + e] = (_Float16)(BITS == kFirstBits ? p : kPaired ? __builtin_fmaf(p, less, first) : first);
+          if constexpr (BITS == kTwice) rest[t * 4 + e] = (_Float16)(p - first);
         }
       }
     }
@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
         acc[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), w[ct], acc[ct][t], 0, 0, 0);
+      if constexpr (BITS == kTwice) acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), rest, acc[0][t], 0, 0, 0);
     }
     if constexpr (decltype(more)::value) load_values(d, i + 2);
   };
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(LOCAL ? 64 * kLocalWaves : kThreads, 2)
     float sum = total[ct];
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    if (paired) {                                 // less the sums of what was left, in the lane eight on
+    if constexpr (kPaired) {                                 // less the sums of what was left, in the lane eight on
 #pragma unroll
       for (int t = 0; t < VB; ++t)
 #pragma unroll
@@ -633,10 +634,20 @@ template <int BF16, int DIM>
 static hipError_t launch_dim(const KvAttentionCall& a, const DecodePlan& p, int page_shift, hipStream_t s) {
   const dim3 grid((uint32_t)kernel_blocks(p)), block(kThreads), joins((uint32_t)join_blocks(p, a.b, a.a));
   const dim3 local(64 * kLocalWaves);
-  if (p.local && p.col_groups <= 2) kv_decode_kernel<BF16, DIM, 1, true, true><<<grid, local, 0, s>>>(a, p, page_shift);
-  else if (p.local) kv_decode_kernel<BF16, DIM, 1, true, false><<<grid, local, 0, s>>>(a, p, page_shift);
-  else if (p.col_tiles == 1) kv_decode_kernel<BF16, DIM, 1, false, true><<<grid, block, 0, s>>>(a, p, page_shift);
-  else kv_decode_kernel<BF16, DIM, 2, false, false><<<grid, block, 0, s>>>(a, p, page_shift);
+#define GQ_DECODE(CT, LOCAL, ONCE, BITS) \
+  kv_decode_kernel<BF16, DIM, CT, LOCAL, ONCE, BITS><<<grid, LOCAL ? local : block, 0, s>>>(a, p, page_shift)
+  if (p.local) {
+    if (p.width <= 8) GQ_DECODE(1, true, true, kInPairs);
+    else if (p.col_groups == 1) GQ_DECODE(1, true, true, kTwice);
+    else if (p.col_groups == 2) GQ_DECODE(1, true, true, kFirstBits);
+    else GQ_DECODE(1, true, false, kFirstBits);
+  } else if (p.col_tiles == 1) {
+    if (p.width <= 8) GQ_DECODE(1, false, true, kInPairs);
+    else GQ_DECODE(1, false, true, kTwice);
+  } else {
+    GQ_DECODE(2, false, false, kFirstBits);
+  }
+#undef GQ_DECODE
   if (p.split && p.many_parts) kv_join_kernel<BF16, DIM, kThreads><<<joins, block, 0, s>>>(a, p);
   else if (p.split) kv_join_kernel<BF16, DIM, 64><<<joins, block, 0, s>>>(a, p);
   return hipGetLastError();
