@@ -14,7 +14,7 @@
 //
 // What bounds it: bytes (new rows in, rotated queries in and out, touched pages' codes out, their older
 // codes in too); a token a request: the launch.  Measured (the device's time): 64 requests, one token each,
-// 32 + 8 heads of 128: 5.0 us; 5011 tokens of 7 prompts, 64 + 8 heads, 96 MB: 22.5 us, 4.3 TB/s of the 4.9
+// 32 + 8 heads of 128: 5.0 us; 5011 tokens of 7 prompts, 64 + 8 heads, 96 MB: 22.1 us, 4.3 TB/s of the 4.9
 // that a large copy reaches; reading 5 MB of codes back as 10 MB of float16: 5.5 us.
 #include <hip/hip_runtime.h>
 

@@ -32,11 +32,12 @@
 // operand: values go from memory to the matrix cores without LDS.
 //
 // Measured (the device's time, both launches): 64 sequences of up to 4096 tokens, 8 kv heads of 128, 221
-// MB: 43.5 + 4.7 us, 5.1 TB/s in the first launch; waves start their loads after 2 to 5 us and stream
+// MB: 44.5 + 5.0 us, 5.0 TB/s in the first launch; waves start their loads after 2 to 5 us and stream
 // at 6.8 TB/s (a plain read of as many bytes: 6.85) until the first ends, 7 us before the last.  6
-// sequences of up to 70001, 64 query heads, 325 MB: 59.5 + 6.0 us, 5.5 TB/s.  24 sequences, 5 rows each,
-// a window of 2000, 16 heads of 64, 60 MB: 18.5 + 4.0 us.  1 sequence of 777 tokens, one launch: 11 us,
-// latency.
+// sequences of up to 70001, 64 query heads, 325 MB: 59.6 + 6.3 us, 5.5 TB/s.  24 sequences, 5 rows each,
+// a window of 2000, 16 heads of 64, 60 MB: 19.0 + 4.1 us, no unit at its limit.  1 sequence of 777 tokens, one
+// launch: 11.4 us, of which a wave waits 47 % for results and 18 % for its turn to issue.  500 rows over 9000
+// tokens: 141 + 10.6 us, vector units 61 % (each unit converts all codes).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
