@@ -410,9 +410,9 @@ typedef struct {
  * the cache, the queries' own included: its row i stands at position at[b] - n + i of n rows.
  *   q, out  [rows, q_heads, head_dim] of the call's dtype, 16-byte aligned; out must not overlap q
  *           or the workspace.
- * Value scales hold over float32's range where those of a sequence and head lie within 2^99 of the first one
- * that its rows see and that is not zero, or within 2^-39 .. 2^39; values of a smaller scale count as up to
- * 2^-99 (2^-39) of a larger one's.
+ * Value scales hold over float32's range where those of a sequence and head lie within 2^99 of each
+ * other (zeros aside; after 1024 tokens of zeros up to 2^39), or within 2^-39 .. 2^39; values of a smaller
+ * scale count as up to 2^-99 (2^-39) of a larger one's.
  * A query that sees no token (a negative position, absent pages) gives zeros.  Scores, the running
  * maximum and sum and the output are held in float32.  Matrix operands are float16: codes exactly, q
  * exactly (BF16: scaled by a power of two of its row, values below 2^-28 of its largest lose bits),

@@ -112,3 +112,24 @@ def test_append_of_values_near_the_smallest(size, had, n):
         assert np.all(np.abs(got_scale - scale) <= scale * 4 * 2.0 ** -23 + 2.0 ** -150)
         off = 0.5 + 127 * (16 * 2.0 ** -24 + 2.0 ** -150 / np.maximum(scale, 2.0 ** -149))[:, :, None, None]
         assert np.all(np.abs(got - ideal) <= off), (name, float(np.abs(got - ideal).max()))
+
+
+@pytest.mark.parametrize("form", [([1500], [1], 1, 4), ([1500, 40], [300, 40], 5, 20), ([1500], [60], 1, 8)],
+                         ids=["token", "prompt", "rows"])
+def test_small_values_after_many_zeros(form):
+    """Over 1024 tokens of pages whose value scale is zero, then values near 1e-33."""
+    import torch
+    lens, ns, hkv, hq = form
+    say("zeros first", form)
+    pool = Pool(lens, 16, hkv, 64, seed=3)
+    pool.v_scale = scales("smaller", pool)
+    pool.v_scale[pool.table[0, :70]] = 0.0
+    cu = offsets(ns)
+    q = dev(np.random.default_rng(6).normal(0, 1.5, (int(cu[-1]), hq, 64)), torch.bfloat16)
+    out = host(pool.cache().attention(q, dev(pool.table), dev(np.asarray(lens, np.int32)), dev(cu), max_q=max(ns)))
+    want, weight, most = so.attention(host(q), pool.k_codes, pool.v_codes, pool.k_scale, pool.v_scale, pool.table, lens,
+                                      cu, 64 ** -0.5)
+    bound = HALF["bf16"] * np.abs(want) + (2.0 ** -11 + 2.0 ** -15 + 2.0 ** -19 * (1 + most[..., None])) * weight + 2.0 ** -133
+    bound += smallest_steps(host(q), pool, lens, cu, 64 ** -0.5, 0)
+    err = np.abs(out - want)
+    assert np.all(err <= bound), (form, float((err / bound).max()), np.argwhere(err > bound)[:4].tolist())

@@ -83,11 +83,11 @@ __device__ __forceinline__ float lane_f32(float v, int lane) {
 // 2^(t + log v) 2^(ref - log v).  float32 holds such sums for value scales of 2^(ref - 80) (2^80, weights
 // of 2^14 and 2^30 tokens make 2^124) up to 2^(ref + 118).  ref lies 19 below the first value scale that is
 // not zero (of marked tiles, one a lane), so that scales within 2^99 of that one keep their bits, and between
-// -79 and 41, so that those of 2^-39 .. 2^39 always do.
+// -79 and 41, so that those of 2^-39 .. 2^39 always do (all up to 2^39 after zeros alone).
 __device__ __forceinline__ float scale_reference(float v_scale) {
   const uint64_t some = __ballot(v_scale > 0.0f);
   const int bits = __builtin_amdgcn_readlane(__builtin_bit_cast(int, v_scale), some ? __builtin_ctzll(some) : 0);
-  int e = some ? (bits >> 23) - 126 : 0;
+  int e = some ? (bits >> 23) - 126 : -60;
   e = e < -60 ? -60 : e > 60 ? 60 : e;
   return (float)(e - 19);
 }
