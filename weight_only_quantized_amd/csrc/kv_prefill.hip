@@ -16,8 +16,8 @@
 // one, while the products of the next tile's scores run under this tile's exponentials and the
 // products with the values under the next tile's exponents.  One barrier a step.
 //
-// Measured: one prompt of 8192 tokens, 32 query heads of 128 on 8 kv heads: 555 to 575 us, 956 to 990 TFLOP/s of
-// the 1275 that a large float16 product reaches; chunks of five prompts (115 GFLOP): 144 to 152 us.  The matrix
+// Measured: one prompt of 8192 tokens, 32 query heads of 128 on 8 kv heads: 540 to 577 us, 953 to 1018 TFLOP/s of
+// the 1275 that a large float16 product reaches; chunks of five prompts (115 GFLOP): 142 to 155 us.  The matrix
 // cores are busy 47 % of the time, the vector units 57 %, LDS 35 %; waves wait for their turn to issue 28 % and
 // for memory, LDS or the barrier 28 %.  An earlier form (594 us) took 317 us without reads of operands, with
 // them 484 without staging, barrier and the test for hidden tokens, which cost 90, 30 and 38.  A wave with
