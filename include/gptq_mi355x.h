@@ -457,6 +457,72 @@ gptq_status gptq_lora_workspace_size(const gptq_lora_bank* bank, int64_t M, size
 gptq_status gptq_lora_add(const gptq_lora_bank* bank, const void* x, const void* y, const int32_t* ids, int64_t M,
                           void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Microscaled 4-bit floating point -------------------------------------------------------------
+ * Weights, and activations where wanted, in blocks of 32 consecutive inputs of a row: 32 codes of 4 bits
+ * (bit 3 the sign, bits 2..0 one of 0 0.5 1 1.5 2 3 4 6) and one scale byte s,
+ *     value = e2m1(code) * 2^(s - 127);   every value of a block with s = 255 is NaN.
+ * The card multiplies this format as it is (both sides 4 bits: four times the rate of 16-bit products).
+ * Conventions as for the calls above: device pointers, caller-owned buffers, checks before any
+ * device work, work queued on `stream` only, no allocation and no synchronisation. */
+
+/* Rows of the format. */
+typedef struct {
+  uint8_t* codes;       /* [rows, K / 2], contiguous, 16-byte aligned: input 2 i in the low four
+                           bits of byte i, input 2 i + 1 in the high ones                      */
+  uint8_t* scales;      /* [rows, K / 32], rows scale_stride bytes apart, 4-byte aligned.  All
+                           rows * scale_stride bytes are the caller's; those between K / 32 and
+                           the stride may be read, and count for nothing                       */
+  int64_t scale_stride; /* at least K / 32, a multiple of 4, up to 2^20                         */
+  int64_t rows;         /* 0 .. 2^24                                                           */
+  int32_t K;            /* a multiple of 32 up to 2^20                                         */
+  int32_t reserved;     /* must be 0                                                           */
+} gptq_mx_tensor;
+
+/* x [out->rows, K] (dtype F16, BF16 or F32, rows x_stride elements apart, x_stride * size of an element a
+ * multiple of 16, 16-byte aligned) -> codes and scales.  For each block, with a = max |x|:
+ *   e = floor(log2 a) - 2 within [-127, 127] (-127 when a is 0), s = e + 127;
+ *   a code is the nearest value to x * 2^-e, ties to the even code, past 6 to 6, with x's sign (a value
+ *   that rounds to zero keeps it too).
+ * A block that holds an infinity or a NaN gets s = 255 and codes 0.  Padding bytes of the scales are left alone.
+ * Errors: GPTQ_E_INVALID_ARG (NULL, alignment, strides, dtype, reserved, overlap), GPTQ_E_SHAPE (rows, K),
+ * GPTQ_E_DEVICE, GPTQ_E_HIP.  rows == 0: GPTQ_OK, nothing launched. */
+gptq_status gptq_mx_quantize(const void* x, int64_t x_stride, int32_t dtype, const gptq_mx_tensor* out, void* stream);
+
+/* The values of x as [rows, K] of dtype F16, BF16 or F32, contiguous, 16-byte aligned: each rounded once to
+ * nearest even (BF16 and F32 hold every finite one up to 2^128; what is past a type's range becomes
+ * infinite).  Errors as for gptq_mx_quantize. */
+gptq_status gptq_mx_dequantize(const gptq_mx_tensor* x, void* out, int32_t dtype, void* stream);
+
+typedef enum { GPTQ_MX_PLAIN = 0, GPTQ_MX_SILU = 1, GPTQ_MX_GELU_TANH = 2 } gptq_mx_activation;
+
+/* Weights laid out for the products, once when they are loaded: W [N, K], or the two projections of a gated
+ * feed-forward block, [N, K] each, when `up` is given.  `packed` (gptq_mx_weight_bytes() bytes, 256-byte
+ * aligned) holds all that a call reads; the source may be freed after the stream has passed.
+ * N: 1 .. 2^20.  Errors as above; GPTQ_E_INVALID_ARG when the two differ in shape. */
+gptq_status gptq_mx_weight_bytes(int32_t N, int32_t K, int32_t gated, size_t* bytes);
+gptq_status gptq_mx_pack(const gptq_mx_tensor* weight, const gptq_mx_tensor* up, void* packed, void* stream);
+
+typedef struct {
+  const void* packed;   /* from gptq_mx_pack                                                   */
+  int32_t N, K;         /* as packed                                                           */
+  int32_t activation;   /* gptq_mx_activation: PLAIN for one projection, else of a gated pair  */
+  int32_t reserved;     /* must be 0                                                           */
+} gptq_mx_weight;
+
+/* y[M, N] = x W^T (PLAIN), or act(x Wg^T) * (x Wu^T) in one kernel (SILU: g / (1 + exp(-g)); GELU_TANH:
+ * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))), in float32 throughout, rounded once to y's dtype.
+ * gptq_mx_gemm: x [M, K] in F16 or BF16 as it is, rows x_stride elements apart (a multiple of 8, up to 2^21),
+ *   y of the same dtype.  BF16: every weight is exact.  F16: exact where its block's scale is at least 2^-36
+ *   times the largest of its output's, otherwise rounded to 2^-37 times that.
+ * gptq_mx_gemm_mx: x in the format, y F16 or BF16 (y_dtype).
+ * y is contiguous, 16-byte aligned, and must not overlap x or the weights.  NaN blocks make the outputs that
+ * they take part in NaN.  A call with the same arguments gives the same bits.
+ * Errors: GPTQ_E_INVALID_ARG, GPTQ_E_SHAPE (sizes out of range, or a launch of 2^32 threads or more),
+ * GPTQ_E_DEVICE, GPTQ_E_HIP.  M == 0: GPTQ_OK, nothing launched. */
+gptq_status gptq_mx_gemm(const gptq_mx_weight* weight, const void* x, int64_t x_stride, int32_t dtype, int64_t M, void* y,
+                         void* stream);
+gptq_status gptq_mx_gemm_mx(const gptq_mx_weight* weight, const gptq_mx_tensor* x, void* y, int32_t y_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,8 @@ There is no CPU or PyTorch fallback.
 
 Next to the projections of a served decoder layer (serving.py): LoraBank (low-rank adapters of many
 requests beside a projection) and KVCache (a paged cache in 8 bits: append with rotation, attention,
-read back).
+read back).  In microscaled 4-bit floating point (mx.py): MXTensor (quantize, dequantize), MXLinear and
+MXGatedLinear (products with such weights, activations in 16 bits or in the same format).
 """
 from __future__ import annotations
 
@@ -18,7 +19,8 @@ import ctypes
 import os
 
 __all__ = ["LIB_PATH", "GPTQError", "Desc", "Handle", "load_library", "repack", "validate", "symbols",
-           "STATUS", "PATH_AUTO", "PATH_SKINNY", "PATH_TILED", "KVCache", "LoraBank"]
+           "STATUS", "PATH_AUTO", "PATH_SKINNY", "PATH_TILED", "KVCache", "LoraBank",
+           "MXTensor", "MXLinear", "MXGatedLinear"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq_mi355x.so")
 
@@ -35,7 +37,9 @@ symbols = ["gptq_validate", "gptq_repack", "gptq_workspace_size", "gptq_gemm", "
            "gptq_info", "gptq_decode_runtime", "gptq_status_str", "gptq_last_hip_error", "gptq_hessian",
            "gptq_quantize_workspace_size", "gptq_quantize", "gptq_pack", "gptq_read_floor",
            "gptq_kv_append", "gptq_kv_read", "gptq_kv_attention_workspace_size", "gptq_kv_attention",
-           "gptq_lora_workspace_size", "gptq_lora_add"]
+           "gptq_lora_workspace_size", "gptq_lora_add",
+           "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_weight_bytes", "gptq_mx_pack", "gptq_mx_gemm",
+           "gptq_mx_gemm_mx"]
 
 
 class GPTQError(RuntimeError):
@@ -109,12 +113,20 @@ def load_library(path: str = LIB_PATH):
     lib.gptq_kv_attention.argtypes = [P, P, P, P, P, P, SZ, P]
     lib.gptq_lora_workspace_size.argtypes = [P, I64, ctypes.POINTER(SZ)]
     lib.gptq_lora_add.argtypes = [P, P, P, P, I64, P, P, SZ, P]
+    lib.gptq_mx_quantize.argtypes = [P, I64, I32, P, P]
+    lib.gptq_mx_dequantize.argtypes = [P, P, I32, P]
+    lib.gptq_mx_weight_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(SZ)]
+    lib.gptq_mx_pack.argtypes = [P, P, P, P]
+    lib.gptq_mx_gemm.argtypes = [P, P, I64, I32, I64, P, P]
+    lib.gptq_mx_gemm_mx.argtypes = [P, P, P, I32, P]
     for f in ("gptq_validate", "gptq_repack", "gptq_workspace_size", "gptq_gemm", "gptq_gemm_bias", "gptq_gemm_noalloc",
               "gptq_destroy",
               "gptq_info", "gptq_decode_runtime", "gptq_last_hip_error", "gptq_hessian",
               "gptq_quantize_workspace_size", "gptq_quantize", "gptq_pack", "gptq_read_floor",
               "gptq_kv_append", "gptq_kv_read", "gptq_kv_attention_workspace_size", "gptq_kv_attention",
-              "gptq_lora_workspace_size", "gptq_lora_add"):
+              "gptq_lora_workspace_size", "gptq_lora_add",
+              "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_weight_bytes", "gptq_mx_pack", "gptq_mx_gemm",
+              "gptq_mx_gemm_mx"):
         getattr(lib, f).restype = I32
     _lib = lib
     return lib
@@ -398,4 +410,7 @@ def __getattr__(name):
     if name in ("KVCache", "LoraBank"):
         from . import serving
         return getattr(serving, name)
+    if name in ("MXTensor", "MXLinear", "MXGatedLinear"):
+        from . import mx
+        return getattr(mx, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
