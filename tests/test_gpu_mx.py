@@ -209,3 +209,48 @@ def test_product_any_values(tag, M, N, K):
         assert np.all(np.abs(got - want) <= HALF_STEP[tag] * np.abs(want) + K * 2.0 ** -23 * most + SMALLEST[tag])
         # the sums' own error is far below the results' rounding, taken over all of them
         assert np.linalg.norm(got - want) <= (HALF_STEP[tag] * 1.01) * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("M", [1, 30, 64, 70, 200, 700])
+@pytest.mark.parametrize("K", [32, 96, 160, 288, 416, 1056])
+def test_product_reads_nothing_beside(M, K):
+    """Rows whose neighbours in memory are NaN: inputs past K, bytes past a row's scales, rows past the last."""
+    import torch
+    import weight_only_quantized_amd as wq
+    from weight_only_quantized_amd.mx import _scales_fit
+    rng = np.random.default_rng(M + K)
+    w = _exact_pair(rng, 200, K)
+    layer, wv = wq.MXLinear(_mx(*w)), mo.values(*w)
+    x = _x16(rng, M, K, "bf16")
+    wide = torch.full((M + 300, K + 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:M, :K] = _dev(x, "bf16")
+    assert np.array_equal(_f64(layer.gemm(wide[:M, :K])), _rounded(mo.gemm(x, wv), "bf16"))
+    c, s = _exact_pair(rng, M, K)
+    codes = torch.full((M + 300, K // 2), 255, dtype=torch.uint8, device="cuda")
+    scales = torch.full((M + 300, K // 32 // 4 * 4 + 8), 255, dtype=torch.uint8, device="cuda")
+    codes[:M], scales[:M, :K // 32] = _dev(c), _dev(s)
+    assert _scales_fit(scales[:M, :K // 32])
+    t = wq.MXTensor(codes[:M], scales[:M, :K // 32])
+    assert t.scales.data_ptr() == scales.data_ptr()
+    assert np.array_equal(_f64(layer.gemm(t)), _rounded(mo.gemm(mo.values(c, s), wv), "bf16"))
+
+
+@pytest.mark.parametrize("x_kind", ["16", "mx"])
+@pytest.mark.parametrize("M,N,K", [(4400, 4104, 96), (4097, 4360, 1056), (2049, 8200, 1312), (5000, 4096, 2048)])
+def test_product_of_many_tiles(x_kind, M, N, K):
+    """More tiles than the card has compute units: a workgroup takes several, one after the other."""
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M + N + K)
+    w = _exact_pair(rng, N, K)
+    wv = mo.values(*w)
+    if x_kind == "16":
+        x = _x16(rng, M, K, "f16")
+        given, xv = _dev(x, "f16"), x
+    else:
+        xq = _exact_pair(rng, M, K)
+        given, xv = _mx(*xq), mo.values(*xq)
+    import torch
+    got = wq.MXLinear(_mx(*w)).gemm(given, dtype=torch.float16)
+    # float32 holds these sums exactly in any order, as it does in the product
+    want = torch.from_numpy(xv.astype(np.float32)).cuda() @ torch.from_numpy(wv.astype(np.float32)).cuda().t()
+    assert torch.equal(got, want.half())

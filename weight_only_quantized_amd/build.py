@@ -15,7 +15,7 @@ SOURCES = ["api.cpp", "repack.hip", "skinny.hip", "skinny_b2.hip", "skinny_b3.hi
            "skinny_b5.hip", "skinny_b6.hip", "skinny_b7.hip", "skinny_b8.hip", "mid.hip", "mid_b2.hip", "mid_b3.hip",
            "mid_b4.hip", "mid_b5.hip", "mid_b6.hip", "mid_b7.hip", "mid_b8.hip", "tiled.hip", "quantize.hip",
            "read_floor.hip", "serving.cpp", "kv_append.hip", "kv_decode.hip", "kv_prefill.hip", "lora.hip",
-           "mx.cpp", "mx_quantize.hip", "mx_skinny.hip"]
+           "mx.cpp", "mx_quantize.hip", "mx_skinny.hip", "mx_tiled.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 

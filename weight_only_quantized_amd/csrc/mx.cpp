@@ -60,10 +60,11 @@ gptq_status run_gemm(const gptq_mx_weight* w, MxGemmCall& c, void* stream) {
   c.K = w->K;
   c.act = w->activation;
   if (overlaps(c.y, (size_t)c.M * c.N * 2, c.packed, c.lay.bytes)) return GPTQ_E_INVALID_ARG;
-  if (!mx_gemm_fits(c)) return GPTQ_E_SHAPE;
+  const bool few = c.M <= kMxSkinnyRows;
+  if (few ? !mx_skinny_fits(c) : !mx_tiled_fits(c)) return GPTQ_E_SHAPE;
   const gptq_status st = check_device();
   if (st != GPTQ_OK) return st;
-  const hipError_t e = launch_mx_skinny(c, (hipStream_t)stream);
+  const hipError_t e = few ? launch_mx_skinny(c, (hipStream_t)stream) : launch_mx_tiled(c, (hipStream_t)stream);
   return e == hipSuccess ? GPTQ_OK : hip_fail(e);
 }
 

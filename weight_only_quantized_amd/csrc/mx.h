@@ -8,7 +8,9 @@
 // matrix instruction's operand is read 16 bytes a lane in runs of 256 bytes, whatever its shape:
 // 16 x 16 x 128 takes four blocks of a tile, 32 x 32 x 64 two blocks of two tiles.  Its scales are 32
 // words, [block & 1][row]: byte j of a word belongs to block 2 j + (block & 1), so the four
-// 32 x 32 x 64 instructions of a stage name bytes 0..3 of one register.
+// 32 x 32 x 64 instructions of a stage name bytes 0..3 of one register.  All tiles' first stages
+// come first: neighbouring tiles, which are multiplied at the same time, then lie side by side over all
+// channels of the caches (tile after tile, with strides of a power of two, reads took 1.5 times as long).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -56,7 +58,11 @@ struct MxGemmCall {
   uint16_t* y;                            // [M, N]
   int y_bf16;
 };
-bool mx_gemm_fits(const MxGemmCall& c);
+// Calls of up to this many rows stream the weights (mx_skinny.hip), longer ones go by tiles (mx_tiled.hip).
+constexpr int64_t kMxSkinnyRows = 64;
+bool mx_skinny_fits(const MxGemmCall& c);
 hipError_t launch_mx_skinny(const MxGemmCall& c, hipStream_t s);
+bool mx_tiled_fits(const MxGemmCall& c);
+hipError_t launch_mx_tiled(const MxGemmCall& c, hipStream_t s);
 
 }  // namespace gq

@@ -29,15 +29,11 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmCall a, int group
   const int rows = a.M - m0 < MT * 16 ? (int)(a.M - m0) : MT * 16, blocks = a.K / 32;
   const int chunks = 2 * a.lay.stages - ((blocks & 7) == 1 || (blocks & 7) == 2);       // chunk 1 starts at block 2
 
-  const uint32_t w_size = (uint32_t)a.lay.stages * kMxTileBytes, s_size = (uint32_t)a.lay.stages * 128;
-  rsrc_t w_rsrc[SIDES], s_rsrc[SIDES];
   int lift[SIDES] = {};                   // added to a scale byte (float16 activations)
+  if constexpr (X == kMxF16) {
 #pragma unroll
-  for (int i = 0; i < SIDES; ++i) {
-    const size_t tile = (size_t)column * SIDES + i;
-    w_rsrc[i] = make_rsrc(a.packed + tile * w_size, w_size);
-    s_rsrc[i] = make_rsrc(a.packed + a.lay.scales_at + tile * s_size, s_size);
-    if constexpr (X == kMxF16) lift[i] = 127 + kF16Top - a.packed[a.lay.tops_at + tile * 16 + r];
+    for (int i = 0; i < SIDES; ++i)
+      lift[i] = 127 + kF16Top - a.packed[a.lay.tops_at + ((size_t)column * SIDES + i) * 16 + r];
   }
   const rsrc_t x_rsrc = make_rsrc(a.x + m0 * a.x_bytes, (uint32_t)(rows * a.x_bytes));
   const rsrc_t xs_rsrc = X == kMxCodes ? make_rsrc(a.x_scales + m0 * a.x_scale_stride, (uint32_t)(rows * a.x_scale_stride))
@@ -52,10 +48,14 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmCall a, int group
     for (int d = 0; d < DEPTH; ++d) {
       const int q = base + d * waves, stage = q >> 1, block = chunk_block(g, q & 1);
       const bool in = stage * 8 + block < blocks;        // of x's row; packed weights hold whole stages
+      // chunks past the last read as zeros
+      const size_t tile = q < chunks ? (size_t)stage * a.lay.tiles + (size_t)column * SIDES : 0;
+      const rsrc_t w_rsrc = make_rsrc(a.packed + tile * kMxTileBytes, q < chunks ? SIDES * kMxTileBytes : 0);
+      const rsrc_t s_rsrc = make_rsrc(a.packed + a.lay.scales_at + tile * 128, q < chunks ? SIDES * 128 : 0);
 #pragma unroll
       for (int i = 0; i < SIDES; ++i) {
-        w[d][i] = load_b128(w_rsrc[i], q < chunks ? (uint32_t)(block * 256 + r * 16) : kOob, (uint32_t)stage * kMxTileBytes);
-        ws[d][i] = load_b32(s_rsrc[i], q < chunks ? (uint32_t)((g & 1) * 64 + r * 4) : kOob, (uint32_t)stage * 128);
+        w[d][i] = load_b128(w_rsrc, (uint32_t)(block * 256 + r * 16) + i * kMxTileBytes, 0);
+        ws[d][i] = load_b32(s_rsrc, (uint32_t)((g & 1) * 64 + r * 4) + i * 128, 0);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmCall a, int group
 
 template <int X, int MT, int SIDES>
 hipError_t run(const MxGemmCall& c, hipStream_t s) {
-  constexpr int DEPTH = MT * (X == kMxCodes ? 1 : 4) <= 4 ? 4 : 1;
+  constexpr int DEPTH = MT * SIDES * (X == kMxCodes ? 1 : 4) <= 4 ? 4 : MT * (X == kMxCodes ? 1 : 4) <= 4 ? 2 : 1;
   const int groups = c.lay.tiles / SIDES, waves = 8;
   const int64_t row_blocks = (c.M + MT * 16 - 1) / (MT * 16);
   const size_t lds = (size_t)waves * SIDES * MT * 64 * sizeof(f32x4);
@@ -164,7 +164,7 @@ hipError_t run_sides(const MxGemmCall& c, hipStream_t s) {
 
 }  // namespace
 
-bool mx_gemm_fits(const MxGemmCall& c) { return grid_fits((c.M + 15) / 16 * (c.lay.tiles / c.lay.sides), 512); }
+bool mx_skinny_fits(const MxGemmCall& c) { return grid_fits((c.M + 15) / 16 * (c.lay.tiles / c.lay.sides), 512); }
 
 hipError_t launch_mx_skinny(const MxGemmCall& c, hipStream_t s) {
   if (c.x_kind == kMxCodes) return run_sides<kMxCodes>(c, s);
