@@ -8,9 +8,9 @@
 // matrix instruction's operand is read 16 bytes a lane in runs of 256 bytes, whatever its shape:
 // 16 x 16 x 128 takes four blocks of a tile, 32 x 32 x 64 two blocks of two tiles.  Its scales are 32
 // words, [block & 1][row]: byte j of a word belongs to block 2 j + (block & 1), so the four
-// 32 x 32 x 64 instructions of a stage name bytes 0..3 of one register.  All tiles' first stages
-// come first: neighbouring tiles, which are multiplied at the same time, then lie side by side over all
-// channels of the caches (tile after tile, with strides of a power of two, reads took 1.5 times as long).
+// 32 x 32 x 64 instructions of a stage name bytes 0..3 of one register.  A tile's stages follow
+// one another: a wave that streams one reads on in memory (one row, 4096 -> 14336: 7.7 us; 9.1 with all tiles' first
+// stages first, where the kernel by tiles takes the same time).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>

@@ -159,12 +159,14 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(PackSide a, PackSide b, 
   const int tile = blockIdx.x, side = tile % lay.sides, blocks = K / 32;
   const PackSide src = side ? b : a;
   const int64_t n0 = (int64_t)(tile / lay.sides) * 16;
+  uint8_t* codes = out + (size_t)tile * lay.stages * kMxTileBytes;
+  uint32_t* scales = (uint32_t*)(out + lay.scales_at) + (size_t)tile * lay.stages * 32;
   for (int i = threadIdx.x; i < lay.stages * 128; i += kThreads) {
     const int64_t n = n0 + i % 16;
     const int block = i / 16;
     u32x4 v = {0, 0, 0, 0};
     if (n < N && block < blocks) v = *(const u32x4*)(src.codes + n * (K / 2) + (int64_t)block * 16);
-    *(u32x4*)(out + ((size_t)(i / 128) * lay.tiles + tile) * kMxTileBytes + i % 128 * 16) = v;
+    *(u32x4*)(codes + (size_t)i * 16) = v;
   }
   for (int i = threadIdx.x; i < lay.stages * 32; i += kThreads) {
     const int64_t n = n0 + i % 16;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(PackSide a, PackSide b, 
     uint32_t word = 0;
     for (int j = 0; j < 4; ++j)
       if (n < N && block + 2 * j < blocks) word |= (uint32_t)src.scales[n * src.scale_stride + block + 2 * j] << (8 * j);
-    *(uint32_t*)(out + lay.scales_at + ((size_t)(i / 32) * lay.tiles + tile) * 128 + i % 32 * 4) = word;
+    scales[i] = word;
   }
   int top = 0, bad = 0;
   if (n0 + threadIdx.x % 16 < N)

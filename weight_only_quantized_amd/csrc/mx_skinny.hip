@@ -13,87 +13,121 @@
 namespace gq {
 namespace {
 
-// Which block of its stage lane group g (16 lanes) multiplies in chunk c (0 or 1) of it: any order serves
-// as long as both operands agree, and this one takes both bytes from one scale word of each operand.
-__device__ __forceinline__ int chunk_block(int g, int c) { return (g & 1) + 4 * (g >> 1) + 2 * c; }
+constexpr int kSkinnyWaves = 8;
 
-// Inputs in flight: DEPTH chunks a wave.
-template <int X, int MT, int SIDES, int DEPTH>
-__global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmCall a, int groups) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  f32x4* sums = (f32x4*)smem;             // [wave][side][row tile][lane]
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+// Four registers of lane group g (16 lanes) hold words 0..3 of block g; after it register p holds word g of block p.
+__device__ __forceinline__ u32x4 turned(u32x4 v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return u32x4{c[0], c[1], d[0], d[1]};
+}
+
+// MT tiles of 16 rows by CT tiles of 16 packed outputs (a gated pair: two) a wave, DEPTH chunks of it in flight.
+template <int X, int MT, int CT, int SIDES, int DEPTH, int BOUND>
+__global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int groups) {
+  constexpr int waves = kSkinnyWaves;
+  constexpr int kFit = 64 / (waves * SIDES * MT), kOutTiles = CT / SIDES;        // output tiles joined at once, in 64 KB
+  constexpr int kBatch = kFit < 1 ? 1 : kFit < kOutTiles ? kFit : kOutTiles, kBatchTiles = kBatch * SIDES;
+  __shared__ f32x4 sums[waves * kBatchTiles * MT * 64];                          // [wave][output tile][row tile][lane]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int column = blockIdx.x % groups;                // tile of 16 outputs
+  const int tile0 = blockIdx.x % groups * CT, last = a.lay.tiles - 1 - tile0;
   const int64_t m0 = (int64_t)(blockIdx.x / groups) * (MT * 16);
   const int rows = a.M - m0 < MT * 16 ? (int)(a.M - m0) : MT * 16, blocks = a.K / 32;
-  const int chunks = 2 * a.lay.stages - ((blocks & 7) == 1 || (blocks & 7) == 2);       // chunk 1 starts at block 2
+  const int chunks = (blocks + 3) / 4;
 
-  int lift[SIDES] = {};                   // added to a scale byte (float16 activations)
-  if constexpr (X == kMxF16) {
+  const uint32_t w_size = (uint32_t)a.lay.stages * kMxTileBytes, s_size = (uint32_t)a.lay.stages * 128;
+  rsrc_t w_rsrc[CT], s_rsrc[CT];
+  int lift[CT] = {};                      // added to a scale byte (float16 activations)
 #pragma unroll
-    for (int i = 0; i < SIDES; ++i)
-      lift[i] = 127 + kF16Top - a.packed[a.lay.tops_at + ((size_t)column * SIDES + i) * 16 + r];
+  for (int i = 0; i < CT; ++i) {
+    const size_t tile = tile0 + (i < last ? i : last);   // past the last: not stored
+    w_rsrc[i] = make_rsrc(a.packed + tile * w_size, w_size);
+    s_rsrc[i] = make_rsrc(a.packed + a.lay.scales_at + tile * s_size, s_size);
+    if constexpr (X == kMxF16) lift[i] = 127 + kF16Top - a.packed[a.lay.tops_at + tile * 16 + r];
   }
   const rsrc_t x_rsrc = make_rsrc(a.x + m0 * a.x_bytes, (uint32_t)(rows * a.x_bytes));
   const rsrc_t xs_rsrc = X == kMxCodes ? make_rsrc(a.x_scales + m0 * a.x_scale_stride, (uint32_t)(rows * a.x_scale_stride))
                                        : x_rsrc;
-  constexpr int kBlockBytes = X == kMxCodes ? 16 : 64, XL = kBlockBytes / 16;
+  constexpr int XL = X == kMxCodes ? 1 : 4, WS = X == kMxCodes ? 1 : 2;
 
-  f32x4 acc[SIDES][MT] = {};
-  for (int base = wave; base < chunks; base += waves * DEPTH) {
-    u32x4 w[DEPTH][SIDES], x[DEPTH][MT][XL];
-    uint32_t ws[DEPTH][SIDES], xs[DEPTH][MT];
+  // Chunk q is blocks 4 q .. 4 q + 3.  Codes: lane group g multiplies block g of it, whole.  16 bits: product p takes block
+  // p, a quarter of it each group, so that a load of x reads runs of 64 bytes.  A wave takes DEPTH chunks
+  // at once: of many rows neighbouring ones, whose scales it reads together (61 rows in codes, 8192 -> 8192: 17.9 -> 13.0 us),
+  // of up to 16 rows every eighth, so that the waves read side by side (one row, 4096 -> 14336: 8.2 us against 9.6).
+  constexpr bool kNear = MT > 1;
+  constexpr int kStep = kNear ? 1 : waves, kStages = kNear ? (DEPTH + 1) / 2 : DEPTH;
+  f32x4 acc[CT][MT] = {};
+  u32x4 w[DEPTH][CT], x[DEPTH][MT][XL];
+  uint32_t ws[kStages][CT][WS], xs[MT][DEPTH];
+  // (Loads of the next chunks under the products of these take registers that resident waves use better: one row, 4096 ->
+  // 14336, 11.9 us against 8.1.)
+  for (int q0 = kNear ? wave * DEPTH : wave; q0 < chunks; q0 += waves * DEPTH) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      const int q = base + d * waves, stage = q >> 1, block = chunk_block(g, q & 1);
-      const bool in = stage * 8 + block < blocks;        // of x's row; packed weights hold whole stages
-      // chunks past the last read as zeros
-      const size_t tile = q < chunks ? (size_t)stage * a.lay.tiles + (size_t)column * SIDES : 0;
-      const rsrc_t w_rsrc = make_rsrc(a.packed + tile * kMxTileBytes, q < chunks ? SIDES * kMxTileBytes : 0);
-      const rsrc_t s_rsrc = make_rsrc(a.packed + a.lay.scales_at + tile * 128, q < chunks ? SIDES * 128 : 0);
+      const int q = q0 + d * kStep, c = q & 1, stage = kNear ? d / 2 : d;
+      const bool in = q < chunks;         // past the last all reads as zeros
 #pragma unroll
-      for (int i = 0; i < SIDES; ++i) {
-        w[d][i] = load_b128(w_rsrc, (uint32_t)(block * 256 + r * 16) + i * kMxTileBytes, 0);
-        ws[d][i] = load_b32(s_rsrc, (uint32_t)((g & 1) * 64 + r * 4) + i * 128, 0);
+      for (int i = 0; i < CT; ++i) {
+        w[d][i] = load_b128(w_rsrc[i], in ? (uint32_t)(c * 1024 + lane * 16) : kOob, (uint32_t)(q >> 1) * kMxTileBytes);
+        if (!kNear || d % 2 == 0) {
+#pragma unroll
+          for (int h = 0; h < WS; ++h)
+            ws[stage][i][h] = load_b32(s_rsrc[i], in ? (uint32_t)((WS == 1 ? g & 1 : h) * 64 + r * 4) : kOob, (uint32_t)(q >> 1) * 128);
+        }
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int row = m * 16 + r;
-        const bool there = in && row < rows;
-        const uint32_t at = (uint32_t)(row * a.x_bytes) + (uint32_t)(stage * 8 + block) * kBlockBytes;
 #pragma unroll
-        for (int p = 0; p < XL; ++p) x[d][m][p] = load_b128(x_rsrc, there ? at + p * 16 : kOob, 0);
-        if constexpr (X == kMxCodes) {
-          // the word that holds the block's byte; a block past K may share it, and is masked below
-          const uint32_t word = (uint32_t)(row * a.x_scale_stride) + (uint32_t)(stage * 8 + 4 * (g >> 1));
-          xs[d][m] = load_b32(xs_rsrc, there ? word : kOob, 0);
+        for (int p = 0; p < XL; ++p) {
+          const bool there = 4 * q + (X == kMxCodes ? g : p) < blocks && row < rows;
+          const uint32_t piece = X == kMxCodes ? q * 64 + g * 16 : q * 256 + p * 64 + g * 16;
+          x[d][m][p] = load_b128(x_rsrc, there ? (uint32_t)(row * a.x_bytes) + piece : kOob, 0);
+        }
+      }
+    }
+    if constexpr (X == kMxCodes) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int row = m * 16 + r;
+        const uint32_t at = row < rows ? (uint32_t)(row * a.x_scale_stride) + (uint32_t)q0 * 4 : kOob;
+        if constexpr (kNear) {
+          load_words<DEPTH, 0>(xs_rsrc, at, 0, xs[m]);
+        } else {
+#pragma unroll
+          for (int d = 0; d < DEPTH; ++d) xs[m][d] = load_b32(xs_rsrc, at + d * waves * 4, 0);
         }
       }
     }
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      const int c = (base + d * waves) & 1;
+      const int q = q0 + d * kStep, c = q & 1, stage = kNear ? d / 2 : d;
 #pragma unroll
-      for (int i = 0; i < SIDES; ++i) {
-        const uint32_t byte = ws[d][i] >> (16 * (g >> 1) + 8 * c) & 255;
+      for (int i = 0; i < CT; ++i) {
+        // byte j of word h is the scale of the stage's block 2 j + h
         if constexpr (X == kMxCodes) {
+          const uint32_t byte = ws[stage][i][0] >> (16 * c + 8 * (g >> 1)) & 255;
+          const u32x4 u = w[d][i];
+          const i32x8 wa = {(int)u[0], (int)u[1], (int)u[2], (int)u[3], 0, 0, 0, 0};
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const u32x4 u = w[d][i], v = x[d][m][0];
-            const i32x8 wa = {(int)u[0], (int)u[1], (int)u[2], (int)u[3], 0, 0, 0, 0};
+            const u32x4 v = x[d][m][0];
             const i32x8 xb = {(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
-            const uint32_t x_byte = xs[d][m] >> (8 * (g & 1) + 16 * c) & 255;
+            // a byte past the row's blocks may be anything
+            const uint32_t x_byte = 4 * q + g < blocks ? xs[m][d] >> (8 * g) & 255 : 0;
             acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, xb, acc[i][m], kFp4, kFp4, 0, (int)byte, 0,
                                                                          (int)x_byte);
           }
         } else {
-          int s = (int)byte;
-          if constexpr (X == kMxF16) s = s + lift[i] > 0 ? s + lift[i] : 0;
-          const float scale = scale_of(s);
+          const u32x4 u = turned(w[d][i]);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            const u32x4 wa = mx_values<X == kMxBf16>(w[d][i][p], scale);
+            int s = (int)(ws[stage][i][p & 1] >> (16 * c + 8 * (p >> 1)) & 255);
+            if constexpr (X == kMxF16) s = s + lift[i] > 0 ? s + lift[i] : 0;
+            const u32x4 wa = mx_values<X == kMxBf16>(u[p], scale_of(s));
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[i][m] = mfma16<X == kMxBf16>(wa, x[d][m][p], acc[i][m]);
           }
@@ -101,60 +135,82 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmCall a, int group
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < SIDES; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) sums[((wave * SIDES + i) * MT + m) * 64 + lane] = acc[i][m];
-  __syncthreads();
   // lane l of a product holds outputs 4 (l / 16) .. + 3 of row l % 16
-  for (int q = threadIdx.x; q < MT * 64; q += blockDim.x) {
-    const int row = (q >> 6) * 16 + (q & 15), o = 4 * ((q & 63) >> 4);
-    if (row >= rows) continue;
-    f32x4 t[SIDES];
 #pragma unroll
-    for (int i = 0; i < SIDES; ++i) {
-      t[i] = sums[i * MT * 64 + q];
-      for (int k = 1; k < waves; ++k) t[i] += sums[(k * SIDES + i) * MT * 64 + q];
-      if constexpr (X == kMxF16) {
-        const uint32_t tops = *(const uint32_t*)(a.packed + a.lay.tops_at + ((size_t)column * SIDES + i) * 16 + o);
+  for (int first = 0; first < kOutTiles; first += kBatch) {
+    if (first > 0) __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[i][e] *= mx_row_factor(tops >> (8 * e) & 255);
+    for (int i = 0; i < kBatchTiles; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        if (first * SIDES + i < CT) sums[((wave * kBatchTiles + i) * MT + m) * 64 + lane] = acc[first * SIDES + i][m];
+    __syncthreads();
+    for (int q = threadIdx.x; q < kBatch * MT * 64; q += waves * 64) {
+      const int l = q & 63, m = (q >> 6) % MT, out = (q >> 6) / MT;
+      const int row = m * 16 + (l & 15), o = 4 * (l >> 4), tile = tile0 + (first + out) * SIDES;
+      if (row >= rows || tile >= a.lay.tiles || first + out >= kOutTiles) continue;
+      f32x4 t[SIDES];
+#pragma unroll
+      for (int i = 0; i < SIDES; ++i) {
+        const int at = ((out * SIDES + i) * MT + m) * 64 + l;
+        t[i] = sums[at];
+#pragma unroll
+        for (int k = 1; k < waves; ++k) t[i] += sums[k * kBatchTiles * MT * 64 + at];
+        if constexpr (X == kMxF16) {
+          const uint32_t tops = *(const uint32_t*)(a.packed + a.lay.tops_at + (size_t)(tile + i) * 16 + o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[i][e] *= mx_row_factor(tops >> (8 * e) & 255);
+        }
       }
-    }
-    uint16_t v[4];
+      uint16_t v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (SIDES == 2) t[0][e] = mx_gate(t[0][e], t[1][e], a.act);
-      v[e] = mx_round(t[0][e], a.y_bf16);
-    }
-    const int n = column * 16 + o;
-    uint16_t* y = a.y + (m0 + row) * a.N + n;
-    if (a.N % 4 == 0 && n < a.N) {
-      *(uint64_t*)y = (uint64_t)(v[0] | (uint32_t)v[1] << 16) | (uint64_t)(v[2] | (uint32_t)v[3] << 16) << 32;
-    } else {
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (SIDES == 2) t[0][e] = mx_gate(t[0][e], t[1][e], a.act);
+        v[e] = mx_round(t[0][e], a.y_bf16);
+      }
+      const int n = tile / SIDES * 16 + o;
+      uint16_t* y = a.y + (m0 + row) * a.N + n;
+      if (a.N % 4 == 0 && n < a.N) {
+        *(uint64_t*)y = (uint64_t)(v[0] | (uint32_t)v[1] << 16) | (uint64_t)(v[2] | (uint32_t)v[3] << 16) << 32;
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < a.N) y[e] = v[e];
+        for (int e = 0; e < 4; ++e)
+          if (n + e < a.N) y[e] = v[e];
+      }
     }
   }
 }
 
-template <int X, int MT, int SIDES>
+template <int X, int MT, int CT, int SIDES>
 hipError_t run(const MxGemmCall& c, hipStream_t s) {
-  constexpr int DEPTH = MT * SIDES * (X == kMxCodes ? 1 : 4) <= 4 ? 4 : MT * (X == kMxCodes ? 1 : 4) <= 4 ? 2 : 1;
-  const int groups = c.lay.tiles / SIDES, waves = 8;
+  // registers: 4 CT MT of sums, and DEPTH times the operands
+  constexpr int kChunk = X == kMxCodes ? 5 * CT + 5 * MT : 6 * CT + 16 * MT, kFree = 190 - 4 * CT * MT;
+  constexpr int DEPTH = kFree >= 4 * kChunk ? 4 : kFree >= 2 * kChunk ? 2 : 1;
+  constexpr int BOUND = MT == 1 && CT <= 2 ? 1024 : 512;
+  const int groups = (c.lay.tiles + CT - 1) / CT;
   const int64_t row_blocks = (c.M + MT * 16 - 1) / (MT * 16);
-  const size_t lds = (size_t)waves * SIDES * MT * 64 * sizeof(f32x4);
-  mx_skinny_kernel<X, MT, SIDES, DEPTH><<<(unsigned)(groups * row_blocks), waves * 64, lds, s>>>(c, groups);
+  mx_skinny_kernel<X, MT, CT, SIDES, DEPTH, BOUND><<<(unsigned)(groups * row_blocks), kSkinnyWaves * 64, 0, s>>>(c, groups);
   return hipGetLastError();
+}
+
+// More tiles a wave read x less often (every workgroup reads all of it), fewer fill the card: as many as leave 200
+// workgroups.  Us for 1 / 2 / 4: 16 rows in 16 bits, 8192 -> 28672: 62 / 44 / 34; 61 in codes, 8192 -> 8192: 31 / 18 / 26; 48 gated, 4096 ->
+// 14336: - / 49 / 31.  Up to 8 rows x is little, and more workgroups are better: one row, 4096 -> 14336: 8.5 / 8.2 / 9.1; 4 in codes,
+// 8192 -> 8192: 7.7 / 8.0 / 9.0.
+template <int X, int MT, int SIDES>
+hipError_t run_tiles(const MxGemmCall& c, hipStream_t s) {
+  const int tiles = c.lay.tiles;
+  if (c.M > 8 && tiles >= 4 * 200) return run<X, MT, 4, SIDES>(c, s);
+  if (SIDES == 2 || tiles >= 2 * (c.M > 8 ? 200 : 400)) return run<X, MT, 2, SIDES>(c, s);
+  return run<X, MT, SIDES, SIDES>(c, s);
 }
 
 template <int X, int SIDES>
 hipError_t run_rows(const MxGemmCall& c, hipStream_t s) {
-  if (c.M <= 16) return run<X, 1, SIDES>(c, s);
-  if (c.M <= 32) return run<X, 2, SIDES>(c, s);
-  if (c.M <= 48) return run<X, 3, SIDES>(c, s);
-  return run<X, 4, SIDES>(c, s);
+  if (c.M <= 16) return run_tiles<X, 1, SIDES>(c, s);
+  if (c.M <= 32) return run_tiles<X, 2, SIDES>(c, s);
+  if (c.M <= 48) return run_tiles<X, 3, SIDES>(c, s);
+  return run_tiles<X, 4, SIDES>(c, s);
 }
 
 template <int X>

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, half = lane >> 5;
   const int wave_m = wave & 1, wave_n = wave >> 1;
-  const uint32_t x_bytes = (uint32_t)a.x_bytes, xs_bytes = (uint32_t)a.x_scale_stride, y_bytes = (uint32_t)a.N * 2;
+  const uint32_t x_bytes = (uint32_t)a.x_bytes, xs_bytes = (uint32_t)a.x_scale_stride, tile_bytes = (uint32_t)a.lay.stages * kMxTileBytes;
   const int blocks = a.K / 32, real = (a.K + S::kInputs - 1) / S::kInputs;
   // a workgroup of several tiles takes whole groups of four steps (inputs past K count as zeros)
   const int steps = S::kLong ? (real + 3) & ~3 : real;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
   // checked against a resource's size: rows past `rows` and tiles past `tiles` lie behind it, and so do blocks past K.
   struct Source {
     const uint8_t *x, *w;
-    uint32_t x_size, w_size, at[2];
+    uint32_t x_size, w_size, w_base, at[2];
     int wave;                             // as a value that no address is computed from ahead of the loop
   };
   auto source_of = [&](const Place& p, int step) {
@@ -100,8 +100,9 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
     if (S::kLong && stage >= a.lay.stages) stage = a.lay.stages - 1;    // times zeros
     f.x = a.x + (uint64_t)p.m0 * x_bytes;
     f.x_size = (uint32_t)p.rows * x_bytes;
-    f.w = a.packed + ((size_t)stage * a.lay.tiles + p.tile0) * kMxTileBytes;
-    f.w_size = (uint32_t)p.tiles * kMxTileBytes;
+    f.w = a.packed + (size_t)p.tile0 * tile_bytes;
+    f.w_size = (uint32_t)p.tiles * tile_bytes;
+    f.w_base = (uint32_t)stage * kMxTileBytes + (X == kMxCodes ? 0 : (step & 3) * S::kTileStep);
     f.wave = wave;
     asm("" : "+s"(f.wave));
 #pragma unroll
@@ -121,14 +122,10 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(buf + (f.wave * kXLoads + i) * 1024), 16, at, base, 0, 0);
     } else {
       const int first = ((i - kXLoads) * kWaves + f.wave) * 1024;       // byte of the step's weights
-      uint32_t at, base;
-      if constexpr (X == kMxCodes) {
-        at = lane * 16 + first;
-        base = 0;
-      } else {                            // a quarter of each tile: two tiles a load
-        at = half * kMxTileBytes + l32 * 16 + first / S::kTileStep * kMxTileBytes;
-        base = (step & 3) * S::kTileStep;
-      }
+      // 16-bit x: a quarter of each tile, two tiles a load
+      const uint32_t at = (X == kMxCodes ? lane * 16 : half * tile_bytes + l32 * 16) +
+                          (uint32_t)(first / S::kTileStep) * tile_bytes + first % S::kTileStep;
+      const uint32_t base = f.w_base;
       const rsrc_t rsrc = make_rsrc(f.w, f.w_size);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(buf + S::kWAt + first), 16, at, base, 0, 0);
     }
@@ -142,8 +139,8 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
     int stage = X == kMxCodes ? byte / S::kWsStage : 0;
     stage = stage < last ? stage : last;
     const int tile = rest / 128 < p.tiles ? rest / 128 : p.tiles - 1;
-    const rsrc_t rsrc = make_rsrc(a.packed + a.lay.scales_at + ((size_t)first * a.lay.tiles + p.tile0) * 128, 0x7fffffffu);
-    const uint32_t at = (uint32_t)(stage * a.lay.tiles + tile) * 128 + rest % 128;
+    const rsrc_t rsrc = make_rsrc(a.packed + a.lay.scales_at + ((size_t)p.tile0 * a.lay.stages + first) * 128, 0x7fffffffu);
+    const uint32_t at = (uint32_t)(tile * a.lay.stages + stage) * 128 + rest % 128;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(to + n * 1024), 16, at, 0, 0, 0);
   };
   // Rows of x: through registers, since a lane's products take every other byte.  Sixteen bytes (two steps) of a row a
