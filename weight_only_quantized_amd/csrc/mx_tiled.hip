@@ -26,6 +26,8 @@ template <int X, int FR, int FC>
 struct Shape {
   // A workgroup alone on its CU goes through several tiles, without a pause between them.
   static constexpr bool kLong = FR * FC >= 16;
+  // Small tiles are bound by the way of their operands: two steps to a buffer, a barrier every other step.
+  static constexpr int kSub = FR * FC == 1 ? 2 : 1;
   static constexpr int kRows = 64 * FR, kOuts = 64 * FC, kTiles = kOuts / 16;
   static constexpr int kInputs = X == kMxCodes ? 256 : 64;              // of a step
   static constexpr int kTileStep = X == kMxCodes ? kMxTileBytes : kMxTileBytes / 4;      // bytes of a tile's codes in a step
@@ -69,8 +71,8 @@ template <int X, int FR, int FC, int SIDES>
 __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a, int row_tiles, int col_tiles) {
   using S = Shape<X, FR, FC>;
   // separate arrays: the compiler then knows that reads of one do not wait for loads into another
-  __shared__ __align__(1024) uint8_t buf0[S::kBytes];
-  __shared__ __align__(1024) uint8_t buf1[S::kBytes];
+  __shared__ __align__(1024) uint8_t buf0[S::kSub * S::kBytes];
+  __shared__ __align__(1024) uint8_t buf1[S::kSub * S::kBytes];
   __shared__ __align__(1024) uint8_t w_scales[2][S::kWsLoads * 1024];   // of four steps and the next four
   __shared__ __align__(1024) uint8_t x_scales[2][S::kXsBytes];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -220,9 +222,10 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
   };
 
   // A turn multiplies step `step` (in buffer `here`, parity T) and prepares what follows it:
+  enum { kLoad, kNoLoad, kInside };
   struct Next {
-    Place two, group;                     // tiles of the step after the next, and of the next four steps' scales
-    int two_step, group_at;               // their places in them
+    Place two, group;                     // tiles of the steps that follow the other buffer's, and of the next four steps' scales
+    int two_step[S::kSub], group_at;      // their places in them
     int one_side, group_side;             // where the next step's scales lie, and the next four steps' go
   };
   // Part J: FC x FR products, each followed by its share of the reads for the next part (after part 3: for the next
@@ -231,9 +234,12 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
   // else the compiler's order, loads first, is the better one (1024 rows 128 x 128: 20 %).
   auto part = [&](auto J, auto T, auto L, const uint8_t* from, uint8_t* fill, int step, const Next& n) {
     constexpr int j = decltype(J)::value, t = decltype(T)::value;
-    constexpr int products = FC * FR, reads = j == 3 ? kFirstReads : kReads, loads = j == 3 && !decltype(L)::value ? kLoads : 0;
-    Source from_memory;
-    if constexpr (loads > 0) from_memory = source_of(n.two, n.two_step);
+    constexpr int products = FC * FR, reads = j == 3 ? kFirstReads : kReads, loads = j == 3 && decltype(L)::value == kLoad ? S::kSub * kLoads : 0;
+    Source from_memory[S::kSub];
+    if constexpr (loads > 0) {
+#pragma unroll
+      for (int i = 0; i < S::kSub; ++i) from_memory[i] = source_of(n.two, n.two_step[i]);
+    }
     u32x4 v;
     auto product = [&](auto P) {
       constexpr int p = decltype(P)::value, c = p / FR, r = p % FR;
@@ -260,15 +266,19 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
       constexpr int p = decltype(P)::value, places = decltype(Places)::value;
       if constexpr (j == 3 && p == 0) {
         read_scales(Int<t ^ 1>{}, step + 1, n.one_side);
-        if constexpr (X == kMxCodes && t == 0) store_xs(step >> 1 & 1, x_scales[n.group_side]);
+        if constexpr (X == kMxCodes && S::kSub == 1 && t == 0) store_xs(step >> 1 & 1, x_scales[n.group_side]);
+        if constexpr (X == kMxCodes && S::kSub == 2 && t == 1)
+          if (!(step & 2)) store_xs(0, x_scales[n.group_side]);
       }
       if constexpr (j == 0 && p == places - 1) {
-        if constexpr (X == kMxCodes && t == 0) load_xs(step >> 1 & 1, n.group, n.group_at);
+        if constexpr (X == kMxCodes && S::kSub == 1 && t == 0) load_xs(step >> 1 & 1, n.group, n.group_at);
+        if constexpr (X == kMxCodes && S::kSub == 2 && t == 0)
+          if (!(step & 2)) load_xs(0, n.group, n.group_at);
         issue_ws(t * kWaves + wave, n.group, n.group_at, w_scales[n.group_side]);
       }
       if constexpr (X == kMxCodes && j == 1 && t == 0) {
         constexpr int k0 = 4 * p / places, k1 = 4 * (p + 1) / places;
-        each<k1 - k0>([&](auto K) { keep_xs(Int<k0 + decltype(K)::value>{}, step >> 1 & 1, n.group_at); });
+        each<k1 - k0>([&](auto K) { keep_xs(Int<k0 + decltype(K)::value>{}, S::kSub == 1 ? step >> 1 & 1 : 0, n.group_at); });
       }
       constexpr int soon = places > 8 ? places * 5 / 8 : places;
       constexpr int read0 = p < soon ? reads * p / soon : reads, read1 = p < soon ? reads * (p + 1) / soon : reads;
@@ -276,7 +286,10 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
         read(Int<read0 + decltype(K)::value>{}, Int<(j + 1) & 3>{}, Int<j == 3 ? t ^ 1 : t>{}, from);
       });
       constexpr int issue0 = loads * p / places, issue1 = loads * (p + 1) / places;
-      each<issue1 - issue0>([&](auto K) { issue(Int<issue0 + decltype(K)::value>{}, from_memory, n.two_step, fill); });
+      each<issue1 - issue0>([&](auto K) {
+        constexpr int i = issue0 + decltype(K)::value, sub = i / kLoads;
+        issue(Int<i % kLoads>{}, from_memory[sub], n.two_step[sub], fill + sub * S::kBytes);
+      });
     };
     if constexpr (S::kLong) {
       each<products>([&](auto P) {
@@ -290,26 +303,34 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
       each<products>([&](auto P) { product(P); });
     }
   };
-  // A step's last part runs behind the barrier, from registers: there every wave has read the rest of the step and
-  // has its own loads of the next one in LDS (a full wait: a count of loads into LDS that may stay in flight
-  // is not a sound wait on this card).  So the next step's operands arrive under part 3, and this one's buffer
-  // takes the step after it (L: none yet, the results go through it first).
-  auto turn = [&](auto T, auto L, int step, uint8_t* here, uint8_t* next, const Next& n) {
+  // The last part of a buffer's last step runs behind the barrier, from registers: there every wave has read the rest of
+  // the buffer and has its own loads of the other one in LDS (a full wait: a count of loads into LDS that may stay
+  // in flight is not a sound wait on this card).  So the next step's operands arrive under part 3, and this buffer
+  // (`fill`) takes the steps after the other one's.  L: kLoad; kNoLoad: the results go through the buffer first;
+  // kInside: not a buffer's last step.
+  auto turn = [&](auto T, auto L, int step, const uint8_t* here, const uint8_t* next, uint8_t* fill, const Next& n) {
     settle(T, step);
     part(Int<0>{}, T, L, here, nullptr, step, n);
     part(Int<1>{}, T, L, here, nullptr, step, n);
     part(Int<2>{}, T, L, here, nullptr, step, n);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    part(Int<3>{}, T, L, next, here, step, n);
+    if constexpr (decltype(L)::value != kInside) {
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+    }
+    part(Int<3>{}, T, L, next, fill, step, n);
   };
 
   const int total = row_tiles * col_tiles;
   Place here = place_of<S>(a, blockIdx.x, row_tiles, col_tiles);
-  {
-    const Source f = source_of(here, 0);
-    each<kLoads>([&](auto I) { issue(I, f, 0, buf0); });
-  }
+  auto fill_buffer = [&](const Place& p, int step, uint8_t* buf) {
+    each<S::kSub>([&](auto I) {
+      constexpr int sub = decltype(I)::value;
+      const int at = step + sub < steps ? step + sub : steps - 1;
+      const Source f = source_of(p, at);
+      each<kLoads>([&](auto K) { issue(K, f, at, buf + sub * S::kBytes); });
+    });
+  };
+  fill_buffer(here, 0, buf0);
   for (int n = wave; n < S::kWsLoads; n += kWaves) issue_ws(n, here, 0, w_scales[0]);
   if constexpr (X == kMxCodes) {
     for (int part = 0; part < 2; ++part) {
@@ -322,11 +343,7 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
   __syncthreads();
   read_scales(Int<0>{}, 0, 0);
   each<kFirstReads>([&](auto I) { read(I, Int<0>{}, Int<0>{}, buf0); });
-  {
-    const int one = steps > 1 ? 1 : 0;
-    const Source f = source_of(here, one);
-    each<kLoads>([&](auto I) { issue(I, f, one, buf1); });
-  }
+  fill_buffer(here, S::kSub, buf1);
 
   int round = 0;                          // groups of four steps so far: the parity of their scales
   for (int id = blockIdx.x;;) {
@@ -351,7 +368,11 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
       Next n;
       const bool last_two = step + 2 >= steps, last_four = (step | 3) + 1 >= steps;
       n.two = S::kLong && last_two ? after : here;
-      n.two_step = !last_two ? step + 2 : S::kLong ? step + 2 - steps : steps - 1;
+#pragma unroll
+      for (int i = 0; i < S::kSub; ++i) {
+        const int at = step + 1 + S::kSub + i;
+        n.two_step[i] = at < steps ? at : S::kLong ? at - steps : steps - 1;
+      }
       n.group = S::kLong && last_four ? after : here;
       n.group_at = last_four && S::kLong ? 0 : (step >> 2) + 1;
       n.group_side = (round + (step >> 2) + 1) & 1;
@@ -360,21 +381,41 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
     };
     int step = 0;
     auto pair = [&](auto L) {
-      turn(Int<0>{}, Int<0>{}, step, buf0, buf1, next_of(step));
-      turn(Int<1>{}, L, step + 1, buf1, buf0, next_of(step + 1));
+      turn(Int<0>{}, Int<kLoad>{}, step, buf0, buf1, buf0, next_of(step));
+      turn(Int<1>{}, L, step + 1, buf1, buf0, buf1, next_of(step + 1));
       step += 2;
     };
     if constexpr (S::kLong) {
-      do pair(Int<0>{});
+      do pair(Int<kLoad>{});
       while (step + 2 < steps);
-      pair(Int<1>{});
+      pair(Int<kNoLoad>{});
 #pragma unroll
       for (int c = 0; c < FC; ++c)
 #pragma unroll
         for (int r = 0; r < FR; ++r) asm("" : "+a"(acc[c][r]));
+    } else if constexpr (S::kSub == 2) {
+      auto first = [&](const uint8_t* buf) {
+        turn(Int<0>{}, Int<kInside>{}, step, buf, buf + S::kBytes, nullptr, next_of(step));
+        ++step;
+      };
+      auto second = [&](uint8_t* buf, const uint8_t* other) {
+        turn(Int<1>{}, Int<kLoad>{}, step, buf + S::kBytes, other, buf, next_of(step));
+        ++step;
+      };
+      while (step + 3 < steps) {
+        first(buf0);
+        second(buf0, buf1);
+        first(buf1);
+        second(buf1, buf0);
+      }
+      if (step < steps) first(buf0);
+      if (step < steps) second(buf0, buf1);
+      if (step < steps) first(buf1);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
     } else {
-      while (step + 1 < steps) pair(Int<0>{});
-      if (step < steps) turn(Int<0>{}, Int<0>{}, step, buf0, buf1, next_of(step));
+      while (step + 1 < steps) pair(Int<kLoad>{});
+      if (step < steps) turn(Int<0>{}, Int<kLoad>{}, step, buf0, buf1, buf0, next_of(step));
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
     }
@@ -408,8 +449,8 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
     // past the caches: with runs of 32 bytes, straight from registers, 4096 x 28672 results took 100 us of 490, so 40.
     constexpr int kGroup = FC < 2 * SIDES ? FC : 2 * SIDES;             // products side by side in a pass
     constexpr int kWide = 32 * kGroup / SIDES, kPitch = kWide * 2 + 16; // outputs of a pass, bytes of its rows
-    constexpr int kHigh = FR >= 2 && 4 * 64 * kPitch <= S::kBytes ? 2 : 1;      // products one below the other
-    static_assert(4 * kHigh * 32 * kPitch <= S::kBytes && FC % kGroup == 0 && FR % kHigh == 0, "four waves share a buffer");
+    constexpr int kHigh = FR >= 2 && 4 * 64 * kPitch <= S::kSub * S::kBytes ? 2 : 1;     // products one below the other
+    static_assert(4 * kHigh * 32 * kPitch <= S::kSub * S::kBytes && FC % kGroup == 0 && FR % kHigh == 0, "four waves share a buffer");
     uint8_t* mine = buf1 + wave * (kHigh * 32 * kPitch);
 #pragma unroll
     for (int c0 = 0; c0 < FC; c0 += kGroup)
@@ -452,8 +493,7 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
     id = next_id;
     here = after;
     __syncthreads();
-    const Source f = source_of(here, 1);
-    each<kLoads>([&](auto I) { issue(I, f, 1, buf1); });
+    fill_buffer(here, 1, buf1);
   }
   __builtin_amdgcn_s_waitcnt(0);          // no load into LDS outlives the workgroup
 }
@@ -472,11 +512,11 @@ hipError_t run(const MxGemmCall& c, hipStream_t s) {
 // Microseconds of a step of a tile when the card is full (`full`, for each tile of a CU), and at least (`least`: a step's
 // loads and its barrier), measured: tiles of 256, 128 and 64 rows and outputs.
 struct Cost { double full, least; };
-constexpr Cost kCodesCost[3] = {{1.95, 1.8}, {0.65, 0.8}, {0.27, 0.6}}, k16Cost[3] = {{1.46, 1.4}, {0.43, 0.5}, {0.165, 0.4}};
+constexpr Cost kCodesCost[3] = {{1.95, 1.8}, {0.65, 0.8}, {0.27, 0.36}}, k16Cost[3] = {{1.46, 1.4}, {0.43, 0.5}, {0.165, 0.33}};
 
 // Large tiles load each operand least often, small ones fill the card and its last round.  The estimate for each
 // size ranks as measured, us for 256 / 128 / 64: 4096 rows in codes, 8192 -> 28672: 439 / 587 / 979; 1301 rows, 4160 -> 4001: 48 /
-// 28 / 34; 257 rows, 4096 -> 4096: 29 / 14 / 12; 512 rows, 8192 -> 8192: 56 / 28 / 38, in 16 bits - / 72 / 89.
+// 28 / 34; 257 rows, 4096 -> 4096: 29 / 14 / 11; 512 rows, 8192 -> 8192: 56 / 28 / 38, in 16 bits - / 72 / 89.
 template <int X>
 int size_of(const MxGemmCall& c) {
   int best = 0;

@@ -36,14 +36,14 @@ def _raise(st, where):
 
 def _rows16(x):
     """(x, elements between its rows) with rows 16 bytes aligned and dense; copied if they are not so."""
-    width, size = x.shape[1], x.element_size()
-    if x.data_ptr() & 15 == 0:
-        if x.is_contiguous():
-            return x, width
+    if x.is_contiguous():
+        if not x.data_ptr() & 15:
+            return x, x.shape[1]
+    elif not x.data_ptr() & 15:
         row, one = x.stride()
-        if one == 1 and width <= row <= 1 << 21 and row * size % 16 == 0 and x.shape[0] > 1:
+        if one == 1 and x.shape[1] <= row <= 1 << 21 and row * x.element_size() % 16 == 0 and x.shape[0] > 1:
             return x, row
-    return x.clone(memory_format=torch.contiguous_format), width
+    return x.clone(memory_format=torch.contiguous_format), x.shape[1]
 
 
 class MXTensor:
@@ -63,47 +63,66 @@ class MXTensor:
             raise ValueError("codes and scales must be on one device")
         if not codes.is_contiguous() or codes.data_ptr() & 15:
             codes = codes.clone(memory_format=torch.contiguous_format)
-        if not _scales_fit(scales):
-            room = _new_scales(rows, K, scales.device)
+        stride = _words(K)
+        if _scales_fit(scales):
+            stride = scales.stride(0) if rows > 1 else stride
+        else:
+            room = torch.empty((rows, stride), dtype=torch.uint8, device=scales.device)[:, :K // 32]
             room.copy_(scales)
             scales = room
-        self._set(codes, scales, rows, K)
+        self._codes, self._scales = self._keep = codes, scales
+        self._set(rows, K, codes.get_device(), codes.data_ptr(), scales.data_ptr(), stride)
 
-    def _set(self, codes, scales, rows, K):
-        self.codes, self.scales, self.rows, self.K = codes, scales, rows, K
-        self.device = codes.device
-        self._index = codes.get_device()
-        self._stride = scales.stride(0) if rows > 1 else (K // 32 + 3) // 4 * 4
-        self._c = _TENSOR.pack(codes.data_ptr(), scales.data_ptr(), self._stride, rows, K, 0)
+    def _set(self, rows, K, index, codes, scales, stride):
+        self.rows, self.K, self._index, self._stride = rows, K, index, stride
+        self._c = _TENSOR.pack(codes, scales, stride, rows, K, 0)
 
-    @classmethod
-    def _empty(cls, rows, K, device):
-        t = cls.__new__(cls)
-        t._set(torch.empty((rows, K // 2), dtype=torch.uint8, device=device), _new_scales(rows, K, device), rows, K)
-        return t
+    # quantize makes one buffer, whose views a call that only passes the tensor on does not need
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._keep[0].as_strided((self.rows, self.K // 2), (self.K // 2, 1))
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._keep[0].as_strided((self.rows, self.K // 32), (self._stride, 1),
+                                                    _codes_room(self.rows, self.K))
+        return self._scales
+
+    @property
+    def device(self):
+        return self._keep[0].device
 
     @classmethod
     def quantize(cls, x, stream=None):
         """x [rows, K] (fp16/bf16/fp32, K a multiple of 32) in the format: each block's scale is
         2 ** (floor(log2 max|x|) - 2), values rounded to nearest, ties to even, past 6 to 6; a block with an
         infinity or NaN is NaN (gptq_mx_quantize)."""
-        code = _ALL.get(x.dtype)
+        code, shape = _ALL.get(x.dtype), x.shape
         if code is None:
             raise TypeError("x must be float16, bfloat16 or float32")
-        if x.dim() != 2 or x.shape[1] < 32 or x.shape[1] % 32:
+        if len(shape) != 2 or shape[1] < 32 or shape[1] % 32:
             raise ValueError("x must be [rows, K] with K a multiple of 32")
         index = x.get_device()
         ptr = _here(stream, index)
         if ptr is not None:
-            return cls._quantize(ptr, x, code)
+            return cls._quantize(ptr, x, code, index)
         with _Queue(stream, index, x) as ptr:
-            return cls._quantize(ptr, x, code)
+            return cls._quantize(ptr, x, code, index)
 
     @classmethod
-    def _quantize(cls, ptr, x, code):
-        x, stride = _rows16(x)
-        t = cls._empty(x.shape[0], x.shape[1], x.device)
-        st = load_library().gptq_mx_quantize(x.data_ptr(), stride, code, t._c, ptr)
+    def _quantize(cls, ptr, x, code, index):
+        x, x_stride = _rows16(x)
+        rows, K = x.shape
+        at, stride = _codes_room(rows, K), _words(K)
+        room = x.new_empty(at + rows * stride, dtype=torch.uint8)
+        t = cls.__new__(cls)
+        t._keep, t._codes, t._scales = (room,), None, None
+        base = room.data_ptr()
+        t._set(rows, K, index, base, base + at, stride)
+        st = load_library().gptq_mx_quantize(x.data_ptr(), x_stride, code, t._c, ptr)
         if st:
             _raise(st, "gptq_mx_quantize")
         return t
@@ -116,20 +135,25 @@ class MXTensor:
         ptr = _here(stream, self._index)
         if ptr is not None:
             return self._dequantize(ptr, dtype, code)
-        with _Queue(stream, self._index, self.codes, self.scales) as ptr:
+        with _Queue(stream, self._index, *self._keep) as ptr:
             return self._dequantize(ptr, dtype, code)
 
     def _dequantize(self, ptr, dtype, code):
-        out = torch.empty((self.rows, self.K), dtype=dtype, device=self.device)
+        out = self._keep[0].new_empty((self.rows, self.K), dtype=dtype)
         st = load_library().gptq_mx_dequantize(self._c, out.data_ptr(), code, ptr)
         if st:
             _raise(st, "gptq_mx_dequantize")
         return out
 
 
-def _new_scales(rows, K, device):
-    """uint8 [rows, K / 32] whose rows are whole 32-bit words."""
-    return torch.empty((rows, (K // 32 + 3) // 4 * 4), dtype=torch.uint8, device=device)[:, :K // 32]
+def _words(K):
+    """Bytes between rows of scales that are whole 32-bit words."""
+    return (K // 32 + 3) // 4 * 4
+
+
+def _codes_room(rows, K):
+    """Bytes from a quantized tensor's codes to its scales (K / 2 is a multiple of 16)."""
+    return rows * K // 2
 
 
 def _scales_fit(s):
@@ -147,7 +171,7 @@ def _scales_fit(s):
 class _MXProduct:
     """Weights laid out for the products (gptq_mx_pack)."""
 
-    def _load(self, weight, up, activation, stream):
+    def _load(self, weight, up, activation):
         for name, t in (("weight", weight),) if up is None else (("gate", weight), ("up", up)):
             if not isinstance(t, MXTensor):
                 raise TypeError(f"{name} must be an MXTensor")
@@ -160,12 +184,11 @@ class _MXProduct:
         st = self._lib.gptq_mx_weight_bytes(self.N, self.K, 0 if up is None else 1, ctypes.byref(size))
         if st:
             _raise(st, "gptq_mx_weight_bytes")
-        ptr = _here(stream, self._index)
+        ptr = _here(None, self._index)
         if ptr is not None:
             self._pack(ptr, weight, up, size.value)
         else:
-            parts = [t for w in (weight, up) if w is not None for t in (w.codes, w.scales)]
-            with _Queue(stream, self._index, *parts) as ptr:
+            with _Queue(None, self._index) as ptr:
                 self._pack(ptr, weight, up, size.value)
         self._c = _WEIGHT.pack(self.packed.data_ptr(), self.N, self.K, activation, 0)
 
@@ -180,39 +203,41 @@ class _MXProduct:
         (the result is of `dtype`, bfloat16 by default).  out, when given, is a contiguous [M, N] tensor of
         that type (gptq_mx_gemm, gptq_mx_gemm_mx)."""
         if isinstance(x, MXTensor):
-            M, index = x.rows, x._index
+            M, index, parts = x.rows, x._index, x._keep
             if x.K != self.K:
                 raise ValueError(f"x must have {self.K} inputs")
             if dtype is None:
                 dtype = torch.bfloat16 if out is None else out.dtype
-            parts = (x.codes, x.scales)
         else:
-            if x.dim() != 2 or x.shape[1] != self.K:
+            shape = x.shape
+            if len(shape) != 2 or shape[1] != self.K:
                 raise ValueError(f"x must be [M, {self.K}]")
+            M, index, parts = shape[0], x.get_device(), (x,)
             if dtype is not None and dtype is not x.dtype:
                 raise TypeError("the result has x's dtype")
-            M, index, dtype, parts = x.shape[0], x.get_device(), x.dtype, (x,)
-        if dtype not in _CODES:
+            dtype = x.dtype
+        code = _CODES.get(dtype)
+        if code is None:
             raise TypeError("x, or dtype, must be float16 or bfloat16")
         if index != self._index:
             raise ValueError(f"x must be on {self.device}")
-        if out is not None and (tuple(out.shape) != (M, self.N) or out.dtype is not dtype or out.get_device() != index
+        if out is not None and (out.shape != (M, self.N) or out.dtype is not dtype or out.get_device() != index
                                 or not out.is_contiguous()):
             raise ValueError(f"out must be a contiguous [M, {self.N}] tensor of {dtype} on {self.device}")
         ptr = _here(stream, index)
         if ptr is not None:
-            return self._gemm(ptr, x, M, out, dtype)
+            return self._gemm(ptr, x, M, out, dtype, code)
         with _Queue(stream, index, out, self.packed, *parts) as ptr:
-            return self._gemm(ptr, x, M, out, dtype)
+            return self._gemm(ptr, x, M, out, dtype, code)
 
-    def _gemm(self, ptr, x, M, out, dtype):
+    def _gemm(self, ptr, x, M, out, dtype, code):
         if out is None:
-            out = torch.empty((M, self.N), dtype=dtype, device=self.device)
+            out = self.packed.new_empty((M, self.N), dtype=dtype)
         if isinstance(x, MXTensor):
-            st, where = self._lib.gptq_mx_gemm_mx(self._c, x._c, out.data_ptr(), _CODES[dtype], ptr), "gptq_mx_gemm_mx"
+            st, where = self._lib.gptq_mx_gemm_mx(self._c, x._c, out.data_ptr(), code, ptr), "gptq_mx_gemm_mx"
         else:
             x, stride = _rows16(x)
-            st = self._lib.gptq_mx_gemm(self._c, x.data_ptr(), stride, _CODES[dtype], M, out.data_ptr(), ptr)
+            st = self._lib.gptq_mx_gemm(self._c, x.data_ptr(), stride, code, M, out.data_ptr(), ptr)
             where = "gptq_mx_gemm"
         if st:
             _raise(st, where)
@@ -222,16 +247,16 @@ class _MXProduct:
 class MXLinear(_MXProduct):
     """y = x W^T for weights W [N, K] in the format.  The source tensors may be freed afterwards."""
 
-    def __init__(self, weight, stream=None):
-        self._load(weight, None, 0, stream)
+    def __init__(self, weight):
+        self._load(weight, None, 0)
 
 
 class MXGatedLinear(_MXProduct):
     """act(x Wg^T) * (x Wu^T) in one kernel for the two projections [N, K] of a gated feed-forward block;
     activation "silu" or "gelu_tanh"."""
 
-    def __init__(self, gate, up, activation="silu", stream=None):
+    def __init__(self, gate, up, activation="silu"):
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
         self.activation = activation
-        self._load(gate, up, ACTIVATIONS[activation], stream)
+        self._load(gate, up, ACTIVATIONS[activation])
