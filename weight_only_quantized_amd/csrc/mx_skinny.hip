@@ -1,12 +1,15 @@
 // Products with packed 4-bit weights for few rows: y = x W^T, or act(x Wg^T) * (x Wu^T).
 //
-// Bound by the weights' bytes.  A wave multiplies a tile of 16 outputs (a gated pair: two) with up to
-// 64 rows, straight from global memory to registers: weights are the first operand of a 16 x 16
-// matrix instruction, read once in 1 KB runs, rows of x the second.  The waves of a workgroup take
-// the chunks of 128 inputs in turn and their sums are added in LDS in a fixed order, so a call's
-// bits do not depend on timing.  Activations in the format go to v_mfma_scale_f32_16x16x128_f8f6f4 with both
-// sides' scales; 16-bit ones to 16x16x32 products with the weights turned into the same type in
-// registers, which is exact (mx_dev.h).
+// Bound by the weights' bytes, and beyond a few rows by the reads of x, which every workgroup makes for
+// itself.  A wave multiplies CT tiles of 16 packed outputs with up to 64 rows: weights go from memory to
+// registers once, in 1 KB runs, as the first operand of a 16 x 16 matrix instruction, rows of x are
+// the second.  The waves of a workgroup share the inputs, in chunks of 128, and their sums are
+// added in LDS in a fixed order, so a call's bits do not depend on timing.  Activations in the format go to
+// v_mfma_scale_f32_16x16x128_f8f6f4 with both sides' scales; 16-bit ones to 16x16x32 products with the
+// weights turned into the same type in registers, which is exact (mx_dev.h).
+//
+// Measured: one row, 4096 -> 14336: 8.1 us, 3.8 TB/s (7.4 in codes), the pair of a gated block 12.0, 5.2 TB/s, launch and
+// Python's call (6 us on the host) included; 16 rows in 16 bits, 8192 -> 28672: 30 us, 4.2 TB/s; 61 in codes, 8192 -> 8192: 11.7.
 #include "mx_dev.h"
 #include "serving.h"
 
@@ -25,12 +28,13 @@ __device__ __forceinline__ u32x4 turned(u32x4 v) {
 }
 
 // MT tiles of 16 rows by CT tiles of 16 packed outputs (a gated pair: two) a wave, DEPTH chunks of it in flight.
-template <int X, int MT, int CT, int SIDES, int DEPTH, int BOUND>
+template <int X, int MT, int CT, int SIDES, int DEPTH, int BOUND, bool STAGE>
 __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int groups) {
   constexpr int waves = kSkinnyWaves;
   constexpr int kFit = 64 / (waves * SIDES * MT), kOutTiles = CT / SIDES;        // output tiles joined at once, in 64 KB
   constexpr int kBatch = kFit < 1 ? 1 : kFit < kOutTiles ? kFit : kOutTiles, kBatchTiles = kBatch * SIDES;
-  __shared__ f32x4 sums[waves * kBatchTiles * MT * 64];                          // [wave][output tile][row tile][lane]
+  constexpr int kSums = waves * kBatchTiles * MT * 64, XL = X == kMxCodes ? 1 : 4, kStaged = STAGE ? waves * XL * 64 : 0;
+  __shared__ f32x4 sums[kSums > kStaged ? kSums : kStaged];                      // [wave][output tile][row tile][lane]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int tile0 = blockIdx.x % groups * CT, last = a.lay.tiles - 1 - tile0;
@@ -51,7 +55,7 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
   const rsrc_t x_rsrc = make_rsrc(a.x + m0 * a.x_bytes, (uint32_t)(rows * a.x_bytes));
   const rsrc_t xs_rsrc = X == kMxCodes ? make_rsrc(a.x_scales + m0 * a.x_scale_stride, (uint32_t)(rows * a.x_scale_stride))
                                        : x_rsrc;
-  constexpr int XL = X == kMxCodes ? 1 : 4, WS = X == kMxCodes ? 1 : 2;
+  constexpr int WS = X == kMxCodes ? 1 : 2;
 
   // Chunk q is blocks 4 q .. 4 q + 3.  Codes: lane group g multiplies block g of it, whole.  16 bits: product p takes block
   // p, a quarter of it each group, so that a load of x reads runs of 64 bytes.  A wave takes DEPTH chunks
@@ -59,6 +63,14 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
   // of up to 16 rows every eighth, so that the waves read side by side (one row, 4096 -> 14336: 8.2 us against 9.6).
   constexpr bool kNear = MT > 1;
   constexpr int kStep = kNear ? 1 : waves, kStages = kNear ? (DEPTH + 1) / 2 : DEPTH;
+  // STAGE: neighbouring lanes read neighbouring pieces of a row, and a wave turns them in LDS (piece j of row r at a place
+  // such that sixteen rows' pieces of one number lie on all banks).  Straight from memory a load takes 16 bytes of each of
+  // sixteen rows, a cache access for every lane: 48 gated rows in 16 bits, 4096 -> 14336: 30.4 us against 24.5; 32 rows, 4096 -> 4096:
+  // 10.4 against 7.5; of up to 8 rows, or 16 in codes, there is little to gain (16 in codes, 4096 -> 14336: 7.5 against 7.8).
+  u32x4* staged = (u32x4*)sums + wave * XL * 64;
+  const auto place = [](int row, int piece) {
+    return X == kMxCodes ? row * 4 + (piece ^ (row >> 2 & 3)) : row * 16 + (piece ^ row);
+  };
   f32x4 acc[CT][MT] = {};
   u32x4 w[DEPTH][CT], x[DEPTH][MT][XL];
   uint32_t ws[kStages][CT][WS], xs[MT][DEPTH];
@@ -80,12 +92,12 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int row = m * 16 + r;
 #pragma unroll
         for (int p = 0; p < XL; ++p) {
-          const bool there = 4 * q + (X == kMxCodes ? g : p) < blocks && row < rows;
-          const uint32_t piece = X == kMxCodes ? q * 64 + g * 16 : q * 256 + p * 64 + g * 16;
-          x[d][m][p] = load_b128(x_rsrc, there ? (uint32_t)(row * a.x_bytes) + piece : kOob, 0);
+          const int row = m * 16 + (!STAGE ? r : X == kMxCodes ? lane >> 2 : 4 * p + g);
+          const int piece = X == kMxCodes ? (STAGE ? lane & 3 : g) : STAGE ? r : 4 * p + g;
+          const bool there = 4 * q + (X == kMxCodes ? piece : piece >> 2) < blocks && row < rows;
+          x[d][m][p] = load_b128(x_rsrc, there ? (uint32_t)(row * a.x_bytes) + (uint32_t)(q * XL * 64 + piece * 16) : kOob, 0);
         }
       }
     }
@@ -105,6 +117,21 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       const int q = q0 + d * kStep, c = q & 1, stage = kNear ? d / 2 : d;
+      if constexpr (STAGE) {
+        // rows' pieces as they were loaded, to where their products take them; a wave's LDS accesses stay in order
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int p = 0; p < XL; ++p) {
+            const int row = X == kMxCodes ? lane >> 2 : 4 * p + g, piece = X == kMxCodes ? lane & 3 : r;
+            staged[place(row, piece)] = x[d][m][p];
+          }
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int p = 0; p < XL; ++p) x[d][m][p] = staged[place(r, X == kMxCodes ? g : 4 * p + g)];
+          __builtin_amdgcn_wave_barrier();
+        }
+      }
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
         // byte j of word h is the scale of the stage's block 2 j + h
@@ -138,7 +165,7 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
   // lane l of a product holds outputs 4 (l / 16) .. + 3 of row l % 16
 #pragma unroll
   for (int first = 0; first < kOutTiles; first += kBatch) {
-    if (first > 0) __syncthreads();
+    if (STAGE || first > 0) __syncthreads();
 #pragma unroll
     for (int i = 0; i < kBatchTiles; ++i)
 #pragma unroll
@@ -181,15 +208,18 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
   }
 }
 
-template <int X, int MT, int CT, int SIDES>
+template <int X, int MT, int CT, int SIDES, bool STAGE = (MT > 1 || (X != kMxCodes && CT == 4))>
 hipError_t run(const MxGemmCall& c, hipStream_t s) {
-  // registers: 4 CT MT of sums, and DEPTH times the operands
-  constexpr int kChunk = X == kMxCodes ? 5 * CT + 5 * MT : 6 * CT + 16 * MT, kFree = 190 - 4 * CT * MT;
+  // Registers: 4 CT MT of sums, and DEPTH times the operands.  Fewer chunks at once leave room for a second workgroup on a CU,
+  // but for few tiles of codes.  Us with 190 / 120 here: 16 rows in 16 bits, 8192 -> 28672: 39 / 30; 32, 14336 -> 4096: 17.6 / 15.1; 64 gated
+  // rows in codes, 4096 -> 14336: 19.0 / 17.7; 61 rows in codes, 8192 -> 8192 (CT 2): 11.7 / 12.7.
+  constexpr int kChunk = X == kMxCodes ? 5 * CT + 5 * MT : 6 * CT + 16 * MT;
+  constexpr int kFree = (STAGE && !(X == kMxCodes && CT <= 2) ? 120 : 190) - 4 * CT * MT;
   constexpr int DEPTH = kFree >= 4 * kChunk ? 4 : kFree >= 2 * kChunk ? 2 : 1;
   constexpr int BOUND = MT == 1 && CT <= 2 ? 1024 : 512;
   const int groups = (c.lay.tiles + CT - 1) / CT;
   const int64_t row_blocks = (c.M + MT * 16 - 1) / (MT * 16);
-  mx_skinny_kernel<X, MT, CT, SIDES, DEPTH, BOUND><<<(unsigned)(groups * row_blocks), kSkinnyWaves * 64, 0, s>>>(c, groups);
+  mx_skinny_kernel<X, MT, CT, SIDES, DEPTH, BOUND, STAGE><<<(unsigned)(groups * row_blocks), kSkinnyWaves * 64, 0, s>>>(c, groups);
   return hipGetLastError();
 }
 
