@@ -60,7 +60,7 @@ gptq_status run_gemm(const gptq_mx_weight* w, MxGemmCall& c, void* stream) {
   c.K = w->K;
   c.act = w->activation;
   if (overlaps(c.y, (size_t)c.M * c.N * 2, c.packed, c.lay.bytes)) return GPTQ_E_INVALID_ARG;
-  const bool few = c.M <= kMxSkinnyRows;
+  const bool few = c.M <= kMxSkinnyRows || (mx_skinny_fits(c) && mx_skinny_us(c) < mx_tiled_us(c));
   if (few ? !mx_skinny_fits(c) : !mx_tiled_fits(c)) return GPTQ_E_SHAPE;
   const gptq_status st = check_device();
   if (st != GPTQ_OK) return st;

@@ -58,10 +58,17 @@ struct MxGemmCall {
   uint16_t* y;                            // [M, N]
   int y_bf16;
 };
-// Calls of up to this many rows stream the weights (mx_skinny.hip), longer ones go by tiles (mx_tiled.hip).
+constexpr int kMxCus = 256;               // compute units of the card
+
+// The kernel that streams the weights for each 64 rows (mx_skinny.hip) takes calls of up to this many rows ...
 constexpr int64_t kMxSkinnyRows = 64;
 bool mx_skinny_fits(const MxGemmCall& c);
 hipError_t launch_mx_skinny(const MxGemmCall& c, hipStream_t s);
+// ... and longer ones that its estimate, in us, puts before the kernel by tiles (mx_tiled.hip): few outputs, or 16 bits and few
+// rows.  Us by tiles / streamed: 128 rows in 16 bits, 4096 -> 4096: 22.5 / 16.7, 14336 -> 4096: 72 / 45, 4096 -> 14336 gated: 38 / 53; 256 rows,
+// 4096 -> 512: 23 / 10, 4096 -> 4096: 23 / 28; in codes 128 rows, 4096 -> 4096: 8.6 / 10.8, 256 rows, 4096 -> 512: 7.7 / 6.5.
+double mx_skinny_us(const MxGemmCall& c);
+double mx_tiled_us(const MxGemmCall& c);
 bool mx_tiled_fits(const MxGemmCall& c);
 hipError_t launch_mx_tiled(const MxGemmCall& c, hipStream_t s);
 

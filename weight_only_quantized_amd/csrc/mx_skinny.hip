@@ -227,12 +227,18 @@ hipError_t run(const MxGemmCall& c, hipStream_t s) {
 // workgroups.  Us for 1 / 2 / 4: 16 rows in 16 bits, 8192 -> 28672: 62 / 44 / 34; 61 in codes, 8192 -> 8192: 31 / 18 / 26; 48 gated, 4096 ->
 // 14336: - / 49 / 31.  Up to 8 rows x is little, and more workgroups are better: one row, 4096 -> 14336: 8.5 / 8.2 / 9.1; 4 in codes,
 // 8192 -> 8192: 7.7 / 8.0 / 9.0.
+int tiles_a_wave(const MxGemmCall& c) {
+  if (c.M > 8 && c.lay.tiles >= 4 * 200) return 4;
+  return c.lay.sides == 2 || c.lay.tiles >= 2 * (c.M > 8 ? 200 : 400) ? 2 : 1;
+}
+
 template <int X, int MT, int SIDES>
 hipError_t run_tiles(const MxGemmCall& c, hipStream_t s) {
-  const int tiles = c.lay.tiles;
-  if (c.M > 8 && tiles >= 4 * 200) return run<X, MT, 4, SIDES>(c, s);
-  if (SIDES == 2 || tiles >= 2 * (c.M > 8 ? 200 : 400)) return run<X, MT, 2, SIDES>(c, s);
-  return run<X, MT, SIDES, SIDES>(c, s);
+  switch (tiles_a_wave(c)) {
+    case 4: return run<X, MT, 4, SIDES>(c, s);
+    case 2: return run<X, MT, 2, SIDES>(c, s);
+    default: return run<X, MT, SIDES, SIDES>(c, s);
+  }
 }
 
 template <int X, int SIDES>
@@ -249,6 +255,14 @@ hipError_t run_sides(const MxGemmCall& c, hipStream_t s) {
 }
 
 }  // namespace
+
+// Rounds of workgroups over the card, of chunks over a workgroup's waves, and what a chunk takes (measured, 64 rows).
+double mx_skinny_us(const MxGemmCall& c) {
+  const int ct = tiles_a_wave(c), chunks = (c.K + 127) / 128;
+  const int64_t groups = (c.M + 63) / 64 * ((c.lay.tiles + ct - 1) / ct);
+  const double chunk = c.x_kind == kMxCodes ? 0.5 + 0.33 * ct : 1.1 + 0.5 * ct;
+  return 3.0 + (double)((groups + kMxCus - 1) / kMxCus) * ((chunks + kSkinnyWaves - 1) / kSkinnyWaves) * chunk;
+}
 
 bool mx_skinny_fits(const MxGemmCall& c) { return grid_fits((c.M + 15) / 16 * (c.lay.tiles / c.lay.sides), 512); }
 

@@ -18,7 +18,6 @@
 namespace gq {
 namespace {
 
-constexpr int kCus = 256;                 // compute units of the card
 constexpr int kWaves = 4, kTiledThreads = 64 * kWaves;
 constexpr int kXRow = 128;                // bytes of a row of x in a step
 
@@ -504,7 +503,7 @@ hipError_t run(const MxGemmCall& c, hipStream_t s) {
   const int64_t row_tiles = (c.M + S::kRows - 1) / S::kRows;
   const int col_tiles = (c.lay.tiles + S::kTiles - 1) / S::kTiles;
   int64_t groups = row_tiles * col_tiles;
-  if (S::kLong && groups > kCus) groups = kCus;
+  if (S::kLong && groups > kMxCus) groups = kMxCus;
   mx_tiled_kernel<X, FR, FC, SIDES><<<(unsigned)groups, kTiledThreads, 0, s>>>(c, (int)row_tiles, col_tiles);
   return hipGetLastError();
 }
@@ -517,22 +516,24 @@ constexpr Cost kCodesCost[3] = {{1.95, 1.8}, {0.65, 0.8}, {0.27, 0.36}}, k16Cost
 // Large tiles load each operand least often, small ones fill the card and its last round.  The estimate for each
 // size ranks as measured, us for 256 / 128 / 64: 4096 rows in codes, 8192 -> 28672: 439 / 587 / 979; 1301 rows, 4160 -> 4001: 48 /
 // 28 / 34; 257 rows, 4096 -> 4096: 29 / 14 / 11; 512 rows, 8192 -> 8192: 56 / 28 / 38, in 16 bits - / 72 / 89.
-template <int X>
-int size_of(const MxGemmCall& c) {
+int size_of(const MxGemmCall& c, double* us) {
+  const bool codes = c.x_kind == kMxCodes;
+  const int64_t steps = (c.K + (codes ? 255 : 63)) / (codes ? 256 : 64);
   int best = 0;
-  double least = 0;
   for (int i = 0; i < 3; ++i) {
     const int64_t side = 256 >> i, tiles = (c.M + side - 1) / side * ((c.lay.tiles + side / 16 - 1) / (side / 16));
-    const Cost& cost = (X == kMxCodes ? kCodesCost : k16Cost)[i];
-    const double full = (double)((tiles + kCus - 1) / kCus) * cost.full, t = full > cost.least ? full : cost.least;
-    if (i == 0 || t < least) best = i, least = t;
+    const Cost& cost = (codes ? kCodesCost : k16Cost)[i];
+    const double full = (double)((tiles + kMxCus - 1) / kMxCus) * cost.full;
+    const double t = 3.0 + (double)steps * (full > cost.least ? full : cost.least);
+    if (i == 0 || t < *us) best = i, *us = t;
   }
   return best;
 }
 
 template <int X, int SIDES>
 hipError_t run_size(const MxGemmCall& c, hipStream_t s) {
-  switch (size_of<X>(c)) {
+  double us;
+  switch (size_of(c, &us)) {
     case 0: return run<X, 4, 4, SIDES>(c, s);
     case 1: return run<X, 2, 2, SIDES>(c, s);
     default: return run<X, 1, 1, SIDES>(c, s);
@@ -545,6 +546,12 @@ hipError_t run_sides(const MxGemmCall& c, hipStream_t s) {
 }
 
 }  // namespace
+
+double mx_tiled_us(const MxGemmCall& c) {
+  double us;
+  size_of(c, &us);
+  return us;
+}
 
 bool mx_tiled_fits(const MxGemmCall& c) { return grid_fits((c.M + 63) / 64 * ((c.lay.tiles + 3) / 4), kTiledThreads); }
 
