@@ -254,3 +254,285 @@ def test_product_of_many_tiles(x_kind, M, N, K):
     # float32 holds these sums exactly in any order, as it does in the product
     want = torch.from_numpy(xv.astype(np.float32)).cuda() @ torch.from_numpy(wv.astype(np.float32)).cuda().t()
     assert torch.equal(got, want.half())
+
+
+# ---- every form of the products ------------------------------------------------------------------
+
+def _exact_on_gpu(x, *sides):
+    """x W^T of exactly summable values, in float32 (any order gives the same), as float64 tensors."""
+    import torch
+    t = torch.from_numpy(x.astype(np.float32)).cuda()
+    return [(t @ torch.from_numpy(w.astype(np.float32)).cuda().t()).double() for w in sides]
+
+
+# rows, outputs, inputs: one and several row tiles, one to nine steps (even, odd, last ones not full), few and many
+# tiles a wave, tiles of 64, 128 and 256; see the rules in mx_skinny.hip and mx_tiled.hip
+FORMS = ([(m, 12805, k) for m in (1, 8, 9, 16, 17, 33, 64) for k in (288, 1120)]
+         + [(200, 4100, k) for k in (32, 64, 96, 256, 288, 512, 544, 768, 1056, 1312, 1568, 2304)]
+         + [(m, 6401, k) for m in (5, 16, 30, 48, 60) for k in (416,)] + [(1301, 4001, 416), (1301, 4000, 1312), (300, 130, 2048)])
+
+
+@pytest.mark.parametrize("x_kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_every_form(x_kind, M, N, K):
+    import torch
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M + N + K)
+    w = _exact_pair(rng, N, K)
+    if x_kind == "mx":
+        xq = _exact_pair(rng, M, K)
+        given, xv, dt = _mx(*xq), mo.values(*xq), torch.bfloat16
+    else:
+        xv = _x16(rng, M, K, x_kind)
+        given, dt = _dev(xv, x_kind), _dt(x_kind)
+    got = wq.MXLinear(_mx(*w)).gemm(given, dtype=dt)
+    assert torch.equal(got, _exact_on_gpu(xv, mo.values(*w))[0].to(dt))
+
+
+@pytest.mark.parametrize("x_kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("M,N,K", [(m, 6404, 416) for m in (1, 16, 30, 48, 60)] + [(200, 2050, k) for k in (96, 544, 1312)]
+                         + [(1301, 2001, 416), (4100, 2056, 288), (4100, 2051, 1056)])
+def test_every_gated_form(x_kind, M, N, K):
+    import torch
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M + N + K)
+    g, u = _exact_pair(rng, N, K), _exact_pair(rng, N, K)
+    g = (g[0], g[1] - 5)
+    if x_kind == "mx":
+        xq = _exact_pair(rng, M, K)
+        xq = (xq[0], xq[1] - 4)
+        given, xv, tag = _mx(*xq), mo.values(*xq), "bf16"
+    else:
+        xv = _x16(rng, M, K, x_kind) / 16
+        given, tag = _dev(xv, x_kind), x_kind
+    gv, uv = _exact_on_gpu(xv, mo.values(*g), mo.values(*u))
+    got = wq.MXGatedLinear(_mx(*g), _mx(*u), activation="silu").gemm(given, dtype=_dt(tag))
+    gv, uv = _f64(gv), _f64(uv)
+    _check_gated(_f64(got), mo.silu(gv) * uv, gv, uv, "silu", tag)
+
+
+# ---- the ends of the format ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_blocks_of_nan(M):
+    """A block of NaN makes the outputs it takes part in NaN, and no others."""
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M)
+    K, N = 544, 4100
+    w, xq = _exact_pair(rng, N, K), _exact_pair(rng, M, K)
+    w[1][7, 16], w[1][4099, 0], xq[1][M // 2, 3] = 255, 255, 255
+    layer = wq.MXLinear(_mx(*w))
+    x = _x16(rng, M, K, "f16")
+    x[0, 5] = np.nan
+    for given, xv, tag in ((_dev(x, "f16"), x, "f16"), (_dev(x, "bf16"), x, "bf16"), (_mx(*xq), mo.values(*xq), "bf16")):
+        got = _f64(layer.gemm(given, dtype=_dt(tag)))
+        bad = np.isnan(xv).any(1)[:, None] | np.isnan(mo.values(*w)).any(1)[None]
+        assert np.array_equal(np.isnan(got), bad)
+        want = _rounded(mo.gemm(np.nan_to_num(xv), np.nan_to_num(mo.values(*w))), tag)
+        assert np.array_equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("M", [1, 12, 300])
+def test_infinite_activations(M):
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M)
+    K, N = 288, 4100
+    w = (np.full((N, K // 2), 0x22, np.uint8), np.full((N, K // 32), 127, np.uint8))       # all ones
+    x = _x16(rng, M, K, "bf16")
+    x[0, 7] = np.inf
+    x[-1, 200] = -np.inf
+    for tag in ("f16", "bf16"):
+        got, want = _f64(wq.MXLinear(_mx(*w)).gemm(_dev(x, tag))), x.sum(1)
+        for m in range(M):
+            if np.isfinite(want[m]):
+                assert (got[m] == _rounded(want[m:m + 1], tag)[0]).all()
+            else:
+                assert np.array_equal(got[m], np.full(N, want[m]), equal_nan=True)
+
+
+@pytest.mark.parametrize("M", [2, 200])
+@pytest.mark.parametrize("x_kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("top", [40, 127, 200])
+def test_scales_far_apart(x_kind, M, top):
+    """Rows of weights of one size each, 2^-36 and up below the largest of their own; whole rows by the type's range."""
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M + top)
+    K, N = 256, 4100
+    codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    scales = rng.integers(top - 36, top + 1, (N, K // 32)).astype(np.uint8)
+    scales[:, 3] = top
+    wv = mo.values(codes, scales)
+    layer = wq.MXLinear(_mx(codes, scales))
+    shift = 2.0 ** (127 - top)                               # results near one: the types hold them
+    if x_kind == "mx":
+        c = rng.integers(0, 256, (M, K // 2), dtype=np.uint8)
+        s = np.full((M, K // 32), 254 - top, np.uint8)
+        given, xv, tag = _mx(c, s), mo.values(c, s), "bf16"
+    elif x_kind == "bf16":
+        xv = _x16(rng, M, K, "bf16") * shift
+        given, tag = _dev(xv, "bf16"), "bf16"
+    else:
+        if top != 127:
+            pytest.skip("float16 has no activations that bring such results near one")
+        xv = _x16(rng, M, K, "f16")
+        given, tag = _dev(xv, "f16"), "f16"
+    want, most = mo.gemm(xv, wv), mo.gemm(np.abs(xv), np.abs(wv))
+    got = _f64(layer.gemm(given, dtype=_dt(tag)))
+    assert np.all(np.abs(got - want) <= HALF_STEP[tag] * np.abs(want) + K * 2.0 ** -23 * most + SMALLEST[tag])
+
+
+def test_float16_weights_below_the_range():
+    """Scales more than 2^-36 below their row's largest: rounded to 2^-37 of that, as stated."""
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(0)
+    K, N, M = 128, 64, 3
+    codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    scales = rng.integers(127 - 60, 128 - 36, (N, K // 32)).astype(np.uint8)
+    scales[:, 0] = 127
+    x = _x16(rng, M, K, "f16")
+    x[:, :32] = 0                                            # only the small blocks count
+    want = mo.gemm(x * 2.0 ** 15, mo.values(codes, scales))
+    got = _f64(wq.MXLinear(_mx(codes, scales)).gemm(_dev(x * 2.0 ** 13, "f16"))) * 4
+    assert np.all(np.abs(got - want) <= (np.abs(x) * 2.0 ** 15).sum(1)[:, None] * 2.0 ** -37 + 2.0 ** -11 * np.abs(want) + 2.0 ** -23)
+
+
+# ---- calls ---------------------------------------------------------------------------------------
+
+def test_strides_out_and_equal_bits():
+    import torch
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(3)
+    K, N = 288, 333
+    w = _exact_pair(rng, N, K)
+    layer = wq.MXLinear(_mx(*w))
+    wide = torch.randn((90, 1024), device="cuda").bfloat16()
+    for x in (wide[:, 8:8 + K], wide[:, 3:3 + K], wide[::3, :K], wide.t()[:K].t()[:, :K], wide[5:6, :K], wide[:0, :K]):
+        out = torch.empty((x.shape[0], N), dtype=torch.bfloat16, device="cuda")
+        assert layer.gemm(x, out=out) is out
+        assert torch.equal(out, layer.gemm(x.contiguous()))
+    for M in (1, 64, 300):
+        x = torch.randn((M, K), device="cuda").half()
+        a = layer.gemm(x)
+        for _ in range(3):
+            assert torch.equal(a, layer.gemm(x))
+    q = wq.MXTensor.quantize(wide[:, :K])
+    assert layer.gemm(q).dtype == torch.bfloat16 and layer.gemm(q, dtype=torch.float16).dtype == torch.float16
+    for kw, error in ((dict(dtype=torch.float32), TypeError), (dict(out=torch.empty((90, N), device="cuda")), TypeError),
+                      (dict(out=torch.empty((89, N), device="cuda").half()), ValueError)):
+        with pytest.raises(error):
+            layer.gemm(q, **kw)
+    with pytest.raises(ValueError):
+        layer.gemm(wide)
+    with pytest.raises(TypeError):
+        layer.gemm(wide[:, :K].float())
+    with pytest.raises(wq.GPTQError):
+        layer.gemm(q, out=layer.packed[:90 * N * 2].view(torch.bfloat16).view(90, N))
+
+
+def test_other_streams_and_graphs():
+    import torch
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(4)
+    K, N, M = 1056, 700, 150
+    g, u, d = (_mx(*mo.quantize(rng.standard_normal(s) / 30)) for s in ((N, K), (N, K), (K, 704)))
+    up, down = wq.MXGatedLinear(g, u), wq.MXLinear(d)
+    x = torch.randn((M, K), device="cuda").bfloat16()
+
+    def block(x, stream=None):
+        h = torch.zeros((M, 704), dtype=x.dtype, device="cuda")
+        h[:, :N] = up.gemm(wq.MXTensor.quantize(x))
+        return down.gemm(wq.MXTensor.quantize(h)) + down.gemm(h)
+
+    want = block(x)
+    side = torch.cuda.Stream()
+    q = wq.MXTensor.quantize(x, stream=side)
+    h = up.gemm(q, stream=side)
+    back = q.dequantize(torch.float32, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(h, up.gemm(wq.MXTensor.quantize(x)))
+    assert torch.equal(back, wq.MXTensor.quantize(x).dequantize(torch.float32))
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block(x)
+    torch.cuda.current_stream().wait_stream(side)
+    static, graph = x.clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = block(static)
+    for i in range(4):
+        new = torch.randn((M, K), device="cuda").bfloat16() if i else x
+        static.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, block(new) if i else want), i
+
+
+def test_feed_forward_block_with_adapters():
+    """Gate, up and down projections in the format, a request's adapter beside the last: as a layer is served."""
+    import torch
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(6)
+    D, F, M = 512, 1376, 9
+    g, u, d = (mo.quantize(rng.standard_normal(s) / s[1] ** 0.5) for s in ((F, D), (F, D), (D, F)))
+    up, down = wq.MXGatedLinear(_mx(*g), _mx(*u), activation="gelu_tanh"), wq.MXLinear(_mx(*d))
+    a = torch.randn((3, 16, F), device="cuda").bfloat16() * F ** -0.5
+    b = torch.randn((3, D, 16), device="cuda").bfloat16() * 0.25
+    bank = wq.LoraBank(a, b, torch.ones(3, device="cuda"))
+    ids = torch.tensor([0, 1, 2, -1, 0, 0, 2, 1, -1], dtype=torch.int32, device="cuda")
+    x = torch.randn((M, D), device="cuda").bfloat16()
+    for mx in (False, True):
+        h = up.gemm(wq.MXTensor.quantize(x) if mx else x)
+        hv, y = _f64(h), down.gemm(wq.MXTensor.quantize(h) if mx else h)
+        got = _f64(bank.add(y, h, ids, out=y))
+        if mx:
+            xv, hin = mo.values(*mo.quantize(_f64(x))), mo.values(*mo.quantize(hv))
+        else:
+            xv, hin = _f64(x), hv
+        # each step against the step before it as it was, rounded: half a step each, and sums' own error
+        want_h = mo.gated(xv, mo.values(*g), mo.values(*u), "gelu_tanh")
+        assert np.linalg.norm(hv - want_h) <= 1.02 * HALF_STEP["bf16"] * np.linalg.norm(want_h)
+        y0, extra = mo.gemm(hin, mo.values(*d)), np.zeros((M, D))
+        av, bv = _f64(a), _f64(b)
+        for m, i in enumerate(ids.tolist()):
+            if i >= 0:
+                extra[m] = bv[i] @ (av[i] @ hv[m])
+        bound = HALF_STEP["bf16"] * 1.05 * (np.linalg.norm(y0) + np.linalg.norm(y0 + extra))
+        assert np.linalg.norm(got - (y0 + extra)) <= bound
+
+
+def test_offsets_past_32_bits():
+    """Weights of more than 4 GiB of codes, results of more than 2^32 bytes, quantized rows past 2^31 values."""
+    import torch
+    import weight_only_quantized_amd as wq
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    N, K = (1 << 19) + 5, 16640
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    scales = torch.randint(127, 129, (N, K // 32), dtype=torch.uint8, device="cuda", generator=gen)
+    assert codes.numel() > 1 << 32
+    layer = wq.MXLinear(wq.MXTensor(codes, scales))
+    rng = np.random.default_rng(1)
+    at = [0, 1, 262143, 262144, 400001, N - 17, N - 1]
+    wv = mo.values(codes[at].cpu().numpy(), scales[at].cpu().numpy())
+    x = _x16(rng, 3, K, "f16") / 4
+    got = _f64(layer.gemm(_dev(x, "f16"))[:, at])
+    assert np.array_equal(got, _rounded(mo.gemm(x, wv), "f16"))
+    xq = _random(rng, 70, K, 124, 126)
+    got = _f64(layer.gemm(_mx(*xq), dtype=torch.float16)[:, at])
+    assert np.array_equal(got, _rounded(mo.gemm(mo.values(*xq), wv), "f16"))
+    del codes, scales, layer
+    M, N, K = 70001, 33000, 32
+    w = _exact_pair(rng, N, K)
+    x = (torch.randint(-16, 17, (M, K), device="cuda", generator=gen) / 4).bfloat16()
+    y = wq.MXLinear(_mx(*w)).gemm(x)
+    assert y.numel() * 2 > 1 << 32
+    rows = [0, 1, 32767, 65536, M - 1]
+    assert np.array_equal(_f64(y[rows]), _rounded(mo.gemm(_f64(x[rows]), mo.values(*w)), "bf16"))
+    del y
+    x = torch.randn((1 << 17, 16448), device="cuda", generator=gen).bfloat16()
+    assert x.numel() > 1 << 31
+    t = wq.MXTensor.quantize(x)
+    back = t.dequantize(torch.bfloat16)
+    rows = [0, 65535, 65536, 130560, 131071]
+    c, s = mo.quantize(_f64(x[rows]))
+    assert np.array_equal(t.codes[rows].cpu().numpy(), c) and np.array_equal(t.scales[rows].cpu().numpy(), s)
+    assert np.array_equal(_f64(back[rows]), mo.values(c, s))

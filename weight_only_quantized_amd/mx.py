@@ -172,7 +172,7 @@ class _MXProduct:
     """Weights laid out for the products (gptq_mx_pack)."""
 
     def _load(self, weight, up, activation):
-        for name, t in (("weight", weight),) if up is None else (("gate", weight), ("up", up)):
+        for name, t in (("gate", weight), ("up", up)) if activation else (("weight", weight),):
             if not isinstance(t, MXTensor):
                 raise TypeError(f"{name} must be an MXTensor")
         if up is not None and (up.rows != weight.rows or up.K != weight.K or up.device != weight.device):
