@@ -1,9 +1,11 @@
 #!/usr/bin/env python3
 """One attention layer of a served decoder on an MI355X: quantized projections with the requests' own
-low-rank adapters beside them, a paged 8-bit cache, prompts first and then token by token.
+low-rank adapters beside them, a paged 8-bit cache, prompts first and then token by token; with
+--feed-forward the layer's feed-forward block too, its weights in microscaled 4-bit floating point.
 
     python examples/serve_layer.py                      # Llama-3-8B-shaped layer, 4 requests
     python examples/serve_layer.py --requests 64 --tokens 100 --graph
+    python examples/serve_layer.py --requests 64 --feed-forward 14336 --graph
 
 Weights, adapters and inputs are random: the layer shows how the calls go together and prints times.
 """
@@ -84,6 +86,28 @@ class AttentionLayer:
         return z
 
 
+class FeedForward:
+    """x -> down(act(x Wg^T) * (x Wu^T)) with weights in the format.  Few rows are multiplied as they are (the
+    weights' bytes take the time), many in 4 bits too (four times the rate of 16-bit products)."""
+
+    def __init__(self, gate, up, down, activation="silu", many=256):
+        self.gate_up, self.down, self.many = wq.MXGatedLinear(gate, up, activation), wq.MXLinear(down), many
+
+    def __call__(self, x):
+        quantized = wq.MXTensor.quantize if x.shape[0] > self.many else lambda t: t
+        return self.down.gemm(quantized(self.gate_up.gemm(quantized(x), dtype=x.dtype)), dtype=x.dtype)
+
+
+def random_feed_forward(hidden, inner, seed=2):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+
+    def weights(N, K):
+        return wq.MXTensor.quantize(torch.empty((N, K), device="cuda").normal_(0, K ** -0.5, generator=gen))
+
+    return FeedForward(weights(inner, hidden), weights(inner, hidden), weights(hidden, inner))
+
+
 def random_projection(K, N, gen, bits=4, group=128):
     """A repacked 4-bit layer of random codes with weights of about K ** -0.5."""
     G = K // group
@@ -121,6 +145,7 @@ def main(argv=None):
     p.add_argument("--tokens", type=int, default=32, help="tokens to generate")
     p.add_argument("--page", type=int, default=16)
     p.add_argument("--rank", type=int, default=16)
+    p.add_argument("--feed-forward", type=int, default=0, help="width of the feed-forward block, a multiple of 32 (0: none)")
     p.add_argument("--graph", action="store_true", help="replay the token step as one HIP graph")
     a = p.parse_args(argv)
     hidden, q_heads, kv_heads, dim, dtype = 4096, 32, 8, 128, torch.bfloat16
@@ -128,6 +153,7 @@ def main(argv=None):
     longest = max(prompts) + a.tokens
     width = -(-longest // a.page)
     layer = random_layer(hidden, q_heads, kv_heads, dim, width * a.requests, a.page, longest, 8, a.rank, dtype)
+    block = random_feed_forward(hidden, a.feed_forward) if a.feed_forward else None
     pages = Pages(width * a.requests, a.page, a.requests, width)
     gen = torch.Generator(device="cuda")
     gen.manual_seed(1)
@@ -142,6 +168,8 @@ def main(argv=None):
     torch.cuda.synchronize()
     t = time.perf_counter()
     z = layer(x, table, start, cu, max(prompts), ids)
+    if block is not None:
+        z = z + block(z)
     torch.cuda.synchronize()
     print(f"prompts of {sum(prompts)} tokens: {1e3 * (time.perf_counter() - t):.2f} ms (first call)")
 
@@ -152,6 +180,8 @@ def main(argv=None):
 
     def step():
         z = layer(x, table, length, one, 1, adapter)
+        if block is not None:
+            z = z + block(z)
         z.mul_(z.float().pow(2).mean(-1, keepdim=True).rsqrt().to(z.dtype))
         length.add_(1)
         x.copy_(z)

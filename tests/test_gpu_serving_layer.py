@@ -93,3 +93,28 @@ def test_command_runs(example, graph, capsys):
     if graph:
         import torch
         assert torch.equal(x, example.main(argv[:-1]))
+
+
+def test_feed_forward_block(example, capsys):
+    """The block against the float64 oracle, few rows as they are and many in 4 bits, and the command with it."""
+    import torch
+    import oracle.mx_oracle as mo
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(9)
+    D, F = 256, 704
+    parts = [mo.quantize(rng.standard_normal(s) * s[1] ** -0.5) for s in ((F, D), (F, D), (D, F))]
+    block = example.FeedForward(*(wq.MXTensor(torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda()) for c, s in parts), many=20)
+    g, u, d = (mo.values(*p) for p in parts)
+    half_step = 2.0 ** -8
+    for rows in (3, 20, 21, 150):
+        x = torch.from_numpy(rng.standard_normal((rows, D)).astype(np.float32)).cuda().bfloat16()
+        quantized = (lambda t: mo.values(*mo.quantize(t))) if rows > 20 else (lambda t: t)
+        host = lambda t: t.cpu().double().numpy()  # noqa: E731
+        h = block.gate_up.gemm(wq.MXTensor.quantize(x) if rows > 20 else x, dtype=x.dtype)
+        want_h = mo.gated(quantized(host(x)), g, u, "silu")
+        assert np.linalg.norm(host(h) - want_h) <= 1.02 * half_step * np.linalg.norm(want_h)
+        want = mo.gemm(quantized(host(h)), d)
+        assert np.linalg.norm(host(block(x)) - want) <= 1.02 * half_step * np.linalg.norm(want)
+    argv = ["--requests", "3", "--prompt", "90", "--tokens", "6", "--feed-forward", "352"]
+    x = example.main(argv)
+    assert torch.equal(x, example.main(argv + ["--graph"]))
