@@ -55,6 +55,10 @@ __device__ __forceinline__ float mx_gate(float g, float u, int act) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * t)) * u;
 }
 
+// Results of rows whose length is odd lie at any even address: vectors that say so.
+typedef u32x4 __attribute__((aligned(2), may_alias)) u32x4_at2;
+typedef u32x2 __attribute__((aligned(2), may_alias)) u32x2_at2;
+
 __device__ __forceinline__ uint16_t mx_round(float v, int bf16) { return bf16 ? from_f32<1>(v) : from_f32<0>(v); }
 
 }  // namespace gq

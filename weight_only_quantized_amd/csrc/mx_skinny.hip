@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
       }
       const int n = tile / SIDES * 16 + o;
       uint16_t* y = a.y + (m0 + row) * a.N + n;
-      if (a.N % 4 == 0 && n < a.N) {
-        *(uint64_t*)y = (uint64_t)(v[0] | (uint32_t)v[1] << 16) | (uint64_t)(v[2] | (uint32_t)v[3] << 16) << 32;
+      if (n + 4 <= a.N) {
+        *(u32x2_at2*)y = u32x2{(uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16};
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)

@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
         __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the wave's own writes
         __builtin_amdgcn_wave_barrier();
         const int n0 = (here.tile0 + (wave_n * FC + c0) * 2) / SIDES * 16, row0 = wave_m * FR * 32 + r0 * 32;
+        constexpr int kLanes = kWide / 8;                // of a row, 16 bytes each
         if (a.N % 8 == 0) {
-          constexpr int kLanes = kWide / 8;              // of a row, 16 bytes each
 #pragma unroll 4
           for (int i = 0; i < kHigh * 32; i += 64 / kLanes) {
             const int row = i + lane / kLanes, n = n0 + lane % kLanes * 8;
@@ -478,11 +478,16 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
               __builtin_nontemporal_store(v, (u32x4*)(a.y + (int64_t)(here.m0 + row0 + row) * a.N + n));
           }
         } else {
-#pragma unroll 4
-          for (int i = 0; i < kHigh * 32; i += 64 / kWide) {
-            const int row = i + lane / kWide, n = n0 + lane % kWide;
-            if (row0 + row < here.rows && n < a.N)
-              a.y[(int64_t)(here.m0 + row0 + row) * a.N + n] = *(const uint16_t*)(mine + row * kPitch + lane % kWide * 2);
+#pragma unroll 1
+          for (int i = 0; i < kHigh * 32; i += 64 / kLanes) {
+            const int row = i + lane / kLanes, n = n0 + lane % kLanes * 8;
+            const uint16_t* v = (const uint16_t*)(mine + row * kPitch + lane % kLanes * 16);
+            uint16_t* y = a.y + (int64_t)(here.m0 + row0 + row) * a.N + n;
+            const int left = row0 + row < here.rows ? a.N - n : 0;
+            if (left >= 8) *(u32x4_at2*)y = *(const u32x4*)v;
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+              if (left < 8 && e < left) y[e] = v[e];
           }
         }
         __builtin_amdgcn_s_waitcnt(0xC07F);
