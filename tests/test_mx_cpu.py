@@ -1,10 +1,14 @@
 """Refusals of the entry points on microscaled 4-bit floating point (host checks: no GPU, no launch), and
 pins of their oracle."""
+import copy
 import ctypes
+import pickle
+import struct
 from fractions import Fraction
 
 import numpy as np
 import pytest
+import torch
 
 import oracle.mx_oracle as mo
 import weight_only_quantized_amd as wq
@@ -250,3 +254,20 @@ def test_planted_mistakes_fail():
     away = [int(np.argmin(np.abs(abs(v) - mo.VALUES[::-1]))) for v in x[0, :4]]
     assert [7 - a for a in away] != [7, 0, 4, 6]
     assert not np.array_equal((codes & 15) << 4 | codes >> 4, codes)
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+@pytest.mark.parametrize("rows,inputs", [(0, 32), (1, 96), (5, 96), (3, 128)])
+def test_copies_of_a_tensor_describe_their_own_memory(how, rows, inputs):
+    codes = torch.arange(rows * inputs // 2).reshape(rows, inputs // 2).to(torch.uint8)
+    scales = torch.arange(rows * inputs // 32).reshape(rows, inputs // 32).to(torch.uint8)
+    t = wq.MXTensor(codes, scales)
+    u = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda v: pickle.loads(pickle.dumps(v))}[how](t)
+    assert (u.rows, u.K) == (rows, inputs) and torch.equal(u.codes, codes) and torch.equal(u.scales, scales)
+    at, scales_at, stride, n, k, _ = struct.unpack("PPqqii", u._c)
+    assert (at, scales_at, n, k) == (u.codes.data_ptr(), u.scales.data_ptr(), rows, inputs)
+    assert stride >= inputs // 32 and stride % 4 == 0
+    if rows:
+        assert scales_at + rows * stride <= u.scales.untyped_storage().data_ptr() + u.scales.untyped_storage().nbytes()
+        if how != "copy":
+            assert at != t.codes.data_ptr() and scales_at != t.scales.data_ptr()

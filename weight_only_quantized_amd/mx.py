@@ -77,6 +77,10 @@ class MXTensor:
         self.rows, self.K, self._index, self._stride = rows, K, index, stride
         self._c = _TENSOR.pack(codes, scales, stride, rows, K, 0)
 
+    def __reduce__(self):
+        # a copy or an unpickled tensor packs the addresses of its own memory
+        return type(self), (self.codes, self.scales)
+
     # quantize makes one buffer, whose views a call that only passes the tensor on does not need
     @property
     def codes(self):
