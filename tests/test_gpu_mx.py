@@ -381,6 +381,29 @@ def test_scales_far_apart(x_kind, M, top):
     assert np.all(np.abs(got - want) <= HALF_STEP[tag] * np.abs(want) + K * 2.0 ** -23 * most + SMALLEST[tag])
 
 
+@pytest.mark.parametrize("M", [2, 40, 200, 1100])
+@pytest.mark.parametrize("case", ["bf16 weights", "bf16 activations", "f16 activations", "mx weights", "mx activations"])
+def test_operands_below_the_normal_range(case, M):
+    """Subnormal 16-bit operands, and scales at the format's ends, times what brings them near one.  Sums are fewer
+    than 2^22 steps of one size: float32 holds them exactly."""
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M)
+    K, N = 256, 1300
+    # the smallest weight scale, and the activations' unit or smallest scale byte
+    low, unit, kind = {"bf16 weights": (0, 120, "bf16"), "bf16 activations": (249, -131, "bf16"), "f16 activations": (144, -22, "f16"),
+                       "mx weights": (0, 251, "mx"), "mx activations": (251, 0, "mx")}[case]
+    w = rng.integers(0, 256, (N, K // 2), dtype=np.uint8), rng.integers(low, low + 4, (N, K // 32)).astype(np.uint8)
+    if kind == "mx":
+        xq = rng.integers(0, 256, (M, K // 2), dtype=np.uint8), rng.integers(unit, unit + 4, (M, K // 32)).astype(np.uint8)
+        given, xv, tag = _mx(*xq), mo.values(*xq), "bf16"
+    else:
+        xv = rng.integers(-16, 17, (M, K)) / 4 * 2.0 ** unit
+        given, tag = _dev(xv, kind), kind
+        assert np.array_equal(_f64(given), xv)
+    got = _f64(wq.MXLinear(_mx(*w)).gemm(given, dtype=_dt(tag)))
+    assert np.array_equal(got, _rounded(mo.gemm(xv, mo.values(*w)), tag))
+
+
 def test_float16_weights_below_the_range():
     """Scales more than 2^-36 below their row's largest: rounded to 2^-37 of that, as stated."""
     import weight_only_quantized_amd as wq
