@@ -311,6 +311,34 @@ def test_every_gated_form(x_kind, M, N, K):
     _check_gated(_f64(got), mo.silu(gv) * uv, gv, uv, "silu", tag)
 
 
+@pytest.mark.parametrize("tag", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(33, 25605, 288), (48, 25700, 1120), (40, 25664, 32), (47, 25599, 2336)])
+def test_eight_tiles_a_wave(tag, M, N, K):
+    """33 to 48 rows of 16 bits by many outputs: whole groups of eight tiles, and last ones of one and of seven."""
+    import torch
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M + N + K)
+    w = _exact_pair(rng, N, K)
+    for n, by in ((5, 3), (N - 20, 1), (N - 1, 2)):          # rows of their own largest scale: multiples of 2^-6 below 2^18
+        w[1][n] -= by
+    xv = _x16(rng, M, K, tag)
+    want = _exact_on_gpu(xv, mo.values(*w))[0].to(_dt(tag))
+    assert torch.equal(wq.MXLinear(_mx(*w)).gemm(_dev(xv, tag)), want)
+
+
+@pytest.mark.parametrize("tag", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(48, 12805, 416), (33, 12864, 96)])
+def test_eight_gated_tiles_a_wave(tag, M, N, K):
+    import weight_only_quantized_amd as wq
+    rng = np.random.default_rng(M + N + K)
+    g, u = _exact_pair(rng, N, K), _exact_pair(rng, N, K)
+    g = (g[0], g[1] - 5)
+    xv = _x16(rng, M, K, tag) / 16
+    gv, uv = (_f64(v) for v in _exact_on_gpu(xv, mo.values(*g), mo.values(*u)))
+    got = wq.MXGatedLinear(_mx(*g), _mx(*u), activation="silu").gemm(_dev(xv, tag))
+    _check_gated(_f64(got), mo.silu(gv) * uv, gv, uv, "silu", tag)
+
+
 # ---- the ends of the format ----------------------------------------------------------------------
 
 @pytest.mark.parametrize("M", [1, 40, 300])

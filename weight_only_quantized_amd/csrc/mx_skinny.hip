@@ -42,15 +42,30 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
   const int rows = a.M - m0 < MT * 16 ? (int)(a.M - m0) : MT * 16, blocks = a.K / 32;
   const int chunks = (blocks + 3) / 4;
 
+  // Up to four tiles a base each (one gated row, 4096 -> 14336: 12.4 us, from one base 13.6); more would not fit the scalar registers,
+  // and a tile's place goes into the offset.
+  constexpr bool kOneBase = CT > 4;
+  constexpr int kBases = kOneBase ? 1 : CT;
   const uint32_t w_size = (uint32_t)a.lay.stages * kMxTileBytes, s_size = (uint32_t)a.lay.stages * 128;
-  rsrc_t w_rsrc[CT], s_rsrc[CT];
-  int lift[CT] = {};                      // added to a scale byte (float16 activations)
+  const uint32_t held = !kOneBase ? 1 : last + 1 < CT ? last + 1 : CT;           // tiles of a base
+  rsrc_t w_rsrc[kBases], s_rsrc[kBases];
 #pragma unroll
-  for (int i = 0; i < CT; ++i) {
+  for (int i = 0; i < kBases; ++i) {
     const size_t tile = tile0 + (i < last ? i : last);   // past the last: not stored
-    w_rsrc[i] = make_rsrc(a.packed + tile * w_size, w_size);
-    s_rsrc[i] = make_rsrc(a.packed + a.lay.scales_at + tile * s_size, s_size);
-    if constexpr (X == kMxF16) lift[i] = 127 + kF16Top - a.packed[a.lay.tops_at + tile * 16 + r];
+    w_rsrc[i] = make_rsrc(a.packed + tile * w_size, held * w_size);
+    s_rsrc[i] = make_rsrc(a.packed + a.lay.scales_at + tile * s_size, held * s_size);
+  }
+  // Added to a scale byte (float16 activations): kLift less its row's largest; of more than four tiles those share registers.
+  constexpr int kLift = 127 + kF16Top;
+  int lift[kOneBase ? 1 : CT] = {};
+  uint32_t tops[kOneBase ? (CT + 3) / 4 : 1] = {};
+  if constexpr (X == kMxF16) {
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      const int top = a.packed[a.lay.tops_at + (size_t)(tile0 + (i < last ? i : last)) * 16 + r];
+      if constexpr (kOneBase) tops[i / 4] |= (uint32_t)top << (8 * (i % 4));
+      else lift[i] = kLift - top;
+    }
   }
   const rsrc_t x_rsrc = make_rsrc(a.x + m0 * a.x_bytes, (uint32_t)(rows * a.x_bytes));
   const rsrc_t xs_rsrc = X == kMxCodes ? make_rsrc(a.x_scales + m0 * a.x_scale_stride, (uint32_t)(rows * a.x_scale_stride))
@@ -83,11 +98,14 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
       const bool in = q < chunks;         // past the last all reads as zeros
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
-        w[d][i] = load_b128(w_rsrc[i], in ? (uint32_t)(c * 1024 + lane * 16) : kOob, (uint32_t)(q >> 1) * kMxTileBytes);
+        const int base = kOneBase ? 0 : i;
+        const uint32_t tile = !kOneBase ? 0 : i < last ? i : last;
+        w[d][i] = load_b128(w_rsrc[base], in ? (uint32_t)(c * 1024 + lane * 16) : kOob, tile * w_size + (uint32_t)(q >> 1) * kMxTileBytes);
         if (!kNear || d % 2 == 0) {
 #pragma unroll
           for (int h = 0; h < WS; ++h)
-            ws[stage][i][h] = load_b32(s_rsrc[i], in ? (uint32_t)((WS == 1 ? g & 1 : h) * 64 + r * 4) : kOob, (uint32_t)(q >> 1) * 128);
+            ws[stage][i][h] = load_b32(s_rsrc[base], in ? (uint32_t)((WS == 1 ? g & 1 : h) * 64 + r * 4) : kOob,
+                                       tile * s_size + (uint32_t)(q >> 1) * 128);
         }
       }
 #pragma unroll
@@ -153,7 +171,11 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             int s = (int)(ws[stage][i][p & 1] >> (16 * c + 8 * (p >> 1)) & 255);
-            if constexpr (X == kMxF16) s = s + lift[i] > 0 ? s + lift[i] : 0;
+            if constexpr (X == kMxF16) {
+              if constexpr (kOneBase) s += kLift - (int)(tops[i / 4] >> (8 * (i % 4)) & 255);
+              else s += lift[i];
+              s = s > 0 ? s : 0;
+            }
             const u32x4 wa = mx_values<X == kMxBf16>(u[p], scale_of(s));
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[i][m] = mfma16<X == kMxBf16>(wa, x[d][m][p], acc[i][m]);
@@ -208,7 +230,7 @@ __global__ void __launch_bounds__(BOUND) mx_skinny_kernel(MxGemmCall a, int grou
   }
 }
 
-template <int X, int MT, int CT, int SIDES, bool STAGE = (MT > 1 || (X != kMxCodes && CT == 4))>
+template <int X, int MT, int CT, int SIDES, bool STAGE = (MT > 1 || (X != kMxCodes && CT >= 4))>
 hipError_t run(const MxGemmCall& c, hipStream_t s) {
   // Registers: 4 CT MT of sums, and DEPTH times the operands.  Fewer chunks at once leave room for a second workgroup on a CU,
   // but for few tiles of codes.  Us with 190 / 120 here: 16 rows in 16 bits, 8192 -> 28672: 39 / 30; 32, 14336 -> 4096: 17.6 / 15.1; 64 gated
@@ -226,8 +248,10 @@ hipError_t run(const MxGemmCall& c, hipStream_t s) {
 // More tiles a wave read x less often (every workgroup reads all of it), fewer fill the card: as many as leave 200
 // workgroups.  Us for 1 / 2 / 4: 16 rows in 16 bits, 8192 -> 28672: 62 / 44 / 34; 61 in codes, 8192 -> 8192: 31 / 18 / 26; 48 gated, 4096 ->
 // 14336: - / 49 / 31.  Up to 8 rows x is little, and more workgroups are better: one row, 4096 -> 14336: 8.5 / 8.2 / 9.1; 4 in codes,
-// 8192 -> 8192: 7.7 / 8.0 / 9.0.
+// 8192 -> 8192: 7.7 / 8.0 / 9.0.  Eight for 33 to 48 rows in 16 bits, us for 4 / 8: 48, 8192 -> 28672: 46.9 / 38.0, 14336 -> 28672: 75 / 58;
+// 40 gated, 4096 -> 14336: 22.5 / 22.3.  For 32 rows 4 is better (gated, 4096 -> 14336: 16.6 / 20.3), for more the sums leave no registers.
 int tiles_a_wave(const MxGemmCall& c) {
+  if (c.M > 32 && c.M <= 48 && c.x_kind != kMxCodes && c.lay.tiles >= 8 * 200) return 8;
   if (c.M > 8 && c.lay.tiles >= 4 * 200) return 4;
   return c.lay.sides == 2 || c.lay.tiles >= 2 * (c.M > 8 ? 200 : 400) ? 2 : 1;
 }
@@ -235,6 +259,8 @@ int tiles_a_wave(const MxGemmCall& c) {
 template <int X, int MT, int SIDES>
 hipError_t run_tiles(const MxGemmCall& c, hipStream_t s) {
   switch (tiles_a_wave(c)) {
+    case 8:
+      if constexpr (X != kMxCodes && MT == 3) return run<X, MT, 8, SIDES>(c, s);
     case 4: return run<X, MT, 4, SIDES>(c, s);
     case 2: return run<X, MT, 2, SIDES>(c, s);
     default: return run<X, MT, SIDES, SIDES>(c, s);
