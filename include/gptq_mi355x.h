@@ -513,7 +513,8 @@ typedef struct {
  * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))), in float32 throughout, rounded once to y's dtype.
  * gptq_mx_gemm: x [M, K] in F16 or BF16 as it is, rows x_stride elements apart (a multiple of 8, up to 2^21),
  *   y of the same dtype.  BF16: every weight below 2^128 is exact.  F16: exact where its block's scale is at least 2^-36
- *   times the largest of its output's, otherwise rounded to 2^-37 times that.
+ *   times the largest of its output's (blocks of nothing but zeros aside), otherwise rounded to a multiple of 2^-37
+ *   times that.
  * gptq_mx_gemm_mx: x in the format, y F16 or BF16 (y_dtype).
  * y is contiguous, 16-byte aligned, and must not overlap x or the weights.  NaN blocks make the outputs that
  * they take part in NaN.  A call with the same arguments gives the same bits.

@@ -28,7 +28,7 @@ struct MxPacked {
   size_t scales_at, tops_at, bytes;       // codes lie at 0
 };
 // The parts of N x K weights with `sides` 1 or 2 (gated).  tops: each row's largest scale byte below
-// 255, or 255 when the row has a NaN block.
+// 255 over blocks that hold more than zeros, or 255 when the row has a NaN block.
 inline MxPacked mx_packed(int N, int K, int sides) {
   MxPacked p{sides, sides * ((N + 15) / 16), (K + kMxStage - 1) / kMxStage, 0, 0, 0};
   const size_t pieces = (size_t)p.tiles * p.stages;

@@ -154,36 +154,31 @@ struct PackSide {
   int64_t scale_stride;
 };
 
-// One workgroup a tile (mx.h): runs once, when weights are loaded.
+// One workgroup a tile (mx.h): runs once, when weights are loaded.  A block of nothing but 0 and -0 is packed with scale
+// 0, which its values do not show: whatever its own was, it must not set the unit of its row's other weights (kF16Top).
 __global__ void __launch_bounds__(kThreads) pack_kernel(PackSide a, PackSide b, int N, int K, MxPacked lay, uint8_t* out) {
   __shared__ int tops[kThreads];
   const int tile = blockIdx.x, side = tile % lay.sides, blocks = K / 32;
   const PackSide src = side ? b : a;
-  const int64_t n0 = (int64_t)(tile / lay.sides) * 16;
   uint8_t* codes = out + (size_t)tile * lay.stages * kMxTileBytes;
-  uint32_t* scales = (uint32_t*)(out + lay.scales_at) + (size_t)tile * lay.stages * 32;
+  uint8_t* scales = out + lay.scales_at + (size_t)tile * lay.stages * 128;
+  const int row = threadIdx.x % 16;       // a thread's blocks are all of one row
+  const int64_t n = (int64_t)(tile / lay.sides) * 16 + row;
+  int top = 0, bad = 0;
   for (int i = threadIdx.x; i < lay.stages * 128; i += kThreads) {
-    const int64_t n = n0 + i % 16;
     const int block = i / 16;
     u32x4 v = {0, 0, 0, 0};
-    if (n < N && block < blocks) v = *(const u32x4*)(src.codes + n * (K / 2) + (int64_t)block * 16);
-    *(u32x4*)(codes + (size_t)i * 16) = v;
-  }
-  for (int i = threadIdx.x; i < lay.stages * 32; i += kThreads) {
-    const int64_t n = n0 + i % 16;
-    const int block = i / 32 * 8 + (i / 16) % 2;
-    uint32_t word = 0;
-    for (int j = 0; j < 4; ++j)
-      if (n < N && block + 2 * j < blocks) word |= (uint32_t)src.scales[n * src.scale_stride + block + 2 * j] << (8 * j);
-    scales[i] = word;
-  }
-  int top = 0, bad = 0;
-  if (n0 + threadIdx.x % 16 < N)
-    for (int i = threadIdx.x / 16; i < blocks; i += kThreads / 16) {
-      const int s = src.scales[(n0 + threadIdx.x % 16) * src.scale_stride + i];
+    int s = 0;
+    if (n < N && block < blocks) {
+      v = *(const u32x4*)(src.codes + n * (K / 2) + (int64_t)block * 16);
+      s = src.scales[n * src.scale_stride + block];
       if (s == 255) bad = 1;
+      else if (!((v[0] | v[1] | v[2] | v[3]) & 0x77777777)) s = 0;
       else if (s > top) top = s;
     }
+    *(u32x4*)(codes + (size_t)i * 16) = v;
+    scales[(block / 8 * 32 + block % 2 * 16 + row) * 4 + block % 8 / 2] = (uint8_t)s;
+  }
   tops[threadIdx.x] = bad ? 255 : top;
   __syncthreads();
   if (threadIdx.x < 16) {
