@@ -27,6 +27,7 @@ ACTIVATIONS = {"silu": 1, "gelu_tanh": 2}
 _TENSOR = struct.Struct("PPqqii")          # gptq_mx_tensor
 _WEIGHT = struct.Struct("Piiii")           # gptq_mx_weight
 
+_E_SHAPE = 2                               # GPTQ_E_SHAPE
 _ALL = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 
 
@@ -74,6 +75,8 @@ class MXTensor:
         self._set(rows, K, codes.get_device(), codes.data_ptr(), scales.data_ptr(), stride)
 
     def _set(self, rows, K, index, codes, scales, stride):
+        if K > 0x7fffffff:
+            _raise(_E_SHAPE, "MXTensor")       # as the library says of rows past 2^20 inputs that its structure can name
         self.rows, self.K, self._index, self._stride = rows, K, index, stride
         self._c = _TENSOR.pack(codes, scales, stride, rows, K, 0)
 
