@@ -204,6 +204,11 @@ class _MXProduct:
         st = self._lib.gptq_mx_pack(weight._c, None if up is None else up._c, self.packed.data_ptr(), ptr)
         if st:
             _raise(st, "gptq_mx_pack")
+        # the sources may be freed at once: memory of another stream stays theirs until this one has read it
+        stream = torch.cuda.current_stream(self._index)
+        for t in (weight,) if up is None else (weight, up):
+            for part in t._keep:
+                part.record_stream(stream)
 
     def gemm(self, x, out=None, dtype=None, stream=None):
         """The product with x: a [M, K] fp16/bf16 tensor as it is (the result has its type), or an MXTensor
