@@ -511,6 +511,7 @@ typedef struct {
 
 /* y[M, N] = x W^T (PLAIN), or act(x Wg^T) * (x Wu^T) in one kernel (SILU: g / (1 + exp(-g)); GELU_TANH:
  * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))), in float32 throughout, rounded once to y's dtype.
+ *   An exponential past float32's range makes the activation 0 (g below -88.7; GELU_TANH: -10.06).
  * gptq_mx_gemm: x [M, K] in F16 or BF16 as it is, rows x_stride elements apart (a multiple of 8, up to 2^21),
  *   y of the same dtype.  BF16: every weight below 2^128 is exact.  F16: exact where its block's scale is at least 2^-36
  *   times the largest of its output's (blocks of nothing but zeros aside), otherwise rounded to a multiple of 2^-37

@@ -46,13 +46,15 @@ __device__ __forceinline__ float mx_row_factor(int top) {
   return top == 255 ? __builtin_nanf("") : ldexpf(1.0f, top - 127 - kF16Top);
 }
 
-// act(g) * u.  Both activations are g times a logistic function, whose exponential may overflow or
-// vanish without harm: silu(g) = g / (1 + exp(-g)); gelu's tanh form 0.5 g (1 + tanh(t)) = g / (1 + exp(-2 t)),
+// act(g) * u.  Both activations are g times a logistic function, whose exponential may overflow (what is
+// below 2^-128 counts as 0) or vanish without harm: silu(g) = g / (1 + exp(-g)); gelu's tanh form 0.5 g (1 + tanh(t)) = g / (1 + exp(-2 t)),
 // t = sqrt(2 / pi) (g + 0.044715 g^3), which keeps its digits for negative g, where 1 + tanh cancels.
 __device__ __forceinline__ float mx_gate(float g, float u, int act) {
   constexpr float kLog2e = 1.4426950408889634f, kRoot = 0.7978845608028654f;
   const float t = act == GPTQ_MX_SILU ? g : 2.0f * kRoot * (g + 0.044715f * g * g * g);
-  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * t)) * u;
+  // The card's reciprocal gives 0 below 2^-126, where g times it is still in range: it is taken of a quarter of the sum.
+  const float quarter = __builtin_fmaf(0.25f, __builtin_amdgcn_exp2f(-kLog2e * t), 0.25f);
+  return g * (0.25f * __builtin_amdgcn_rcpf(quarter)) * u;
 }
 
 // Results of rows whose length is odd lie at any even address: vectors that say so.
