@@ -518,7 +518,7 @@ typedef struct {
  *   times that.
  * gptq_mx_gemm_mx: x in the format, y F16 or BF16 (y_dtype).
  * y is contiguous, 16-byte aligned, and must not overlap x or the weights.  NaN blocks make the outputs that
- * they take part in NaN.  A call with the same arguments gives the same bits.
+ * they take part in NaN; so does an infinity of x times a weight of 0, one that F16 rounds to 0 included.  A call with the same arguments gives the same bits.
  * Errors: GPTQ_E_INVALID_ARG, GPTQ_E_SHAPE (sizes out of range, or a launch of 2^32 threads or more),
  * GPTQ_E_DEVICE, GPTQ_E_HIP.  M == 0: GPTQ_OK, nothing launched. */
 gptq_status gptq_mx_gemm(const gptq_mx_weight* weight, const void* x, int64_t x_stride, int32_t dtype, int64_t M, void* y,

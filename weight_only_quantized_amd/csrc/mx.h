@@ -9,8 +9,8 @@
 // 16 x 16 x 128 takes four blocks of a tile, 32 x 32 x 64 two blocks of two tiles.  Its scales are 32
 // words, [block & 1][row]: byte j of a word belongs to block 2 j + (block & 1), so the four
 // 32 x 32 x 64 instructions of a stage name bytes 0..3 of one register.  A tile's stages follow
-// one another: a wave that streams one reads on in memory (one row, 4096 -> 14336: 7.7 us; 9.1 with all tiles' first
-// stages first, where the kernel by tiles takes the same time).
+// one another: a wave that streams one reads on in memory (one row, 4096 -> 14336, when this was chosen: 7.7 us; 9.1 with all
+// tiles' first stages first, where the kernel by tiles takes the same time).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -60,12 +60,17 @@ struct MxGemmCall {
 };
 constexpr int kMxCus = 256;               // compute units of the card
 
-// The kernel that streams the weights for each 64 rows (mx_skinny.hip) takes calls of up to this many rows ...
+// The kernel that streams the weights for each 64 rows (mx_skinny.hip) takes calls of up to this many rows.  Us streamed / by tiles:
+// in 16 bits 33 rows, 8192 -> 28672: 36 / 65, 4096 -> 14336 gated: 21 / 26; 64 rows, 8192 -> 28672: 54 / 67, 14336 -> 4096: 27 / 71, 4096 ->
+// 4096: 11 / 22, 4096 -> 14336 gated: 25.7 / 26.2; in codes 33 rows, 14336 -> 4096: 9.5 / 22, 64 rows there 14.3 / 23.3, 8192 -> 8192: 11.7 /
+// 14.9.  Many outputs in codes are the other way about and go streamed all the same: 33 rows, 8192 -> 28672: 32.6 / 30.1, 64 rows 43.2 /
+// 32.8, 64 gated, 4096 -> 14336: 17.0 / 13.9 ...
 constexpr int64_t kMxSkinnyRows = 64;
 bool mx_skinny_fits(const MxGemmCall& c);
 hipError_t launch_mx_skinny(const MxGemmCall& c, hipStream_t s);
 // ... and longer ones that its estimate, in us, puts before the kernel by tiles (mx_tiled.hip): few outputs, or 16 bits and few
-// rows.  Us by tiles / streamed: 128 rows in 16 bits, 4096 -> 4096: 22.5 / 16.7, 14336 -> 4096: 72 / 45, 4096 -> 14336 gated: 38 / 53; 256 rows,
+// rows.  The estimates count rounds and steps, no bytes: where the weights' bytes alone take longer (64 rows in codes, 8192 -> 28672: 20
+// estimated by tiles, 32.8 measured) both are low.  Us by tiles / streamed: 128 rows in 16 bits, 4096 -> 4096: 22.5 / 16.7, 14336 -> 4096: 72 / 45, 4096 -> 14336 gated: 38 / 53; 256 rows,
 // 4096 -> 512: 23 / 10, 4096 -> 4096: 23 / 28; in codes 128 rows, 4096 -> 4096: 8.6 / 10.8, 256 rows, 4096 -> 512: 7.7 / 6.5.
 double mx_skinny_us(const MxGemmCall& c);
 double mx_tiled_us(const MxGemmCall& c);

@@ -6,10 +6,12 @@
 // the second.  The waves of a workgroup share the inputs, in chunks of 128, and their sums are
 // added in LDS in a fixed order, so a call's bits do not depend on timing.  Activations in the format go to
 // v_mfma_scale_f32_16x16x128_f8f6f4 with both sides' scales; 16-bit ones to 16x16x32 products with the
-// weights turned into the same type in registers, which is exact (mx_dev.h).
+// weights turned into the same type in registers: exact in bfloat16, in float16 down to 2^-36 of the output's largest
+// scale (kF16Top, mx_dev.h).
 //
-// Measured: one row, 4096 -> 14336: 8.1 us, 3.8 TB/s (7.4 in codes), the pair of a gated block 12.0, 5.2 TB/s, launch and
-// Python's call (6 us on the host) included; 16 rows in 16 bits, 8192 -> 28672: 30 us, 4.2 TB/s; 61 in codes, 8192 -> 8192: 11.7.
+// Measured, calls among others from Python: one row, 4096 -> 14336: 7.5 us, 4.2 TB/s (6.8 in codes), the pair of a gated block
+// 11.9, 5.2 TB/s (10.9 in codes); 16 rows in 16 bits, 8192 -> 28672: 29.7 us, 4.2 TB/s; 61 in codes, 8192 -> 8192: 11.2.  In the
+// comments below both sides of a choice are of one run, made when it was taken.
 #include "mx_dev.h"
 #include "serving.h"
 

@@ -3,19 +3,21 @@
 // Four waves share a tile of 64 FR rows by 64 FC packed outputs (a gated pair: 32 FC outputs), each FR x FC
 // products of 32 x 32, weights as the first operand.  A step takes 128 bytes of each row of x: 256 inputs in the
 // format (four v_mfma_scale_f32_32x32x64_f8f6f4 for each product, both sides' scales in the instruction) or 64
-// in 16 bits (four 32x32x16 products; weights become the same type in registers, exactly, see mx_dev.h).  Both
-// operands come through LDS, filled by buffer_load ... lds under the steps before; a part of a step (a quarter) is
-// multiplied from registers while the next part's operands are read.
+// in 16 bits (four 32x32x16 products; weights become the same type in registers: exactly in bfloat16, in float16 down
+// to 2^-36 of the output's largest scale, kF16Top in mx_dev.h).  Both operands come through LDS, filled by
+// buffer_load ... lds under the steps before; a part of a step (a quarter) is multiplied from registers while the next
+// part's operands are read.
 //
 // LDS: rows of x are 128 bytes, piece p (16 bytes) of row r at place p ^ (r / 2 & 7), so that sixteen rows' pieces of
 // one number lie on all banks; weights keep their packed order (mx.h), in which sixteen lanes read a run of 256.
 //
-// What bounds the largest tiles (256 x 256, one workgroup a CU, 512 registers a lane): matrix cores are busy 57 % of
-// the time at the 1.8 GHz that the card keeps under this load, waves wait 14 % of it for loads or the barrier and 39 %
-// for their turn to issue, mostly behind a product.  4096 rows in codes, 8192 -> 28672: 443 us, 4.3 PFLOP/s; 2003 gated rows,
-// 8192 -> 14336: 238 us, 3.9; 2048 in bfloat16, 4096 -> 14336: 184 to 193 us, 1.3 (a library product of two bfloat16 matrices
-// of 8192 reaches 1.18 on this card).  Copies that left parts out, when the first took 474 us: without loads 333, without reads from
-// LDS 433, without both 292; loads alone 287 of them (L2 to LDS at 14 TB/s), and 194 with all of them in L1.
+// What bounds the largest tiles (256 x 256, one workgroup a CU, 512 registers a lane): matrix cores are busy 55 % of
+// the time at the 1.8 GHz that the card keeps under this load, waves wait 16 % of it for loads or the barrier and 34 %
+// for their turn to issue, mostly behind a product (in 16 bits 58, 13 and 44; gated codes 47, 13 and 34).  4096 rows in codes,
+// 8192 -> 28672: 447 us, 4.3 PFLOP/s; 2003 gated rows, 8192 -> 14336: 234 us, 4.0; 2048 in bfloat16, 4096 -> 14336: 182 us, 1.32 (a
+// library product with bfloat16 weights of that shape: 173 us, of 8192 x 8192 x 8192 at most 1.62 PFLOP/s).
+// Copies that left parts out, when the first took 474 us: without loads 333, without reads from LDS 433, without
+// both 292; loads alone 287 of them (L2 to LDS at 14 TB/s), and 194 with all of them in L1.
 // Small tiles are bound by the way of a step's operands: 0.36 us a step of 64 x 64, with two steps to a barrier (0.5 with one).
 #include <type_traits>
 #include <utility>
