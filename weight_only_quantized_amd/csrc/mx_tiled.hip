@@ -14,8 +14,8 @@
 // What bounds the largest tiles (256 x 256, one workgroup a CU, 512 registers a lane): matrix cores are busy 55 % of
 // the time at the 1.8 GHz that the card keeps under this load, waves wait 16 % of it for loads or the barrier and 34 %
 // for their turn to issue, mostly behind a product (in 16 bits 58, 13 and 44; gated codes 47, 13 and 34).  4096 rows in codes,
-// 8192 -> 28672: 447 us, 4.3 PFLOP/s; 2003 gated rows, 8192 -> 14336: 234 us, 4.0; 2048 in bfloat16, 4096 -> 14336: 182 us, 1.32 (a
-// library product with bfloat16 weights of that shape: 173 us, of 8192 x 8192 x 8192 at most 1.62 PFLOP/s).
+// 8192 -> 28672: 447 us, 4.3 PFLOP/s; 2003 gated rows, 8192 -> 14336: 234 to 240 us, 4.0; 2048 in bfloat16, 4096 -> 14336: 182 to
+// 186 us, 1.3 (a library product with bfloat16 weights of that shape: 173 us, of 8192 x 8192 x 8192 at most 1.62 PFLOP/s).
 // Copies that left parts out, when the first took 474 us: without loads 333, without reads from LDS 433, without
 // both 292; loads alone 287 of them (L2 to LDS at 14 TB/s), and 194 with all of them in L1.
 // Small tiles are bound by the way of a step's operands: 0.36 us a step of 64 x 64, with two steps to a barrier (0.5 with one).
